@@ -1,5 +1,5 @@
-"""Thin ctypes binding of ``include/tm_w4a16.h`` and ``include/tm_w8a8.h``
-(argument marshalling only).
+"""Thin ctypes binding of ``include/tm_w4a16.h``, ``include/tm_w8a8.h`` and
+``include/tm_kvb.h`` (argument marshalling only).
 
 Every step of the computation runs in the CUDA library; PyTorch provides
 device memory and streams.  If the library is missing this module raises --
@@ -27,7 +27,8 @@ EXPORTS = ("tm_status_str", "tm_packed_bytes", "tm_pack_weights", "tm_unpack_wei
            "tm_w8_unpack", "tm_w8_packed_info", "tm_w8_packed_free", "tm_w8a8_gemm", "tm_w8a8_gemm_ex",
            "tm_w8_quantize_weight", "tm_kv_append", "tm_w4a16_gemm_host", "tm_w4a16_gemm_host_batch",
            "tm_w8a8_quantize_act_f16", "tm_w8a8_gemm_f16", "tm_w4a16_gemm_host_static",
-           "tm_w4a16_gemm_grouped", "tm_gemm_plan_grouped")
+           "tm_w4a16_gemm_grouped", "tm_gemm_plan_grouped", "tm_kvb_append", "tm_kvb_attention",
+           "tm_kvb_attention_workspace", "tm_kvb_evict")
 
 GROUP_MAX = 4  # TM_GROUP_MAX
 
@@ -36,6 +37,20 @@ class TMError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {_STATUS.get(status, status)} (status {status})")
         self.status = status
+
+
+class KVBCacheStruct(ctypes.Structure):
+    """``tm_kvb_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("format", ctypes.c_int)]
+
+
+class KVBBatchStruct(ctypes.Structure):
+    """``tm_kvb_batch``."""
+    _fields_ = [("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("table_stride", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("max_len", ctypes.c_int), ("rows", ctypes.c_longlong)]
 
 
 class GemmConfig(ctypes.Structure):
@@ -134,6 +149,15 @@ def load(path: Optional[str] = None):
     lib.tm_w4a16_gemm_grouped.argtypes = [ctypes.POINTER(GemmProblem), ci, ci, ctypes.POINTER(GemmConfig), vp]
     lib.tm_gemm_plan_grouped.argtypes = [ctypes.POINTER(GemmProblem), ci, ci, ctypes.POINTER(GemmConfig),
                                          ctypes.POINTER(GemmConfig), ctypes.POINTER(ci)]
+    pc, pb, ll = ctypes.POINTER(KVBCacheStruct), ctypes.POINTER(KVBBatchStruct), ctypes.c_longlong
+    lib.tm_kvb_append.restype = ci
+    lib.tm_kvb_append.argtypes = [pc, pb, vp, ll, vp, ll, ci, vp, ll, vp]
+    lib.tm_kvb_attention_workspace.restype = ci
+    lib.tm_kvb_attention_workspace.argtypes = [pc, pb, ci, ci, ctypes.POINTER(csz)]
+    lib.tm_kvb_attention.restype = ci
+    lib.tm_kvb_attention.argtypes = [pc, pb, vp, ll, ci, ci, ctypes.c_float, vp, vp, vp, vp, ll, vp, csz, vp]
+    lib.tm_kvb_evict.restype = ci
+    lib.tm_kvb_evict.argtypes = [pc, pb, vp, ci, vp, ll, vp, ll, ci, ci, ci, vp, vp, vp]
     _lib = lib
     return lib
 
@@ -709,3 +733,205 @@ def w8a8_gemm_f16(xq16: torch.Tensor, sx: torch.Tensor, w: W8Packed, out: Option
                                    _dev(out, torch.float16, "out"), M, split, tile_m, ctypes.c_void_p(st.cuda_stream)),
            "tm_w8a8_gemm_f16")
     return out
+
+
+# ---- paged 8-bit KV cache with a scale per page and head (include/tm_kvb.h) ----
+
+_KVB_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_KVB_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+class KVBlocks:
+    """The pages of one layer: codes ``k``, ``v`` [pages][Hkv][T][D] (int8 or
+    float8_e4m3fn: the dtype is the format) and scales ``ks``, ``vs`` fp32
+    [pages][Hkv], all contiguous on one device.  ``KVBlocks.empty`` allocates them."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor, vs: torch.Tensor):
+        if k.dim() != 4 or k.dtype not in _KVB_FORMATS:
+            raise ValueError("k must be int8 or float8_e4m3fn [pages][Hkv][T][D]")
+        if v.shape != k.shape:
+            raise ValueError("v must have the shape of k")
+        for t, name in ((ks, "ks"), (vs, "vs")):
+            if t.shape != k.shape[:2]:
+                raise ValueError(f"{name} must be fp32 [pages][Hkv]")
+        pages, Hkv, T, D = k.shape
+        if T not in (16, 32, 64, 128) or D not in (64, 128) or Hkv < 1:
+            raise ValueError("a page holds 16, 32, 64 or 128 tokens of Hkv >= 1 heads of 64 or 128 dimensions")
+        if not (k.device == v.device == ks.device == vs.device):
+            raise ValueError("k, v, ks and vs must be on one device")
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        self.pages, self.Hkv, self.T, self.D = pages, Hkv, T, D
+        self.device = k.device
+        self._c = KVBCacheStruct(_dev(k, k.dtype, "k"), _dev(v, k.dtype, "v"), _dev(ks, torch.float32, "ks"),
+                           _dev(vs, torch.float32, "vs"), pages, Hkv, T, D, _KVB_FORMATS[k.dtype])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, T: int, D: int, dtype=torch.int8, device="cuda") -> "KVBlocks":
+        """Pages of zeros."""
+        codes = lambda: torch.zeros((pages, Hkv, T, D), dtype=torch.uint8, device=device).view(dtype)  # noqa: E731
+        scales = lambda: torch.zeros((pages, Hkv), dtype=torch.float32, device=device)  # noqa: E731
+        return cls(codes(), codes(), scales(), scales())
+
+
+class KVBatch:
+    """The sequences of one step, shared by every layer's calls.
+
+    table:   int32 [B][n], row-contiguous: the page of each block of T tokens
+             (entries that name no page are holes)
+    kv_len:  int32 [B], the tokens of each sequence, this step's included
+    q_start: int32 [B + 1], where each sequence's rows begin in Q, K and V;
+             None: one row each
+    max_q, max_len: bounds of a sequence's rows and tokens that the host knows
+             (max_len 0: the room of the table)
+
+    The tensors are kept and read on the device at each call: a program advances
+    kv_len, and fills in table entries, in place."""
+
+    def __init__(self, table: torch.Tensor, kv_len: torch.Tensor, q_start: Optional[torch.Tensor] = None,
+                 max_q: int = 1, max_len: int = 0):
+        if table.dim() != 2 or kv_len.shape != table.shape[:1]:
+            raise ValueError("table must be int32 [B][n] and kv_len int32 [B]")
+        if q_start is not None and q_start.shape != (table.shape[0] + 1,):
+            raise ValueError("q_start must be int32 [B + 1]")
+        if max_q < 1 or max_len < 0:
+            raise ValueError("max_q must be at least 1 and max_len at least 0")
+        self.table, self.kv_len, self.q_start = table, kv_len, q_start
+        self.B, self.max_q, self.max_len = table.shape[0], max_q, max_len
+        self.device = table.device
+        self._c = KVBBatchStruct(_dev(table, torch.int32, "table"), _dev(kv_len, torch.int32, "kv_len"),
+                           None if q_start is None else _dev(q_start, torch.int32, "q_start"), table.shape[0],
+                           table.shape[1], max_q, max_len, table.shape[0])
+        self._ref = ctypes.byref(self._c)
+
+    def _rows(self, rows: int):
+        if self.q_start is None and rows != self.B:
+            raise ValueError("without q_start there is one row per sequence")
+        self._c.rows = rows
+        return self._ref
+
+
+def _kvb_rows(t: torch.Tensor, heads, D: int, name: str):
+    """Device pointer and token stride of [rows][heads][D] whose heads lie together."""
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][heads][{D}]")
+    if t.dtype not in _KVB_DTYPES:
+        raise ValueError(f"{name} must be fp16 or bf16")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}'s heads must be contiguous (its rows may have a stride)")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _kvb_weights(t: Optional[torch.Tensor], B: int, Hkv: int, name: str):
+    if t is None:
+        return None, 0
+    if t.dim() != 3 or t.shape[:2] != (B, Hkv):
+        raise ValueError(f"{name} must be fp32 [B][Hkv][tokens]")
+    return _dev(t, torch.float32, name), t.shape[2]
+
+
+def _kvb_stream(device, stream, *made):
+    """The call's stream; what the call allocated is kept for it."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def kvb_append(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.Tensor, w: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise the step's keys and values, fp16 or bf16 [rows][Hkv][D] (rows may
+    be strided), into the pages of the last tokens of each sequence
+    (tm_kvb_append).  w: token weights fp32 [B][Hkv][tokens], set to 0 for the
+    new tokens."""
+    kp, ks = _kvb_rows(K, cache.Hkv, cache.D, "K")
+    vp, vs = _kvb_rows(V, cache.Hkv, cache.D, "V")
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("V must have the shape and dtype of K")
+    wp, wn = _kvb_weights(w, batch.B, cache.Hkv, "w")
+    _check(load().tm_kvb_append(cache._ref, batch._rows(K.shape[0]), kp, ks, vp, vs, _KVB_DTYPES[K.dtype], wp, wn,
+                                _kvb_stream(cache.device, stream)), "tm_kvb_append")
+
+
+def kvb_attention_workspace(cache: KVBlocks, batch: KVBatch, Hq: int, rows: int, weights: bool = False) -> int:
+    """Bytes of workspace that kvb_attention needs (tm_kvb_attention_workspace)."""
+    n = ctypes.c_size_t()
+    _check(load().tm_kvb_attention_workspace(cache._ref, batch._rows(rows), Hq, 1 if weights else 0, ctypes.byref(n)),
+           "tm_kvb_attention_workspace")
+    return n.value
+
+
+def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, w_in: Optional[torch.Tensor] = None,
+                  w_out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of the step's queries, fp16 or bf16 [rows][Hq][D] (rows may
+    be strided), over the cache (tm_kvb_attention); append the step's keys and
+    values first.  Returns out [rows][Hq][D].
+
+    lse:   fp32 [rows][Hq], receives the logarithm of each row's softmax sum
+    w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
+           token drew in this call; may be w_in
+    workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
+    qp, qs = _kvb_rows(Q, None, cache.D, "Q")
+    rows, Hq = Q.shape[:2]
+    made_out = made_ws = None
+    if out is None:
+        out = made_out = torch.empty((rows, Hq, cache.D), dtype=Q.dtype, device=Q.device)
+    elif out.shape != Q.shape:
+        raise ValueError("out must have the shape of Q")
+    if lse is not None and lse.shape != (rows, Hq):
+        raise ValueError("lse must be fp32 [rows][Hq]")
+    wi, ni = _kvb_weights(w_in, batch.B, cache.Hkv, "w_in")
+    wo, no = _kvb_weights(w_out, batch.B, cache.Hkv, "w_out")
+    if wi is not None and (wo is None or ni != no):
+        raise ValueError("w_in comes with a w_out of its shape")
+    ref = batch._rows(rows)
+    lib = load()
+    if workspace is None:
+        size = kvb_attention_workspace(cache, batch, Hq, rows, wo is not None)
+        if size:
+            workspace = made_ws = torch.empty(size, dtype=torch.uint8, device=Q.device)
+    st = lib.tm_kvb_attention(cache._ref, ref, qp, qs, Hq, _KVB_DTYPES[Q.dtype], 0.0 if scale is None else scale,
+                              _dev(out, Q.dtype, "out"), None if lse is None else _dev(lse, torch.float32, "lse"),
+                              wi, wo, no, None if workspace is None else _dev(workspace, torch.uint8, "workspace"),
+                              0 if workspace is None else workspace.numel(),
+                              _kvb_stream(cache.device, stream, made_out, made_ws))
+    _check(st, "tm_kvb_attention")
+    return out
+
+
+def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, first: int = 0, recent: int = 0,
+              dst_table: Optional[torch.Tensor] = None, w_out: Optional[torch.Tensor] = None,
+              kept: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None):
+    """Cut every sequence to ``budget`` tokens per KV head (tm_kvb_evict): the first
+    ``first``, the last ``recent`` and the heaviest of the rest by w, fp32
+    [B][Hkv][tokens].  dst_table int32 [B][n]: the pages that take them (None: in
+    place).  w_out: their weights, fp32 [B][Hkv][>= budget] (None: into w).
+    Returns (kept int32 [B][Hkv][budget], new_len int32 [B]); batch.kv_len is
+    left as it is."""
+    wp, wn = _kvb_weights(w, batch.B, cache.Hkv, "w")
+    op, on = (wp, wn) if w_out is None else _kvb_weights(w_out, batch.B, cache.Hkv, "w_out")
+    made = []
+    if kept is None:
+        kept = torch.empty((batch.B, cache.Hkv, max(budget, 0)), dtype=torch.int32, device=w.device)
+        made.append(kept)
+    elif kept.shape != (batch.B, cache.Hkv, budget):
+        raise ValueError("kept must be int32 [B][Hkv][budget]")
+    if new_len is None:
+        new_len = torch.empty(batch.B, dtype=torch.int32, device=w.device)
+        made.append(new_len)
+    elif new_len.shape != (batch.B,):
+        raise ValueError("new_len must be int32 [B]")
+    dst = batch.table if dst_table is None else dst_table
+    if dst.dim() != 2 or dst.shape[0] != batch.B:
+        raise ValueError("dst_table must be int32 [B][n]")
+    st = load().tm_kvb_evict(cache._ref, batch._ref, _dev(dst, torch.int32, "dst_table"), dst.shape[1], wp, wn, op, on,
+                             budget, first, recent, _dev(kept, torch.int32, "kept"),
+                             _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache.device, stream, *made))
+    _check(st, "tm_kvb_evict")
+    return kept, new_len

@@ -1,0 +1,162 @@
+// Append to the paged 8-bit KV cache: new keys and values quantised into their
+// pages, one scale per page and head.
+//
+// One CTA per (page that new tokens fall into, head, K or V): the new values
+// are read once and stay in registers (at most T D = 16384 of them, 64 per
+// thread) across the maximum and the rounding.  A page that already holds
+// tokens keeps the larger of its scale and the one that the new tokens need;
+// where it grows, the earlier codes are rounded anew (each page sees that a few
+// times while it fills: the maximum of a growing set rises ever more rarely).
+#include "kvb_common.cuh"
+
+namespace w4 {
+namespace kvb {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendVecs = 8;  // vectors of 8 values per thread: 256 x 8 x 8 = 128 tokens x 128
+
+struct AppendParams {
+  View V;
+  const uint16_t* x[2];  // keys, values
+  long long stride[2];   // elements per token
+  int d_shift;           // log2 D
+  int bf16;
+  float* w;
+  long long w_stride;
+};
+
+// NaN to 0, infinities to the type's largest finite value.
+__device__ __forceinline__ float finite(float x, float top) {
+  return x != x ? 0.f : fminf(fmaxf(x, -top), top);
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
+  __shared__ float warp_max[kAppendThreads / 32];
+  const View& V = P.V;
+  const int b = blockIdx.z, h = blockIdx.y, sel = blockIdx.x & 1, tid = threadIdx.x;
+  const Span s = span(V, b);
+  const int T = 1 << V.t_shift;
+  const int first = max(s.old, 0);
+  const int blk = (first >> V.t_shift) + (int)(blockIdx.x >> 1);
+  const int begin = blk << V.t_shift;
+  if (blk >= V.table_stride) return;
+  const int lo = max(first, begin), hi = min(s.old + s.n, begin + T);
+  if (lo >= hi) return;
+  if (sel == 0 && P.w)
+    for (int t = lo + tid; t < hi && t < P.w_stride; t += kAppendThreads)
+      P.w[((size_t)b * V.Hkv + h) * P.w_stride + t] = 0.f;
+  const int page = page_of(V, V.table, b, V.table_stride, blk);
+  if (page < 0) return;
+
+  const int vec_shift = P.d_shift - 3;  // vectors of 8 values per token
+  const int total = (hi - lo) << vec_shift;
+  const uint16_t* src = P.x[sel] + (s.row0 + (long long)(lo - s.old)) * P.stride[sel] + ((long long)h << P.d_shift);
+  const float top = P.bf16 ? 3.3895313892515355e38f : 65504.f;
+  uint4 x[kAppendVecs];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAppendVecs; ++i) {
+    const int v = tid + i * kAppendThreads;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (v < total)
+      x[i] = *reinterpret_cast<const uint4*>(src + (v >> vec_shift) * P.stride[sel] +
+                                             ((v & ((1 << vec_shift) - 1)) << 3));
+  }
+#pragma unroll
+  for (int i = 0; i < kAppendVecs; ++i) {
+    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack(wd[k], P.bf16);
+      a = fmaxf(a, fmaxf(fabsf(finite(f.x, top)), fabsf(finite(f.y, top))));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if ((tid & 31) == 0) warp_max[tid >> 5] = a;
+  const size_t cell = (size_t)page * V.Hkv + h;
+  float* scale = (sel ? V.vs : V.ks) + cell;
+  const bool continued = s.old > begin;
+  const float was = continued ? *scale : 0.f;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) a = fmaxf(a, warp_max[i]);
+  const float now = fmaxf(fmaxf(__fdiv_rn(a, qmax<FMT>()), kScaleFloor), was);
+  if (tid == 0) *scale = now;
+
+  uint8_t* codes = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);
+  uint8_t* dst = codes + ((size_t)(lo - begin) << P.d_shift);
+#pragma unroll
+  for (int i = 0; i < kAppendVecs; ++i) {
+    const int v = tid + i * kAppendThreads;
+    if (v >= total) break;
+    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t c[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack(wd[k], P.bf16);
+      c[k >> 1] |= (encode<FMT>(__fdiv_rn(finite(f.x, top), now)) |
+                    encode<FMT>(__fdiv_rn(finite(f.y, top), now)) << 8)
+                   << (16 * (k & 1));
+    }
+    *reinterpret_cast<uint2*>(dst + ((size_t)v << 3)) = make_uint2(c[0], c[1]);
+  }
+  if (continued && now > was) {
+    const int earlier = (lo - begin) << vec_shift;
+    for (int v = tid; v < earlier; v += kAppendThreads) {
+      uint2* at = reinterpret_cast<uint2*>(codes + ((size_t)v << 3));
+      const uint2 c = *at;
+      uint32_t wd[2] = {c.x, c.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t r = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          r |= encode<FMT>(__fdiv_rn(__fmul_rn(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu), was), now)) << (8 * e);
+        wd[k] = r;
+      }
+      *at = make_uint2(wd[0], wd[1]);
+    }
+  }
+}
+
+}  // namespace kvb
+}  // namespace w4
+
+using namespace w4;
+using namespace w4::kvb;
+
+extern "C" tm_status tm_kvb_append(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Kn,
+                                   long long k_stride, const void* Vn, long long v_stride, int dtype, float* w,
+                                   long long w_stride, void* stream) {
+  AppendParams P;
+  const tm_status st = check(cache, batch, true, &P.V);
+  if (st != TM_OK) return st;
+  if (dtype != TM_KVB_F16 && dtype != TM_KVB_BF16) return TM_ERR_INVALID_ARG;
+  if (!batch->q_start && (batch->rows != batch->B || (batch->B > 0 && batch->max_q < 1))) return TM_ERR_INVALID_ARG;
+  const View& V = P.V;
+  if (V.B == 0 || V.rows == 0 || V.max_q == 0 || V.table_stride == 0) return TM_OK;
+  const long long width = (long long)cache->Hkv * cache->D;
+  if (!Kn || !Vn || k_stride < width || v_stride < width || w_stride < 0) return TM_ERR_INVALID_ARG;
+  if (!aligned(Kn, 16) || !aligned(Vn, 16) || k_stride % 8 || v_stride % 8 || !aligned(w, 4)) return TM_ERR_ALIGNMENT;
+  P.x[0] = static_cast<const uint16_t*>(Kn);
+  P.x[1] = static_cast<const uint16_t*>(Vn);
+  P.stride[0] = k_stride;
+  P.stride[1] = v_stride;
+  P.d_shift = cache->D == 64 ? 6 : 7;
+  P.bf16 = dtype == TM_KVB_BF16;
+  P.w = w;
+  P.w_stride = w_stride;
+  // Pages that max_q consecutive tokens can touch.
+  const long long pages = ((long long)V.max_q + cache->T - 2) / cache->T + 1;
+  const dim3 grid((unsigned)(2 * pages), (unsigned)V.Hkv, (unsigned)V.B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->format == TM_KVB_INT8)
+    append_kernel<TM_KVB_INT8><<<grid, kAppendThreads, 0, s>>>(P);
+  else
+    append_kernel<TM_KVB_E4M3><<<grid, kAppendThreads, 0, s>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return TM_ERR_CUDA;
+  set_launch_count(1);
+  return TM_OK;
+}

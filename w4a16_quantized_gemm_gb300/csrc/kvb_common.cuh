@@ -1,0 +1,169 @@
+// Shared pieces of the paged 8-bit KV cache (one scale per page and head):
+// argument checks, the codes' conversions and asynchronous copies.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "../../include/tm_kvb.h"
+#include "tm_common.cuh"
+
+namespace w4 {
+namespace kvb {
+
+constexpr float kScaleFloor = 9.31322574615478515625e-10f;  // 2^-30
+
+// What a kernel needs of a cache and a batch.
+struct View {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  const int* table;
+  const int* kv_len;
+  const int* q_start;
+  int pages, Hkv, t_shift;  // T = 1 << t_shift
+  int B, table_stride, max_q, max_len;
+  int rows;
+};
+
+inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Host checks that every call shares; fills `view`.  `pointers`: the device
+// fields are checked too.
+inline tm_status check(const tm_kvb_cache* c, const tm_kvb_batch* b, bool pointers, View* view) {
+  if (!c || !b) return TM_ERR_INVALID_ARG;
+  if (c->pages < 0 || c->Hkv < 1 || c->Hkv > 65535 || (c->T != 16 && c->T != 32 && c->T != 64 && c->T != 128) ||
+      (c->D != 64 && c->D != 128) || (c->format != TM_KVB_INT8 && c->format != TM_KVB_E4M3))
+    return TM_ERR_INVALID_ARG;
+  if (b->B < 0 || b->B > 65535 || b->table_stride < 0 || b->max_q < 0 || b->max_len < 0 || b->rows < 0)
+    return TM_ERR_INVALID_ARG;
+  // Row and token indices are 32-bit in the kernels; products with sizes are 64-bit.
+  const long long room = (long long)b->table_stride * c->T;
+  if (room > 0x7fffff00ll || b->rows > 0x7fffff00ll) return TM_ERR_UNSUPPORTED;
+  if (b->B > 0 && pointers) {
+    if (!c->k || !c->v || !c->ks || !c->vs || !b->table || !b->kv_len) return TM_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->ks, 4) || !aligned(c->vs, 4) ||
+        !aligned(b->table, 4) || !aligned(b->kv_len, 4) || !aligned(b->q_start, 4))
+      return TM_ERR_ALIGNMENT;
+  }
+  int shift = 4;
+  while ((1 << shift) < c->T) ++shift;
+  long long len = b->max_len > 0 ? b->max_len : room;
+  if (len > room) len = room;
+  *view = {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->ks, c->vs, b->table, b->kv_len, b->q_start,
+           c->pages, c->Hkv, shift, b->B, b->table_stride, b->max_q, (int)len, (int)b->rows};
+  return TM_OK;
+}
+
+#if defined(__CUDACC__)
+
+// Sequence b: its tokens, those that the call may read, its first row, the
+// rows that the call computes, and the position of the first of them.
+struct Span {
+  int raw, len, row0, n, old;
+};
+__device__ __forceinline__ Span span(const View& V, int b) {
+  Span s;
+  s.raw = max(V.kv_len[b], 0);
+  s.len = min(s.raw, V.max_len);
+  const int lo = V.q_start ? min(max(V.q_start[b], 0), V.rows) : b;
+  const int hi = V.q_start ? min(max(V.q_start[b + 1], 0), V.rows) : b + 1;
+  s.row0 = lo;
+  s.old = s.raw - max(hi - lo, 0);
+  s.n = min(max(hi - lo, 0), V.max_q);
+  return s;
+}
+// The page of block `blk`, or -1 for a hole.
+__device__ __forceinline__ int page_of(const View& V, const int* table, int b, int stride, int blk) {
+  const int p = table[(size_t)b * stride + blk];
+  return (unsigned)p < (unsigned)V.pages ? p : -1;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+// Two e4m3 codes (low and high byte of a 16-bit word) as fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+
+// Four codes of a word as fp16 pairs (bytes 0, 1) and (2, 3), exactly.  int8:
+// the byte with its sign bit flipped is b + 128; OR-ed into the mantissa of
+// 1024.0 it gives 1152 + b.
+template <int FMT>
+__device__ __forceinline__ void codes_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == TM_KVB_INT8) {
+    const uint32_t x = w ^ 0x80808080u;
+    lo = hsub2_u32(prmt(x, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = hsub2_u32(prmt(x, 0x64646464u, 0x4342u), 0x64806480u);
+  } else {
+    lo = e4m3x2_half2((uint16_t)w);
+    hi = e4m3x2_half2((uint16_t)(w >> 16));
+  }
+}
+
+// Codes of two words as four fp16 pairs (byte i of a, byte i of b).
+template <int FMT>
+__device__ __forceinline__ void codes_half_pairs(uint32_t a, uint32_t b, uint32_t (&out)[4]) {
+  codes_half<FMT>(prmt(a, b, 0x5140u), out[0], out[1]);
+  codes_half<FMT>(prmt(a, b, 0x7362u), out[2], out[3]);
+}
+
+// Code of y: to nearest, ties to even, saturating.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode(float y) {
+  if (FMT == TM_KVB_INT8) return (uint32_t)(int)fminf(fmaxf(rintf(y), -127.f), 127.f) & 0xFFu;
+  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+template <int FMT>
+__device__ __forceinline__ float decode(uint32_t c) {
+  if (FMT == TM_KVB_INT8) return (float)(int)(int8_t)c;
+  const uint32_t h = e4m3x2_half2((uint16_t)c);
+  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+}
+template <int FMT>
+__device__ __forceinline__ float qmax() {
+  return FMT == TM_KVB_INT8 ? 127.f : 448.f;
+}
+
+// 16-byte asynchronous copy global -> shared; zeros where !ok.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+#endif  // __CUDACC__
+
+}  // namespace kvb
+}  // namespace w4

@@ -1,0 +1,334 @@
+// Eviction from the paged 8-bit KV cache by accumulated attention weight.
+//
+// One thread-block cluster per (sequence, KV head).  Selection: a radix select
+// of the count-th largest key over the head's weights, 8 bits a round, the
+// histograms summed over the cluster through distributed shared memory; then
+// each kept token's new slot is its rank among the kept ones, from counts of
+// the tokens before it (no atomics on positions, so ties fall to the lowest
+// index).  Move: a warp takes one (new page, K or V), gathers its tokens' codes
+// into shared memory, finds the maximum, rounds them to the new scale, and
+// writes them after a cluster barrier.
+//
+// In place: kept tokens move to lower slots in their order, so a new page reads
+// only from pages at or after itself.  Pages go in waves of increasing index;
+// within a wave every read comes before the barrier and every write after it,
+// and no later wave reads what an earlier one wrote.  No workspace, one launch.
+#include "kvb_common.cuh"
+
+namespace w4 {
+namespace kvb {
+
+constexpr int kEvictThreads = 256;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kKeyCap = 16384;  // keys of a CTA's slice held in shared memory (64 KB); the rest are read again
+
+struct EvictParams {
+  View V;
+  const int* dst_table;
+  int dst_stride;
+  const float* w;
+  long long w_stride;
+  float* w_out;
+  long long w_out_stride;
+  int budget, first, recent;
+  int* kept;
+  int* new_len;
+  int d_shift;
+};
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(addr, rank)) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();  // the barrier's aligned form wants whole warps
+  cluster_sync_all();
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams P) {
+  extern __shared__ __align__(16) uint8_t smem[];  // keys, then the warps' tokens
+  __shared__ uint32_t hist[256], total[256];
+  __shared__ uint32_t warp_gt[kEvictWarps], warp_eq[kEvictWarps], cta_count[2];
+  __shared__ uint32_t found[2];
+  __shared__ float row_scale[kEvictWarps][128];
+  const View& V = P.V;
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int C = gridDim.x;
+  const int T = 1 << V.t_shift, D = 1 << P.d_shift;
+  const int L = min(max(V.kv_len[b], 0), V.max_len);
+  const int count = min(L, P.budget);
+  const size_t head = (size_t)b * V.Hkv + h;
+  const float* w = P.w + head * P.w_stride;
+  int* kept = P.kept + head * P.budget;
+
+  if (L > count) {
+    // ---------------- selection ----------------
+    const int per = ((L + C - 1) / C + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+    const int s0 = min(L, (int)rank * per), s1 = min(L, s0 + per);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+    auto key_of = [&](int j) -> uint32_t {
+      if (j < P.first || j >= L - P.recent) return 0xFFFFFFFFu;
+      if (page_of(V, V.table, b, V.table_stride, j >> V.t_shift) < 0) return 0u;
+      const float x = w[j] + 0.f;  // -0 counts as 0
+      if (x != x) return 0u;
+      const uint32_t u = __float_as_uint(x);
+      return (u >> 31) ? ~u : (u | 0x80000000u);
+    };
+    for (int j = s0 + tid; j < s1 && j - s0 < kKeyCap; j += kEvictThreads) keys[j - s0] = key_of(j);
+    auto key = [&](int j) { return j - s0 < kKeyCap ? keys[j - s0] : key_of(j); };
+    uint32_t prefix = 0u, mask = 0u, want = (uint32_t)count;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      hist[tid] = 0u;
+      __syncthreads();
+      for (int j = s0 + tid; j < s1; j += kEvictThreads) {
+        const uint32_t k = key(j);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      }
+      cluster_barrier();
+      uint32_t sum = 0u;
+      for (int r = 0; r < C; ++r) sum += ld_cluster(smem_u32(&hist[tid]), r);
+      total[tid] = sum;
+      cluster_barrier();
+      if (warp == 0) {
+        // lane l holds bins 255 - 8 l .. 248 - 8 l: from the largest keys down
+        uint32_t mine = 0u;
+        for (int i = 0; i < 8; ++i) mine += total[255 - 8 * lane - i];
+        uint32_t upto = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        uint32_t above = upto - mine;
+        if (above < want && want <= upto) {
+          int bin = 255 - 8 * lane;
+          while (above + total[bin] < want) above += total[bin--];
+          found[0] = (uint32_t)bin;
+          found[1] = want - above;
+        }
+      }
+      __syncthreads();
+      prefix |= found[0] << shift;
+      mask |= 255u << shift;
+      want = found[1];
+      __syncthreads();
+    }
+    // The kept: every key above `prefix`, and the first `want` equal to it.
+    const int sub = per / kEvictWarps;
+    const int w0 = min(s1, s0 + warp * sub), w1 = min(s1, w0 + sub);
+    const uint32_t before = (1u << lane) - 1u;
+    uint32_t gt = 0u, eq = 0u;
+    for (int j = w0; j < w1; j += 32) {
+      const uint32_t k = j + lane < w1 ? key(j + lane) : 0u;
+      gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > prefix));
+      eq += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k == prefix));
+    }
+    if (lane == 0) {
+      warp_gt[warp] = gt;
+      warp_eq[warp] = eq;
+    }
+    __syncthreads();
+    if (tid < 2) {
+      uint32_t v = 0u;
+      for (int i = 0; i < kEvictWarps; ++i) v += tid ? warp_eq[i] : warp_gt[i];
+      cta_count[tid] = v;
+    }
+    cluster_barrier();
+    gt = eq = 0u;
+    for (uint32_t r = 0; r < rank; ++r) {
+      gt += ld_cluster(smem_u32(&cta_count[0]), r);
+      eq += ld_cluster(smem_u32(&cta_count[1]), r);
+    }
+    for (int i = 0; i < warp; ++i) {
+      gt += warp_gt[i];
+      eq += warp_eq[i];
+    }
+    for (int j = w0; j < w1; j += 32) {
+      const bool in = j + lane < w1;
+      const uint32_t k = in ? key(j + lane) : 0u;
+      const uint32_t mg = __ballot_sync(0xffffffffu, in && k > prefix);
+      const uint32_t me = __ballot_sync(0xffffffffu, in && k == prefix);
+      const uint32_t g = gt + __popc(mg & before), e = eq + __popc(me & before);
+      if (in && k > prefix) kept[g + min(e, want)] = j + lane;
+      if (in && k == prefix && e < want) kept[g + e] = j + lane;
+      gt += __popc(mg);
+      eq += __popc(me);
+    }
+  } else {
+    for (int j = (int)rank * kEvictThreads + tid; j < L; j += C * kEvictThreads) kept[j] = j;
+  }
+  for (int j = count + (int)rank * kEvictThreads + tid; j < P.budget; j += C * kEvictThreads) kept[j] = -1;
+  if (rank == 0 && h == 0 && tid == 0) P.new_len[b] = count;
+  cluster_barrier();
+
+  // ---------------- move ----------------
+  const int chunk_shift = P.d_shift - 4;  // 16-byte chunks per token
+  const int chunks = T << chunk_shift;
+  uint8_t* stage = smem + ((size_t)(warp << V.t_shift) << P.d_shift);
+  const uint32_t stage_u = smem_u32(stage);
+  float* rs = row_scale[warp];
+  const int units = 2 * ((count + T - 1) >> V.t_shift);
+  for (int u0 = 0; u0 < units; u0 += C * kEvictWarps) {
+    const int u = u0 + (int)rank * kEvictWarps + warp;
+    const int blk = u >> 1, sel = u & 1;
+    const int base = blk << V.t_shift;
+    bool same = false;
+    int from = -1, to = -1;
+    float now = kScaleFloor;
+    float kw[4];
+    if (u < units) {
+      const int last = min(count, base + T) - 1;
+      same = kept[last] == last;
+      from = page_of(V, V.table, b, V.table_stride, min(blk, V.table_stride - 1));
+      to = page_of(V, P.dst_table, b, P.dst_stride, blk);
+      uint8_t* pool = sel ? V.v : V.k;
+      const float* scales = sel ? V.vs : V.ks;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = lane + 32 * i;
+        if (t < T) {
+          const int pos = base + t;
+          const int j = pos < count ? kept[pos] : -1;
+          const int page = j >= 0 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+          rs[t] = page >= 0 ? scales[(size_t)page * V.Hkv + h] : 0.f;
+          kw[i] = j >= 0 ? w[j] : 0.f;
+        }
+      }
+      for (int c = lane; c < chunks; c += 32) {
+        const int pos = base + (c >> chunk_shift);
+        const int j = pos < count ? kept[pos] : -1;
+        const int page = j >= 0 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+        const uint8_t* src = pool;
+        if (page >= 0)
+          src += ((((size_t)page * V.Hkv + h) << V.t_shift) + (j & (T - 1))) * D +
+                 ((c & ((1 << chunk_shift) - 1)) << 4);
+        cp16(stage_u + 16 * c, src, page >= 0);
+      }
+      cp_commit();
+      cp_wait<0>();
+      __syncwarp();
+      if (same) {
+        if (from >= 0) now = scales[(size_t)from * V.Hkv + h];
+      } else {
+        float a = 0.f;
+        for (int c = lane; c < chunks; c += 32) {
+          const uint4 q = *reinterpret_cast<const uint4*>(stage + 16 * c);
+          const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+          float m = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu)));
+          a = fmaxf(a, __fmul_rn(m, rs[c >> chunk_shift]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        now = fmaxf(__fdiv_rn(a, qmax<FMT>()), kScaleFloor);
+        for (int c = lane; c < chunks; c += 32) {
+          uint4* at = reinterpret_cast<uint4*>(stage + 16 * c);
+          const uint4 q = *at;
+          uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+          const float s = rs[c >> chunk_shift];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              r |= encode<FMT>(__fdiv_rn(__fmul_rn(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu), s), now)) << (8 * e);
+            wd[k] = r;
+          }
+          *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+        }
+      }
+      __syncwarp();
+    }
+    cluster_barrier();
+    if (u < units) {
+      if (sel == 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int pos = base + lane + 32 * i;
+          if (lane + 32 * i < T && pos < count) P.w_out[head * P.w_out_stride + pos] = kw[i];
+        }
+      if (to >= 0 && !(same && to == from)) {
+        const size_t cell = (size_t)to * V.Hkv + h;
+        uint8_t* dst = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);
+        for (int c = lane; c < chunks; c += 32)
+          *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(stage + 16 * c);
+        if (lane == 0) (sel ? V.vs : V.ks)[cell] = now;
+      }
+      __syncwarp();
+    }
+  }
+  for (int j = count + (int)rank * kEvictThreads + tid; j < P.budget; j += C * kEvictThreads)
+    P.w_out[head * P.w_out_stride + j] = 0.f;
+  // No CTA leaves while another may still read its shared memory.
+  cluster_barrier();
+}
+
+template <int FMT>
+tm_status launch_evict(const EvictParams& P, cudaStream_t stream) {
+  const View& V = P.V;
+  const size_t stage = ((size_t)kEvictWarps << V.t_shift) << P.d_shift;
+  const size_t smem = stage > kKeyCap * 4 ? stage : (size_t)kKeyCap * 4;
+  static std::atomic<unsigned long long> done{0};
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), 8 * 128 * 128)) return TM_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  const unsigned C = 8;
+  cfg.gridDim = dim3(C, (unsigned)V.Hkv, (unsigned)V.B);
+  cfg.blockDim = dim3(kEvictThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<FMT>, P) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+}  // namespace kvb
+}  // namespace w4
+
+using namespace w4;
+using namespace w4::kvb;
+
+extern "C" tm_status tm_kvb_evict(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const int* dst_table,
+                                  int dst_stride, const float* w, long long w_stride, float* w_out,
+                                  long long w_out_stride, int budget, int first, int recent, int* kept, int* new_len,
+                                  void* stream) {
+  EvictParams P;
+  const tm_status st = check(cache, batch, true, &P.V);
+  if (st != TM_OK) return st;
+  const View& V = P.V;
+  if (budget < 1 || first < 0 || recent < 0 || (long long)first + recent > budget) return TM_ERR_INVALID_ARG;
+  if (V.B == 0) return TM_OK;
+  if (!dst_table || !w || !w_out || !kept || !new_len || new_len == V.kv_len) return TM_ERR_INVALID_ARG;
+  if ((long long)dst_stride * cache->T < budget || w_stride < V.max_len || w_out_stride < budget)
+    return TM_ERR_INVALID_ARG;
+  if (w == w_out && w_stride != w_out_stride) return TM_ERR_INVALID_ARG;
+  if (!aligned(dst_table, 4) || !aligned(w, 4) || !aligned(w_out, 4) || !aligned(kept, 4) || !aligned(new_len, 4))
+    return TM_ERR_ALIGNMENT;
+  P.dst_table = dst_table;
+  P.dst_stride = dst_stride;
+  P.w = w;
+  P.w_stride = w_stride;
+  P.w_out = w_out;
+  P.w_out_stride = w_out_stride;
+  P.budget = budget;
+  P.first = first;
+  P.recent = recent;
+  P.kept = kept;
+  P.new_len = new_len;
+  P.d_shift = cache->D == 64 ? 6 : 7;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const tm_status r =
+      cache->format == TM_KVB_INT8 ? launch_evict<TM_KVB_INT8>(P, s) : launch_evict<TM_KVB_E4M3>(P, s);
+  if (r == TM_OK) set_launch_count(1);
+  return r;
+}
