@@ -64,7 +64,7 @@ typedef struct {
  * round-to-nearest-even at each step:
  *   a = max |x| over the new tokens in the page (NaN counts as 0, an infinity
  *       as the type's largest finite value)
- *   need = max(a / Qmax, 2^-30),  Qmax = 127 (int8) or 448 (e4m3)
+ *   need = max(a * r, 2^-30),  r = 1 / 127 (int8) or 1 / 448 (e4m3), rounded once
  *   s = max(s_old, need) if the page holds earlier tokens of the sequence,
  *       else need
  *   new codes = Q(x / s); where s > s_old the page's earlier codes become
@@ -119,7 +119,7 @@ tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
  * lowest index; NaN and holes go first).  A sequence of at most `budget`
  * tokens keeps all of them.  Each head keeps its own tokens; they move, in
  * their order, to slots 0, 1, ... of the pages of dst_table:
- *   s = max(max |c * s_old| / Qmax, 2^-30) over a new page's tokens,
+ *   s = max(max |c * s_old| * r, 2^-30) over a new page's tokens, r as in the append,
  *   codes Q((c * s_old) / s); its slots past the last token become 0.
  *   A page whose tokens all keep their slots keeps its codes and its scale.
  *   dst_table: device int32 [B][dst_stride], dst_stride >= ceil(budget / T).

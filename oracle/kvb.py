@@ -12,6 +12,7 @@ import numpy as np
 
 FLOOR = np.float32(2.0 ** -30)
 QMAX = {"int8": np.float32(127), "e4m3": np.float32(448)}
+STEP = {f: np.float32(1) / q for f, q in QMAX.items()}  # a scale is the maximum times this
 
 
 def _e4m3_values() -> np.ndarray:
@@ -65,7 +66,7 @@ def append(codes, scales, table, kv_len, q_start, x, fmt, top=65504.0):
             lo, hi = max(old, blk * T, 0), min(length, (blk + 1) * T)
             for h in range(Hkv):
                 new = x[q_start[b] + lo - old:q_start[b] + hi - old, h]
-                s = max(np.float32(np.abs(new).max() / QMAX[fmt]), FLOOR)
+                s = max(np.float32(np.abs(new).max() * STEP[fmt]), FLOOR)
                 if old > blk * T:
                     was = scales[page, h]
                     if s > was:
@@ -161,6 +162,6 @@ def evict(pools, table, dst_table, kv_len, w, budget, first, recent, fmt):
                             codes[to, h], scales[to, h] = c, old_s[p, h] if there else FLOOR
                         continue
                     x = decode(c, fmt).astype(np.float32) * s[:, None]
-                    now = max(np.float32(np.abs(x).max() / QMAX[fmt]), FLOOR)
+                    now = max(np.float32(np.abs(x).max() * STEP[fmt]), FLOOR)
                     codes[to, h], scales[to, h] = encode(x / now, fmt), now
     return kept, new_len, w_out

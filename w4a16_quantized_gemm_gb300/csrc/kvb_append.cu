@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kAppendThreads / 32; ++i) a = fmaxf(a, warp_max[i]);
-  const float now = fmaxf(fmaxf(__fdiv_rn(a, qmax<FMT>()), kScaleFloor), was);
+  const float now = fmaxf(scale_for<FMT>(a), was);
   if (tid == 0) *scale = now;
 
   uint8_t* codes = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);

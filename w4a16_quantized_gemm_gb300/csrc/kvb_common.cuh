@@ -127,9 +127,11 @@ __device__ __forceinline__ float decode(uint32_t c) {
   const uint32_t h = e4m3x2_half2((uint16_t)c);
   return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
 }
+// The scale that values up to `a` need: a times the binary32 reciprocal of the
+// largest code, at least 2^-30.
 template <int FMT>
-__device__ __forceinline__ float qmax() {
-  return FMT == TM_KVB_INT8 ? 127.f : 448.f;
+__device__ __forceinline__ float scale_for(float a) {
+  return fmaxf(__fmul_rn(a, FMT == TM_KVB_INT8 ? 1.f / 127.f : 1.f / 448.f), kScaleFloor);
 }
 
 // 16-byte asynchronous copy global -> shared; zeros where !ok.

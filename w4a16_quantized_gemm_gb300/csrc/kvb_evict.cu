@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        now = fmaxf(__fdiv_rn(a, qmax<FMT>()), kScaleFloor);
+        now = scale_for<FMT>(a);
         for (int c = lane; c < chunks; c += 32) {
           uint4* at = reinterpret_cast<uint4*>(stage + 16 * c);
           const uint4 q = *at;
