@@ -337,3 +337,22 @@ def test_refusals_of_the_binding():
         binding.KVBlocks(blocks.k, blocks.v, blocks.ks[:2], blocks.vs)
     with pytest.raises(ValueError):
         binding.KVBlocks(blocks.k.view(torch.uint8), blocks.v, blocks.ks, blocks.vs)
+
+
+@pytest.mark.parametrize("fmt,dtype,D,T,Hq,Hkv", SHAPES)
+def test_prompts(fmt, dtype, D, T, Hq, Hkv):
+    """Many rows: one and two row tiles, several pairs of them, tiles cut by the length, slices."""
+    tag = f"kvb/prompt/{fmt}/{dtype}/{D}/{T}"
+    c = Cache(tag, [200, 131, 64, 300, 0, 1], Hkv, D, T, fmt)
+    run_attention(c, [200, 128, 40, 3, 0, 1], Hq, dtype, tag, stride=1)
+    c = Cache(tag, [1500], Hkv, D, T, fmt)
+    run_attention(c, [70], Hq, dtype, tag)
+    assert binding.device_error() == 0
+
+
+def test_prompt_with_holes_and_negative_scale():
+    c = Cache("kvb/prompt/holes", [400, 256], 2, 128, 16, "e4m3")
+    c.table[0, 3], c.table[0, 8:16], c.table[1, :] = -1, -1, 2 ** 30
+    run_attention(c, [150, 90], 8, "fp16", "prompt/holes", scale=-0.1)
+    run_attention(c, [2, 2], 8, "fp16", "draft/holes", scale=-0.1)
+    assert binding.device_error() == 0

@@ -559,26 +559,43 @@ tm_status launch_attn(const AttnParams& P, int groups, cudaStream_t s) {
 
 // Launch settings and the workspace's layout, from the host fields alone.
 struct Plan {
-  int rt, groups, chunk, chunks;
+  int rt;            // 16-row tiles per CTA of the kernel for few rows; 0: the tcgen05 kernel
+  int rows_per_cta;  // rows that share a CTA
+  int groups;        // CTAs along the rows
+  int chunk, chunks;
   bool scores;  // token weights from kept scores (few rows), else from a second pass
   size_t part, part_ml, lse, score, bytes;  // offsets, total
 };
+
+constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows
 
 static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   Plan p = {};
   const int G = Hq / V.Hkv;
   const long long rows = (long long)V.max_q * G;
-  p.rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.groups = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
-  const long long slots = (long long)num_sms(current_device()) * (p.rt == 1 ? 3 : p.rt == 2 ? 2 : 1);
+  const long long sms = num_sms(current_device());
+  p.rt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= kFewRows ? 4 : 0;
+  p.rows_per_cta = p.rt ? 16 * p.rt : 256;
+  p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
   const long long ctas = (long long)V.B * V.Hkv * p.groups;
-  // Enough slices for two waves of CTAs, none shorter than four tiles.
-  long long chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
-  chunk = (chunk + kTile - 1) / kTile * kTile;
-  if (chunk < 4 * kTile) chunk = 4 * kTile;
+  long long chunk, least, unit;
+  if (p.rt) {
+    // Enough slices for two waves of CTAs, none shorter than four tiles.
+    const long long slots = sms * (p.rt == 1 ? 3 : p.rt == 2 ? 2 : 1);
+    unit = kTile;
+    least = 4 * kTile;
+    chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
+  } else {
+    // Slices only where the rows alone leave SMs idle.
+    unit = 128;
+    least = 512;
+    chunk = ctas >= sms ? V.max_len : ((long long)V.max_len * ctas + 2 * sms - 1) / (2 * sms);
+  }
+  chunk = (chunk + unit - 1) / unit * unit;
+  if (chunk < least) chunk = least;
   long long chunks = (V.max_len + chunk - 1) / chunk;
   if (chunks < 1) chunks = 1;
-  p.chunk = (int)(chunk > 0x7fffffc0ll ? 0x7fffffc0ll : chunk);
+  p.chunk = (int)(chunk > 0x7fffff80ll ? 0x7fffff80ll : chunk);
   p.chunks = (int)chunks;
   auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
   const size_t hr = (size_t)V.rows * Hq;
@@ -592,7 +609,7 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   if (weights) {
     p.lse = at;
     at = al(at + hr * 4);
-    p.scores = rows <= 64;
+    p.scores = p.rt != 0;
     if (p.scores) {
       p.score = at;
       at = al(at + hr * (((size_t)V.max_len + kTile - 1) / kTile * kTile) * 4);
@@ -613,7 +630,7 @@ static tm_status check_heads(const View& V, const tm_kvb_batch* batch, int Hq) {
   const bool one_each = batch->q_start == nullptr;
   if (one_each && (batch->rows != batch->B || (batch->B > 0 && batch->max_q < 1))) return TM_ERR_INVALID_ARG;
   const long long rows = (long long)V.max_q * (Hq / V.Hkv);
-  if (rows > 0x7fffffffll || (rows + 15) / 16 * V.Hkv > 65535ll * 4) return TM_ERR_UNSUPPORTED;
+  if (rows > 4000000ll || (long long)V.B * V.Hkv > 0x7fffffffll) return TM_ERR_UNSUPPORTED;  // the grid's limits
   return TM_OK;
 }
 
@@ -630,7 +647,8 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
 
 template <int FMT, int D>
 static tm_status run(const AttnParams& P, const Plan& p, cudaStream_t s, int* launches) {
-  tm_status st = p.rt == 1   ? launch_attn<FMT, D, 1>(P, p.groups, s)
+  tm_status st = p.rt == 0   ? launch_prefill_attn(P, FMT, D, p.groups, s)
+                 : p.rt == 1 ? launch_attn<FMT, D, 1>(P, p.groups, s)
                  : p.rt == 2 ? launch_attn<FMT, D, 2>(P, p.groups, s)
                              : launch_attn<FMT, D, 4>(P, p.groups, s);
   if (st != TM_OK) return st;
@@ -687,7 +705,7 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   P.w_stride = w_stride;
   P.chunk = p.chunk;
   P.chunks = p.chunks;
-  P.rows_per_cta = 16 * p.rt;
+  P.rows_per_cta = p.rows_per_cta;
   if (p.chunks > 1) {
     P.part = reinterpret_cast<float*>(ws + p.part);
     P.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);

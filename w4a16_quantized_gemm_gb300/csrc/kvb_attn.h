@@ -25,5 +25,9 @@ struct AttnParams {
   long long score_stride;
 };
 
+// The tcgen05 kernel (kvb_prefill.cu): `pairs` pairs of 128-row tiles per
+// (sequence, KV head); slices of P.chunk tokens, a multiple of 128.
+tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs, cudaStream_t stream);
+
 }  // namespace kvb
 }  // namespace w4

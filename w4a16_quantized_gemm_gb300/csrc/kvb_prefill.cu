@@ -1,0 +1,500 @@
+// Attention over the paged 8-bit KV cache for many rows (prompts and their
+// chunks): bound by the tensor cores, on tcgen05 with the scores, the weights and
+// the output in tensor memory.
+//
+// A CTA takes one (sequence, KV head), 2 x 128 rows (query token, query head of
+// the group: heads that share keys share the tile) and, where there are few
+// rows, a slice of the tokens; tiles of 128 tokens.
+//   warps 0-3, 4-7: softmax of the first and the second 128 rows, one row per
+//     thread: scores from tensor memory, the running maximum (which moves only
+//     when it has grown by more than 8, so that the output is rarely rescaled), weights
+//     as fp16 back into the columns of the scores;
+//   warps 8-11: codes -> fp16 numbers (exact) in shared memory, K and V tiles in
+//     turn through a ring of four; the next tile's codes are requested while
+//     this one's are converted;
+//   warp 12: S_i = Q_i K^T (A, B in shared memory) and O_i += P_i V (A in tensor
+//     memory, V as it lies, MN-major), the two row tiles in turn, so that one
+//     computes while the other's softmax runs;
+//   warp 13: pages and scales of the tiles to come.
+// The scales stay out of the products as in the kernel for few rows: ks
+// multiplies the scores, log2 vs joins the exponent and leaves l again.
+// All waits are bounded.
+#include "kvb_attn.h"
+
+namespace w4 {
+namespace kvb {
+
+static __device__ uint32_t s_err_kvb;
+
+constexpr int kPreThreads = 512;
+constexpr int kPreTile = 128;   // tokens per tile, rows per row tile
+constexpr int kPreSlots = 4;    // K and V tiles in flight
+constexpr int kPreMeta = 4;     // tiles whose scales are in flight
+constexpr float kPreBias = 6.f;
+constexpr float kPreSlack = 8.f;
+constexpr float kPreNone = -1e30f;
+
+template <int D>
+struct PreShape {
+  static constexpr int PANELS = D / 64;                 // 64 fp16 = one 128-byte swizzled row
+  static constexpr uint32_t PANEL = kPreTile * 128;     // 16 KB
+  static constexpr uint32_t TILE = PANELS * PANEL;
+  static constexpr uint32_t Q_OFF = 0;
+  static constexpr uint32_t KV_OFF = 2 * TILE;
+  static constexpr uint32_t META = KV_OFF + kPreSlots * TILE;  // [kPreMeta][8] x {ks, lv, 1 / vs, page}
+  static constexpr uint32_t HOLES = META + kPreMeta * 8 * 16;  // [kPreMeta] bits of the 16-token groups
+  static constexpr uint32_t BARS = HOLES + 16;
+  static constexpr uint32_t SMEM = BARS + 256 + 1024;
+};
+
+// MN-major operand: rows of K (tokens) of 128 bytes, 128-byte swizzle, 8-row
+// atoms 1024 bytes apart along K, 64-element panels `panel` bytes apart along N.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t panel) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParams P) {
+  using SH = PreShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+  const View& V = P.V;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
+  const int chunk = blockIdx.y % P.chunks;
+  const int pair = (int)(gridDim.y / P.chunks) - 1 - blockIdx.y / P.chunks;  // the longest rows first
+  const Span s = span(V, b);
+  const int rows = s.n * P.G;
+  const int row_base = pair * 2 * kPreTile;
+  if (row_base >= rows) return;
+  const int last_i = (min(row_base + 2 * kPreTile, rows) - 1) / P.G;
+  const int j0 = chunk * P.chunk;
+  const int j1 = min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
+  if (j0 >= j1 && chunk > 0) return;  // slice 0 still writes what an empty row gives
+  const int N = j1 > j0 ? (j1 - j0 + kPreTile - 1) / kPreTile : 0;
+  const int M = rows - row_base > kPreTile ? 2 : 1;  // row tiles
+
+  const uint32_t bars = base + SH::BARS;
+  const uint32_t q_full = bars;
+  auto s_full = [&](int i) { return bars + 8 + 8 * i; };
+  auto p_full = [&](int i) { return bars + 24 + 8 * i; };
+  const uint32_t o_full = bars + 40;
+  auto kv_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto kv_empty = [&](int i) { return bars + 80 + 8 * i; };
+  auto meta_full = [&](int i) { return bars + 112 + 8 * i; };
+  auto meta_empty = [&](int i) { return bars + 144 + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 176);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 180);
+  if (tid == 0) {
+    mbar_init(q_full, 4 * M);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+    }
+    mbar_init(o_full, 1);
+    for (int i = 0; i < kPreSlots; ++i) {
+      mbar_init(kv_full(i), 4);
+      mbar_init(kv_empty(i), 1);
+    }
+    for (int i = 0; i < kPreMeta; ++i) {
+      mbar_init(meta_full(i), 1);
+      mbar_init(meta_empty(i), 4 + 4 * M);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S_0, S_1 (P_i over S_i), then O_0, O_1
+
+  if (warp < 8) {
+    // ---------------- softmax: one row per thread ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int row = row_base + i * kPreTile + r;
+    const bool ok = row < rows;
+    const int qi = ok ? row / P.G : 0;
+    const size_t hr = (size_t)(s.row0 + qi) * P.Hq + h * P.G + (ok ? row - qi * P.G : 0);
+    const int last = ok ? min(s.old + qi, s.len - 1) : -1;  // last visible token
+    float mul = fabsf(P.scale_log2);
+    if (i < M) {
+      // The row's queries into shared memory, as fp16; bf16 rows times a power of two.  A negative
+      // scale is taken into their sign.
+      const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;
+      const uint16_t* q = P.Q + (s.row0 + qi) * P.q_stride + (long long)(h * P.G + (ok ? row - qi * P.G : 0)) * D;
+      float up = 1.f;
+      if (P.bf16) {
+        float m = 0.f;
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack(wd[k], true);
+            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);
+        up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
+        mul *= __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
+      }
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
+        uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+        if (P.bf16)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack(wd[k], true);
+            wd[k] = pack_half2(f.x * up, f.y * up);
+          }
+        sts128(base + SH::Q_OFF + i * SH::TILE + (c >> 3) * SH::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+               wd[0] ^ flip, wd[1] ^ flip, wd[2] ^ flip, wd[3] ^ flip);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      float m = kPreNone, l = 0.f;
+      const uint32_t ts = tmem + lanes + 128 * i, to = tmem + lanes + 256 + D * i;
+      bool alive = true;
+      for (int n = 0; n < N; ++n) {
+        const int slot = n % kPreMeta;
+        const uint32_t ph = (uint32_t)(n / kPreMeta) & 1u;
+        alive = mbar_wait(meta_full(slot), ph, abort_flag, &s_err_kvb) &&
+                mbar_wait(s_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t meta = base + SH::META + slot * 128;
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_ld_32x32b_x32(ts + 32 * c, v[c]);
+        tc_wait_ld();
+        const int rel = last - (j0 + n * kPreTile);  // columns 0 .. rel are visible
+        const uint32_t holes = lds32(base + SH::HOLES + 4 * slot);
+        if (!__all_sync(0xffffffffu, rel >= kPreTile - 1) || holes) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > rel || ((holes >> (c >> 4)) & 1u)) v[c >> 5][c & 31] = 0xff800000u;
+        }
+        float tm = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 mt = lds_f4(meta + 16 * g);
+          float a = __uint_as_float(v[g >> 1][16 * (g & 1)]);
+#pragma unroll
+          for (int c = 1; c < 16; ++c) a = fmaxf(a, __uint_as_float(v[g >> 1][16 * (g & 1) + c]));
+          tm = fmaxf(tm, fmaf(a, fmaxf(mt.x * mul, 1e-35f), mt.y));
+        }
+        if (__any_sync(0xffffffffu, tm > m + kPreSlack)) {
+          const float mn = fmaxf(m, tm), f = ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (n > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc_ld_32x32b_x32(to + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tc_st_32x32b_x32(to + c, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int g = 4 * half + k;
+            const float4 mt = lds_f4(meta + 16 * g);
+            const float cg = fmaxf(mt.x * mul, 1e-35f), off = mt.y + kPreBias - m;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(v[g >> 1][16 * (g & 1) + c]), cg, off));
+              const float p1 = ex2(fmaf(__uint_as_float(v[g >> 1][16 * (g & 1) + c + 1]), cg, off));
+              sum += p0 + p1;
+              p[8 * k + c / 2] = pack_half2(p0, p1);
+            }
+            l = fmaf(sum, mt.z, l);
+          }
+          tc_st_32x32b_x32(ts + 32 * half, p);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_full(i));
+          mbar_arrive(meta_empty(slot));
+        }
+      }
+      // ---- the row's output, or its state for the joining launch
+      if (N > 0 && alive) {
+        alive = mbar_wait(o_full, 0, abort_flag, &s_err_kvb);
+        alive = __all_sync(0xffffffffu, alive);
+        tc_fence_after();
+      }
+      if (alive) {
+        const float inv = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (N > 0) {
+            tc_ld_32x32b_x32(to + c, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (!ok) continue;
+          if (P.chunks == 1) {
+            uint16_t* out = P.out + hr * D + c;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t wd[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float f0 = __uint_as_float(o[k + 2 * e]) * inv, f1 = __uint_as_float(o[k + 2 * e + 1]) * inv;
+                wd[e] = P.bf16 ? pack_bf162(f0, f1) : pack_half2(f0, f1);
+              }
+              *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+            }
+          } else {
+            float* dst = P.part + (hr * P.chunks + chunk) * D + c;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        if (ok) {
+          if (P.chunks > 1)
+            P.part_ml[hr * P.chunks + chunk] = make_float2(m - kPreBias, l);
+          else if (P.lse)
+            P.lse[hr] = l == 0.f ? -INFINITY : (log2f(l) + m - kPreBias) * 0.693147180559945f;
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    // ---------------- codes -> fp16 tiles ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // A warp's 16-byte chunks of one pass: 2 (or 4) rows x 4 chunks x panels, so that eight lanes
+    // write two rows of one panel (no bank conflicts).
+    constexpr int RPP = D == 128 ? 16 : 32;  // rows per pass of the four warps
+    constexpr int PASSES = kPreTile / RPP;
+    const int c4 = lane & 3;
+    const int panel = D == 128 ? (lane >> 3) & 1 : 0;
+    const int r0 = (warp - 8) * (RPP / 4) + ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
+    const int code_off = panel * 64 + c4 * 16;
+    const int items = 2 * N;  // K_0, V_0, K_1, V_1, ...
+    uint4 x[PASSES];
+    auto fetch = [&](int item, int p) {
+      const int n = item >> 1, r = r0 + p * RPP, j = j0 + n * kPreTile + r;
+      const int page = (int)lds32(base + SH::META + (n % kPreMeta) * 128 + (r >> 4) * 16 + 12);
+      x[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (page >= 0 && j < j1)
+        x[p] = *reinterpret_cast<const uint4*>((item & 1 ? V.v : V.k) +
+                                               ((((size_t)page * V.Hkv + h) << V.t_shift) + (j & ((1 << V.t_shift) - 1))) * D +
+                                               code_off);
+    };
+    bool alive = true;
+    if (items) {
+      alive = mbar_wait(meta_full(0), 0, abort_flag, &s_err_kvb);
+      if (__all_sync(0xffffffffu, alive)) {
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) fetch(0, p);
+      } else {
+        alive = false;
+      }
+    }
+    for (int item = 0; item < items && alive; ++item) {
+      const int slot = item % kPreSlots;
+      alive = mbar_wait(kv_empty(slot), ((uint32_t)(item / kPreSlots) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+      const bool more = item + 1 < items;
+      if (more && !((item + 1) & 1))
+        alive = alive && mbar_wait(meta_full(((item + 1) >> 1) % kPreMeta), (uint32_t)(((item + 1) >> 1) / kPreMeta) & 1u,
+                                   abort_flag, &s_err_kvb);
+      if (!__all_sync(0xffffffffu, alive)) {
+        alive = false;
+        break;
+      }
+      const uint32_t dst = base + SH::KV_OFF + slot * SH::TILE + panel * SH::PANEL;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = r0 + p * RPP;
+        uint32_t o[8];
+        codes_half<FMT>(x[p].x, o[0], o[1]);
+        codes_half<FMT>(x[p].y, o[2], o[3]);
+        codes_half<FMT>(x[p].z, o[4], o[5]);
+        codes_half<FMT>(x[p].w, o[6], o[7]);
+        if (more) fetch(item + 1, p);
+        const uint32_t at = dst + r * 128;
+        sts128(at + (((2 * c4) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        sts128(at + (((2 * c4 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(kv_full(slot));
+        // The pages of tile n were last read when V_n was fetched, during K_n's turn.
+        if (!(item & 1)) mbar_arrive(meta_empty((item >> 1) % kPreMeta));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    if (warp == 12) {
+      // ---------------- MMA issuer ----------------
+      if (lane == 0 && N > 0) {
+        constexpr uint32_t id_s = idesc_f16_f32(128, 128);
+        constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
+        bool alive = mbar_wait(q_full, 0, abort_flag, &s_err_kvb);
+        auto slot_of = [&](int item) { return base + SH::KV_OFF + (item % kPreSlots) * SH::TILE; };
+        auto scores = [&](int i, int n) {
+          const uint32_t kt = slot_of(2 * n), qt = base + SH::Q_OFF + i * SH::TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * SH::PANEL + (k & 3) * 32;
+            tc_mma_f16(tmem + 128 * i, smem_desc_sw128(qt + off), smem_desc_sw128(kt + off), id_s, k > 0);
+          }
+          tc_commit(s_full(i));
+        };
+        auto wait_kv = [&](int item) {
+          return mbar_wait(kv_full(item % kPreSlots), (uint32_t)(item / kPreSlots) & 1u, abort_flag, &s_err_kvb);
+        };
+        alive = alive && wait_kv(0);
+        if (alive) {
+          tc_fence_after();
+          for (int i = 0; i < M; ++i) scores(i, 0);
+          tc_commit(kv_empty(0));
+        }
+        for (int n = 0; n < N && alive; ++n) {
+          alive = wait_kv(2 * n + 1);
+          const uint64_t dv = smem_desc_mn(slot_of(2 * n + 1), SH::PANEL);
+          for (int i = 0; i < M && alive; ++i) {
+            alive = mbar_wait(p_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
+            if (!alive) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kPreTile / 16; ++k)
+              tc_mma_f16_ta(tmem + 256 + D * i, tmem + 128 * i + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), id_o,
+                            n > 0 || k > 0);
+            if (n + 1 < N) {
+              if (i == 0) alive = wait_kv(2 * n + 2);
+              if (!alive) break;
+              tc_fence_after();
+              scores(i, n + 1);
+            }
+          }
+          if (!alive) break;
+          tc_commit(kv_empty((2 * n + 1) % kPreSlots));
+          if (n + 1 < N) tc_commit(kv_empty((2 * n + 2) % kPreSlots));
+        }
+        tc_commit(o_full);
+        // Nothing is left in flight when tensor memory is freed, on an abort either.
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_wait(o_full, 0)) {
+          if (globaltimer() - t0 > kWaitLimitNs) {
+            atomicOr(&s_err_kvb, kErrTimeout);
+            break;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---------------- pages and scales ----------------
+      for (int n = 0; n < N; ++n) {
+        const int slot = n % kPreMeta;
+        const bool alive =
+            mbar_wait(meta_empty(slot), ((uint32_t)(n / kPreMeta) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+        if (!__all_sync(0xffffffffu, alive)) break;
+        const int j = j0 + n * kPreTile + 16 * lane;
+        bool hole = false;
+        if (lane < 8) {
+          const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+          hole = j < j1 && page < 0;
+          float ks = 1.f, vs = 1.f;
+          if (page >= 0) {
+            const size_t cell = (size_t)page * V.Hkv + h;
+            ks = V.ks[cell];
+            vs = fmaxf(V.vs[cell], kScaleFloor);
+          }
+          const float lv = __log2f(vs);
+          sts128(base + SH::META + slot * 128 + lane * 16, __float_as_uint(ks), __float_as_uint(lv),
+                 __float_as_uint(ex2(-lv)), (uint32_t)page);
+        }
+        const uint32_t holes = __ballot_sync(0xffffffffu, hole);
+        if (lane == 0)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::HOLES + 4 * slot), "r"(holes) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(meta_full(slot));
+        __syncwarp();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int D>
+static tm_status launch(const AttnParams& P, int pairs, cudaStream_t stream) {
+  using SH = PreShape<D>;
+  static std::atomic<unsigned long long> done{0};
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(prefill_kernel<FMT, D>), SH::SMEM)) return TM_ERR_CUDA;
+  const dim3 grid((unsigned)(P.V.B * P.V.Hkv), (unsigned)(pairs * P.chunks));
+  prefill_kernel<FMT, D><<<grid, kPreThreads, SH::SMEM, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs, cudaStream_t stream) {
+  if (format == TM_KVB_INT8)
+    return D == 64 ? launch<TM_KVB_INT8, 64>(P, pairs, stream) : launch<TM_KVB_INT8, 128>(P, pairs, stream);
+  return D == 64 ? launch<TM_KVB_E4M3, 64>(P, pairs, stream) : launch<TM_KVB_E4M3, 128>(P, pairs, stream);
+}
+
+}  // namespace kvb
+
+cudaError_t kvb_error_bits(uint32_t* bits, bool clear) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, kvb::s_err_kvb, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (clear && v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(kvb::s_err_kvb, &zero, sizeof(zero));
+  }
+  *bits = v;
+  return e;
+}
+
+}  // namespace w4
