@@ -430,123 +430,6 @@ __global__ void __launch_bounds__(256) score_weights_kernel(const AttnParams P) 
   P.w_out[at] = (P.w_in ? P.w_in[at] : 0.f) + sum;
 }
 
-// ---- the same for many rows: the scores once more.  A warp takes 16 tokens,
-// their codes in registers, and all rows that see them, 16 at a time.
-template <int FMT, int D>
-__global__ void __launch_bounds__(128) row_weights_kernel(const AttnParams P) {
-  constexpr int KS = D / 16;
-  const View& V = P.V;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
-  const int tok0 = blockIdx.x * 64 + (threadIdx.x >> 5) * 16;
-  const Span s = span(V, b);
-  if (tok0 >= P.w_stride) return;
-  float sum[2][2] = {};
-  const int page = tok0 < s.len ? page_of(V, V.table, b, V.table_stride, tok0 >> V.t_shift) : -1;
-  if (page >= 0) {
-    const size_t cell = (size_t)page * V.Hkv + h;
-    const float ks = V.ks[cell];
-    uint32_t kb[2][KS][2];
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const uint8_t* src = V.k + ((cell << V.t_shift) + ((tok0 + 8 * a + gr) & ((1 << V.t_shift) - 1))) * D;
-#pragma unroll
-      for (int j = 0; j < KS / 4; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + 16 * (t + 4 * j));
-        codes_half<FMT>(x.x, kb[a][4 * j][0], kb[a][4 * j][1]);
-        codes_half<FMT>(x.y, kb[a][4 * j + 1][0], kb[a][4 * j + 1][1]);
-        codes_half<FMT>(x.z, kb[a][4 * j + 2][0], kb[a][4 * j + 2][1]);
-        codes_half<FMT>(x.w, kb[a][4 * j + 3][0], kb[a][4 * j + 3][1]);
-      }
-    }
-    const int rows = s.n * P.G;
-    const int i0 = max(tok0 - s.old, 0);  // the first query that sees a token of the warp
-    for (int row0 = i0 * P.G; row0 < rows; row0 += 16) {
-      uint32_t qa[KS][4];
-      float mul[2], lse[2];
-      int lastv[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = row0 + gr + 8 * e;
-        const bool ok = row < rows;
-        const int i = ok ? row / P.G : 0;
-        const int hq = h * P.G + (ok ? row - i * P.G : 0);
-        const size_t hr = (size_t)(s.row0 + i) * P.Hq + hq;
-        lse[e] = ok ? P.lse[hr] * 1.44269504088896f : -INFINITY;
-        lastv[e] = ok && lse[e] != -INFINITY ? min(s.old + i, s.len - 1) : -1;
-        const uint16_t* q = P.Q + (s.row0 + i) * P.q_stride + (long long)hq * D;
-        float m = 0.f;
-        uint32_t raw[KS][2];
-#pragma unroll
-        for (int j = 0; j < KS / 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 16 * (t + 4 * j) + 8 * k) : make_uint4(0, 0, 0, 0);
-            raw[4 * j + 2 * k][0] = x.x;
-            raw[4 * j + 2 * k][1] = x.y;
-            raw[4 * j + 2 * k + 1][0] = x.z;
-            raw[4 * j + 2 * k + 1][1] = x.w;
-          }
-        mul[e] = ks * P.scale_log2;
-        if (P.bf16) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 f = unpack(raw[k][x], true);
-              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);
-          const float up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
-          mul[e] *= __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 f = unpack(raw[k][x], true);
-              raw[k][x] = pack_half2(f.x * up, f.y * up);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qa[k][e] = raw[k][0];
-          qa[k][2 + e] = raw[k][1];
-        }
-      }
-      float sc[2][4] = {};
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int k = 0; k < KS; ++k) mma_16816(sc[a], qa[k], kb[a][k][0], kb[a][k][1]);
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int j = tok0 + 8 * a + 2 * t + x;
-            const float p = ex2(fmaf(sc[a][2 * e + x], mul[e], -lse[e]));
-            sum[a][x] += j <= lastv[e] ? p : 0.f;
-          }
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float v = sum[a][x];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      const int j = tok0 + 8 * a + 2 * t + x;
-      if (gr == 0 && j < P.w_stride) {
-        const size_t at = ((size_t)b * V.Hkv + h) * P.w_stride + j;
-        P.w_out[at] = (P.w_in ? P.w_in[at] : 0.f) + v;
-      }
-    }
-}
-
 template <int FMT, int D, int RT>
 tm_status launch_attn(const AttnParams& P, int groups, cudaStream_t s) {
   using SH = AttnShape<D, RT>;
@@ -664,8 +547,8 @@ static tm_status run(const AttnParams& P, const Plan& p, cudaStream_t s, int* la
       const dim3 grid((unsigned)((P.w_stride + 255) / 256), (unsigned)V.Hkv, (unsigned)V.B);
       score_weights_kernel<<<grid, 256, 0, s>>>(P);
     } else {
-      const dim3 grid((unsigned)((P.w_stride + 63) / 64), (unsigned)V.Hkv, (unsigned)V.B);
-      row_weights_kernel<FMT, D><<<grid, 128, 0, s>>>(P);
+      st = launch_row_weights(P, FMT, D, s);
+      if (st != TM_OK) return st;
     }
     ++*launches;
   }
@@ -685,7 +568,8 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   if (w_in && !w_out) return TM_ERR_INVALID_ARG;
   if (V.B == 0 || V.rows == 0 || V.max_q == 0) return TM_OK;
   if (!Q || !out || q_stride < (long long)Hq * cache->D) return TM_ERR_INVALID_ARG;
-  if (w_out && (w_stride < V.max_len || w_stride > 0x7fffff00ll)) return TM_ERR_INVALID_ARG;
+  if (w_out && w_stride < V.max_len) return TM_ERR_INVALID_ARG;
+  if (w_out && w_stride > 65535ll * 128) return TM_ERR_UNSUPPORTED;  // the grid's limit
   if (!aligned(Q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(w_in, 4) ||
       !aligned(w_out, 4) || !aligned(workspace, 16))
     return TM_ERR_ALIGNMENT;

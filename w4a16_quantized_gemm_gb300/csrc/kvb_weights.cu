@@ -1,0 +1,283 @@
+// The weight that each token of the paged 8-bit KV cache drew from many rows:
+// w_j += sum over rows of 2^(s_j - lse), the scores once more, on tcgen05.
+//
+// The scores stand transposed: a CTA takes 128 tokens of one (sequence, KV
+// head), their codes exact in fp16 (or bf16, after the queries' type) as the A
+// operand in tensor memory, and all rows that see them, 128 at a time as the B
+// operand in shared memory -- the queries' own bits, no scaling.  A thread of
+// the epilogue owns one token and half of the rows' columns, so the sum needs no
+// exchange but one at the end and has a fixed order; a compensated sum joins the
+// row tiles (a long prompt adds tens of thousands of terms).
+//   warps 0-7: epilogue, warps w and w + 4 on the same tokens;
+//   warps 8-11: query rows by 16-byte asynchronous copies, three tiles ahead, and their lse;
+//   warp 12: the products, scores double-buffered in tensor memory.
+// Bound by the exponentials and the tensor cores about equally.
+#include "kvb_attn.h"
+
+namespace w4 {
+namespace kvb {
+
+static __device__ uint32_t s_err_kvbw;
+
+constexpr int kWtThreads = 416;
+constexpr int kWtTile = 128;  // tokens per CTA, rows per tile
+constexpr int kWtSlots = 3;
+
+template <int D>
+struct WtShape {
+  static constexpr uint32_t PANEL = kWtTile * 128;
+  static constexpr uint32_t TILE = D / 64 * PANEL;
+  static constexpr uint32_t ROWS = kWtSlots * TILE;              // [slots][128] x lse (base 2; +inf: no row)
+  static constexpr uint32_t LAST = ROWS + kWtSlots * 128 * 4;    // [slots][128] x last visible token
+  static constexpr uint32_t SUMS = LAST + kWtSlots * 128 * 4;    // [128]
+  static constexpr uint32_t BARS = SUMS + 128 * 4;
+  static constexpr uint32_t SMEM = BARS + 128 + 1024;
+};
+
+template <int FMT, int D, bool BF16>
+__global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams P) {
+  using SH = WtShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+  const View& V = P.V;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
+  const int tok0 = blockIdx.y * kWtTile;
+  const Span s = span(V, b);
+  const int rows = s.n * P.G;
+  const int first = max(tok0 - s.old, 0);  // the first query that sees a token of the tile
+  const int r0 = first < s.n ? first * P.G : rows;
+  const int N = tok0 < s.len && r0 < rows ? (rows - r0 + kWtTile - 1) / kWtTile : 0;
+
+  const uint32_t bars = base + SH::BARS;
+  auto q_full = [&](int i) { return bars + 8 * i; };
+  auto q_empty = [&](int i) { return bars + 24 + 8 * i; };
+  auto s_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto s_empty = [&](int i) { return bars + 64 + 8 * i; };
+  const uint32_t a_full = bars + 80, done = bars + 88;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 96);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 100);
+  const size_t out = ((size_t)b * V.Hkv + h) * P.w_stride;
+  if (N == 0) {  // nothing is added here
+    const int j = tok0 + tid;
+    if (tid < kWtTile && j < P.w_stride) P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kWtSlots; ++i) {
+      mbar_init(q_full(i), 4);
+      mbar_init(q_empty(i), 1 + 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(s_empty(i), 8);
+    }
+    mbar_init(a_full, 4);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // A in columns 0 .. D/2 - 1, scores from 128 and 256
+
+  if (warp < 8) {
+    // ---------------- one token per thread, columns 64 half .. 64 half + 63 ----------------
+    const int half = warp >> 2, r = tid & 127, j = tok0 + r;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int page = j < s.len ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+    const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
+    if (half == 0) {
+      const uint8_t* src = V.k + ((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 64) {
+        uint32_t o[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = page >= 0 ? *reinterpret_cast<const uint4*>(src + c + 16 * k) : make_uint4(0, 0, 0, 0);
+          codes_half<FMT>(x.x, o[8 * k], o[8 * k + 1]);
+          codes_half<FMT>(x.y, o[8 * k + 2], o[8 * k + 3]);
+          codes_half<FMT>(x.z, o[8 * k + 4], o[8 * k + 5]);
+          codes_half<FMT>(x.w, o[8 * k + 6], o[8 * k + 7]);
+        }
+        if (BF16)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float2 f = unpack(o[k], false);
+            o[k] = pack_bf162(f.x, f.y);
+          }
+        tc_st_32x32b_x32(tmem + lanes + c / 2, o);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full);
+    }
+    const float c = page >= 0 ? V.ks[cell] * P.scale_log2 : 0.f;
+    float sum = 0.f, lost = 0.f;
+    for (int n = 0; n < N; ++n) {
+      const int slot = n % kWtSlots;
+      bool alive = mbar_wait(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
+                   mbar_wait(s_full(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag, &s_err_kvbw);
+      if (!__all_sync(0xffffffffu, alive)) break;
+      tc_fence_after();
+      uint32_t v[2][32];
+      tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * (n & 1) + 64 * half, v[0]);
+      tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * (n & 1) + 64 * half + 32, v[1]);
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_empty(n & 1));
+      const uint32_t row = base + SH::ROWS + slot * 512 + 256 * half;
+      float part[4] = {};
+      if (s.old + (r0 + n * kWtTile) / P.G >= tok0 + kWtTile - 1) {
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const uint4 l = lds128(row + 4 * k);
+          part[0] += ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, -__uint_as_float(l.x)));
+          part[1] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, -__uint_as_float(l.y)));
+          part[2] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 2]), c, -__uint_as_float(l.z)));
+          part[3] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 3]), c, -__uint_as_float(l.w)));
+        }
+      } else {
+        const uint32_t last = base + SH::LAST + slot * 512 + 256 * half;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float p = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, -__uint_as_float(lds32(row + 4 * k))));
+          part[k & 3] += j <= (int)lds32(last + 4 * k) ? p : 0.f;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty(slot));
+      // sum += the tile's, with what rounding drops carried along (Kahan)
+      const float y = __fadd_rn(__fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])), -lost);
+      const float t = __fadd_rn(sum, y);
+      lost = __fadd_rn(__fadd_rn(t, -sum), -y);
+      sum = t;
+    }
+    float* sums = reinterpret_cast<float*>(smem + SH::SUMS);
+    if (half == 1) sums[r] = sum;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (half == 0 && j < P.w_stride) P.w_out[out + j] = (P.w_in ? P.w_in[out + j] : 0.f) + (page >= 0 ? sum + sums[r] : 0.f);
+    tc_fence_before();
+  } else if (warp < 12) {
+    // ---------------- query rows ----------------
+    const int t = tid - 256;
+    constexpr int CPR = D / 8;  // 16-byte chunks per row
+    constexpr int RPP = 128 / CPR;
+    const int c = t % CPR, rr = t / CPR;
+    bool alive = true;
+    auto issue = [&](int n) {
+      if (n < N) {
+        const int slot = n % kWtSlots;
+        alive = alive && mbar_wait(q_empty(slot), ((uint32_t)(n / kWtSlots) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
+        if (alive) {
+          const int row0 = r0 + n * kWtTile;
+#pragma unroll 4
+          for (int p = 0; p < kWtTile / RPP; ++p) {
+            const int q = p * RPP + rr, row = row0 + q;
+            const bool ok = row < rows;
+            const int i = ok ? row / P.G : 0, g = ok ? row - i * P.G : 0;
+            cp16(base + slot * SH::TILE + (c >> 3) * SH::PANEL + q * 128 + (((c & 7) ^ (q & 7)) << 4),
+                 P.Q + (s.row0 + i) * P.q_stride + (long long)(h * P.G + g) * D + 8 * c, ok);
+          }
+          const int row = row0 + t;
+          float l = INFINITY;
+          int last = -1;
+          if (row < rows) {
+            const int i = row / P.G;
+            const float x = P.lse[(size_t)(s.row0 + i) * P.Hq + h * P.G + (row - i * P.G)];
+            if (x != -INFINITY) l = x * 1.44269504088896f;
+            last = min(s.old + i, s.len - 1);
+          }
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + SH::ROWS + slot * 512 + 4 * t), "f"(l) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::LAST + slot * 512 + 4 * t), "r"(last) : "memory");
+        }
+      }
+      cp_commit();
+    };
+    issue(0);
+    issue(1);
+    for (int n = 0; n < N; ++n) {
+      cp_wait<1>();
+      fence_proxy_async_smem();
+      if (!__all_sync(0xffffffffu, alive)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(n % kWtSlots));
+      issue(n + 2);
+    }
+    cp_wait<0>();
+  } else if (lane == 0) {
+    // ---------------- products ----------------
+    constexpr uint32_t id = idesc_f16_f32(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+    bool alive = mbar_wait(a_full, 0, abort_flag, &s_err_kvbw);
+    for (int n = 0; n < N && alive; ++n) {
+      const int slot = n % kWtSlots;
+      alive = mbar_wait(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
+              mbar_wait(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
+      if (!alive) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc_mma_f16_ta(tmem + 128 + 128 * (n & 1), tmem + 8 * k,
+                      smem_desc_sw128(base + slot * SH::TILE + (k >> 2) * SH::PANEL + (k & 3) * 32), id, k > 0);
+      tc_commit(s_full(n & 1));
+      tc_commit(q_empty(slot));
+    }
+    tc_commit(done);
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(done, 0)) {
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        atomicOr(&s_err_kvbw, kErrTimeout);
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int D, bool BF16>
+static tm_status launch(const AttnParams& P, cudaStream_t stream) {
+  using SH = WtShape<D>;
+  static std::atomic<unsigned long long> done{0};
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(weights_kernel<FMT, D, BF16>), SH::SMEM)) return TM_ERR_CUDA;
+  const dim3 grid((unsigned)(P.V.B * P.V.Hkv), (unsigned)((P.w_stride + kWtTile - 1) / kWtTile));
+  weights_kernel<FMT, D, BF16><<<grid, kWtThreads, SH::SMEM, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+template <int FMT, int D>
+static tm_status launch(const AttnParams& P, cudaStream_t stream) {
+  return P.bf16 ? launch<FMT, D, true>(P, stream) : launch<FMT, D, false>(P, stream);
+}
+
+tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream) {
+  if (format == TM_KVB_INT8) return D == 64 ? launch<TM_KVB_INT8, 64>(P, stream) : launch<TM_KVB_INT8, 128>(P, stream);
+  return D == 64 ? launch<TM_KVB_E4M3, 64>(P, stream) : launch<TM_KVB_E4M3, 128>(P, stream);
+}
+
+}  // namespace kvb
+
+cudaError_t kvb_weights_error_bits(uint32_t* bits, bool clear) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, kvb::s_err_kvbw, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (clear && v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(kvb::s_err_kvbw, &zero, sizeof(zero));
+  }
+  *bits = v;
+  return e;
+}
+
+}  // namespace w4
