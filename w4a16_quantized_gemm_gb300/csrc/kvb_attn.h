@@ -33,6 +33,14 @@ tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs,
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream);
 
 #if defined(__CUDACC__)
+// mbar_wait with a spin before the timer comes in.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, err);
+}
+
 // Tensor memory: 32 lanes x 32 consecutive 32-bit columns, thread i to lane (base lane + i).
 __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(

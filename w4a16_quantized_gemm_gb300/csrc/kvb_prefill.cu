@@ -41,7 +41,7 @@ struct PreShape {
   static constexpr uint32_t TILE = PANELS * PANEL;
   static constexpr uint32_t Q_OFF = 0;
   static constexpr uint32_t KV_OFF = 2 * TILE;
-  static constexpr uint32_t META = KV_OFF + kPreSlots * TILE;  // [kPreMeta][8] x {ks, lv, 1 / vs, page}
+  static constexpr uint32_t META = KV_OFF + kPreSlots * TILE;  // [kPreMeta][8] x {ks, lv, 1 / vs, group}
   static constexpr uint32_t HOLES = META + kPreMeta * 8 * 16;  // [kPreMeta] bits of the 16-token groups
   static constexpr uint32_t BARS = HOLES + 16;
   static constexpr uint32_t SMEM = BARS + 256 + 1024;
@@ -54,6 +54,18 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t panel)
          (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
 
+// 16 bytes, or zeros.
+__device__ __forceinline__ uint4 ldg_or_zero(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)ok));
+  return v;
+}
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -174,8 +186,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       for (int n = 0; n < N; ++n) {
         const int slot = n % kPreMeta;
         const uint32_t ph = (uint32_t)(n / kPreMeta) & 1u;
-        alive = mbar_wait(meta_full(slot), ph, abort_flag, &s_err_kvb) &&
-                mbar_wait(s_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
+        alive = wait_bar(meta_full(slot), ph, abort_flag, &s_err_kvb) &&
+                wait_bar(s_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
         if (!__all_sync(0xffffffffu, alive)) {
           alive = false;
           break;
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       }
       // ---- the row's output, or its state for the joining launch
       if (N > 0 && alive) {
-        alive = mbar_wait(o_full, 0, abort_flag, &s_err_kvb);
+        alive = wait_bar(o_full, 0, abort_flag, &s_err_kvb);
         alive = __all_sync(0xffffffffu, alive);
         tc_fence_after();
       }
@@ -306,19 +318,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     const int code_off = panel * 64 + c4 * 16;
     const int items = 2 * N;  // K_0, V_0, K_1, V_1, ...
     uint4 x[PASSES];
+    int grp[PASSES];  // 16-token groups of the pool that the thread's rows of the tile lie in
+    auto groups = [&](int n) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        grp[p] = (int)lds32(base + SH::META + (n % kPreMeta) * 128 + ((r0 + p * RPP) >> 4) * 16 + 12);
+    };
     auto fetch = [&](int item, int p) {
-      const int n = item >> 1, r = r0 + p * RPP, j = j0 + n * kPreTile + r;
-      const int page = (int)lds32(base + SH::META + (n % kPreMeta) * 128 + (r >> 4) * 16 + 12);
-      x[p] = make_uint4(0u, 0u, 0u, 0u);
-      if (page >= 0 && j < j1)
-        x[p] = *reinterpret_cast<const uint4*>((item & 1 ? V.v : V.k) +
-                                               ((((size_t)page * V.Hkv + h) << V.t_shift) + (j & ((1 << V.t_shift) - 1))) * D +
-                                               code_off);
+      // Rows past the end read as zeros: stale codes may be NaN.
+      const int r = r0 + p * RPP;
+      const uint8_t* src = (item & 1 ? V.v : V.k) + (size_t)(unsigned)max(grp[p], 0) * (16 * D) + (r & 15) * D + code_off;
+      x[p] = ldg_or_zero(src, grp[p] >= 0 && j0 + (item >> 1) * kPreTile + r < j1);
     };
     bool alive = true;
     if (items) {
-      alive = mbar_wait(meta_full(0), 0, abort_flag, &s_err_kvb);
+      alive = wait_bar(meta_full(0), 0, abort_flag, &s_err_kvb);
       if (__all_sync(0xffffffffu, alive)) {
+        groups(0);
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) fetch(0, p);
       } else {
@@ -327,15 +343,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     }
     for (int item = 0; item < items && alive; ++item) {
       const int slot = item % kPreSlots;
-      alive = mbar_wait(kv_empty(slot), ((uint32_t)(item / kPreSlots) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+      alive = wait_bar(kv_empty(slot), ((uint32_t)(item / kPreSlots) & 1u) ^ 1u, abort_flag, &s_err_kvb);
       const bool more = item + 1 < items;
       if (more && !((item + 1) & 1))
-        alive = alive && mbar_wait(meta_full(((item + 1) >> 1) % kPreMeta), (uint32_t)(((item + 1) >> 1) / kPreMeta) & 1u,
+        alive = alive && wait_bar(meta_full(((item + 1) >> 1) % kPreMeta), (uint32_t)(((item + 1) >> 1) / kPreMeta) & 1u,
                                    abort_flag, &s_err_kvb);
       if (!__all_sync(0xffffffffu, alive)) {
         alive = false;
         break;
       }
+      if (more && (item & 1)) groups((item + 1) >> 1);
       const uint32_t dst = base + SH::KV_OFF + slot * SH::TILE + panel * SH::PANEL;
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(kv_full(slot));
-        // The pages of tile n were last read when V_n was fetched, during K_n's turn.
+        // Tile n's groups were read into registers before K_n was fetched.
         if (!(item & 1)) mbar_arrive(meta_empty((item >> 1) % kPreMeta));
       }
     }
@@ -365,7 +382,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       if (lane == 0 && N > 0) {
         constexpr uint32_t id_s = idesc_f16_f32(128, 128);
         constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
-        bool alive = mbar_wait(q_full, 0, abort_flag, &s_err_kvb);
+        bool alive = wait_bar(q_full, 0, abort_flag, &s_err_kvb);
         auto slot_of = [&](int item) { return base + SH::KV_OFF + (item % kPreSlots) * SH::TILE; };
         auto scores = [&](int i, int n) {
           const uint32_t kt = slot_of(2 * n), qt = base + SH::Q_OFF + i * SH::TILE;
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           tc_commit(s_full(i));
         };
         auto wait_kv = [&](int item) {
-          return mbar_wait(kv_full(item % kPreSlots), (uint32_t)(item / kPreSlots) & 1u, abort_flag, &s_err_kvb);
+          return wait_bar(kv_full(item % kPreSlots), (uint32_t)(item / kPreSlots) & 1u, abort_flag, &s_err_kvb);
         };
         alive = alive && wait_kv(0);
         if (alive) {
@@ -389,7 +406,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           alive = wait_kv(2 * n + 1);
           const uint64_t dv = smem_desc_mn(slot_of(2 * n + 1), SH::PANEL);
           for (int i = 0; i < M && alive; ++i) {
-            alive = mbar_wait(p_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
+            alive = wait_bar(p_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
             if (!alive) break;
             tc_fence_after();
 #pragma unroll
@@ -423,7 +440,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       for (int n = 0; n < N; ++n) {
         const int slot = n % kPreMeta;
         const bool alive =
-            mbar_wait(meta_empty(slot), ((uint32_t)(n / kPreMeta) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+            wait_bar(meta_empty(slot), ((uint32_t)(n / kPreMeta) & 1u) ^ 1u, abort_flag, &s_err_kvb);
         if (!__all_sync(0xffffffffu, alive)) break;
         const int j = j0 + n * kPreTile + 16 * lane;
         bool hole = false;
@@ -431,14 +448,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
           hole = j < j1 && page < 0;
           float ks = 1.f, vs = 1.f;
+          uint32_t group = 0xffffffffu;
           if (page >= 0) {
             const size_t cell = (size_t)page * V.Hkv + h;
+            group = (uint32_t)(((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) >> 4);
             ks = V.ks[cell];
             vs = fmaxf(V.vs[cell], kScaleFloor);
           }
           const float lv = __log2f(vs);
           sts128(base + SH::META + slot * 128 + lane * 16, __float_as_uint(ks), __float_as_uint(lv),
-                 __float_as_uint(ex2(-lv)), (uint32_t)page);
+                 __float_as_uint(ex2(-lv)), group);
         }
         const uint32_t holes = __ballot_sync(0xffffffffu, hole);
         if (lane == 0)

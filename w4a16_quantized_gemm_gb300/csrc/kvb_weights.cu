@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     float sum = 0.f, lost = 0.f;
     for (int n = 0; n < N; ++n) {
       const int slot = n % kWtSlots;
-      bool alive = mbar_wait(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
-                   mbar_wait(s_full(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag, &s_err_kvbw);
+      bool alive = wait_bar(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
+                   wait_bar(s_full(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag, &s_err_kvbw);
       if (!__all_sync(0xffffffffu, alive)) break;
       tc_fence_after();
       uint32_t v[2][32];
@@ -172,32 +172,45 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     constexpr int CPR = D / 8;  // 16-byte chunks per row
     constexpr int RPP = 128 / CPR;
     const int c = t % CPR, rr = t / CPR;
+    // A thread's rows are RPP apart: (query, head) and its address move by constants, with a carry.
+    const int G = P.G, dq = RPP / G, dg = RPP - dq * G;
+    const long long step = dq * P.q_stride + (long long)dg * D, carry = P.q_stride - (long long)G * D;
+    int row = r0 + rr, g = row % G;
+    const uint16_t* src = P.Q + (long long)(s.row0 + row / G) * P.q_stride + (long long)(h * G + g) * D + 8 * c;
+    int lrow = r0 + t, li = lrow / G, lg = lrow - li * G;  // the row whose lse the thread fetches
+    const int ldq = kWtTile / G, ldg = kWtTile - ldq * G;
     bool alive = true;
     auto issue = [&](int n) {
       if (n < N) {
         const int slot = n % kWtSlots;
-        alive = alive && mbar_wait(q_empty(slot), ((uint32_t)(n / kWtSlots) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
+        const float x = lrow < rows ? P.lse[(size_t)(s.row0 + li) * P.Hq + h * G + lg] : -INFINITY;
+        const int last = lrow < rows ? min(s.old + li, s.len - 1) : -1;
+        alive = alive && wait_bar(q_empty(slot), ((uint32_t)(n / kWtSlots) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
         if (alive) {
-          const int row0 = r0 + n * kWtTile;
-#pragma unroll 4
+          const uint32_t dst = base + slot * SH::TILE + (c >> 3) * SH::PANEL;
+#pragma unroll
           for (int p = 0; p < kWtTile / RPP; ++p) {
-            const int q = p * RPP + rr, row = row0 + q;
-            const bool ok = row < rows;
-            const int i = ok ? row / P.G : 0, g = ok ? row - i * P.G : 0;
-            cp16(base + slot * SH::TILE + (c >> 3) * SH::PANEL + q * 128 + (((c & 7) ^ (q & 7)) << 4),
-                 P.Q + (s.row0 + i) * P.q_stride + (long long)(h * P.G + g) * D + 8 * c, ok);
+            const int q = p * RPP + rr;
+            cp16(dst + q * 128 + (((c & 7) ^ (q & 7)) << 4), row < rows ? src : P.Q, row < rows);
+            row += RPP;
+            g += dg;
+            src += step;
+            if (g >= G) {
+              g -= G;
+              src += carry;
+            }
           }
-          const int row = row0 + t;
-          float l = INFINITY;
-          int last = -1;
-          if (row < rows) {
-            const int i = row / P.G;
-            const float x = P.lse[(size_t)(s.row0 + i) * P.Hq + h * P.G + (row - i * P.G)];
-            if (x != -INFINITY) l = x * 1.44269504088896f;
-            last = min(s.old + i, s.len - 1);
-          }
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + SH::ROWS + slot * 512 + 4 * t), "f"(l) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + SH::ROWS + slot * 512 + 4 * t),
+                       "f"(x != -INFINITY ? x * 1.44269504088896f : INFINITY)
+                       : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::LAST + slot * 512 + 4 * t), "r"(last) : "memory");
+        }
+        lrow += kWtTile;
+        li += ldq;
+        lg += ldg;
+        if (lg >= G) {
+          lg -= G;
+          ++li;
         }
       }
       cp_commit();
@@ -216,11 +229,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   } else if (lane == 0) {
     // ---------------- products ----------------
     constexpr uint32_t id = idesc_f16_f32(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
-    bool alive = mbar_wait(a_full, 0, abort_flag, &s_err_kvbw);
+    bool alive = wait_bar(a_full, 0, abort_flag, &s_err_kvbw);
     for (int n = 0; n < N && alive; ++n) {
       const int slot = n % kWtSlots;
-      alive = mbar_wait(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
-              mbar_wait(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
+      alive = wait_bar(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
+              wait_bar(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
       if (!alive) break;
       tc_fence_after();
 #pragma unroll
