@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
 
   if (warp < 8) {
     // ---------------- softmax: one row per thread ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = row_base + i * kPreTile + r;
@@ -376,43 +376,56 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 12) {
       // ---------------- MMA issuer ----------------
-      if (lane == 0 && N > 0) {
+      // The whole warp walks the loop, so that descriptors and addresses stay uniform; one lane issues.
+      if (N > 0) {
         constexpr uint32_t id_s = idesc_f16_f32(128, 128);
         constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
-        bool alive = wait_bar(q_full, 0, abort_flag, &s_err_kvb);
-        auto slot_of = [&](int item) { return base + SH::KV_OFF + (item % kPreSlots) * SH::TILE; };
-        auto scores = [&](int i, int n) {
-          const uint32_t kt = slot_of(2 * n), qt = base + SH::Q_OFF + i * SH::TILE;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * SH::PANEL + (k & 3) * 32;
-            tc_mma_f16(tmem + 128 * i, smem_desc_sw128(qt + off), smem_desc_sw128(kt + off), id_s, k > 0);
-          }
-          tc_commit(s_full(i));
+        constexpr uint64_t kTileDesc = SH::TILE >> 4, kPanelDesc = SH::PANEL >> 4;
+        const uint64_t dq = smem_desc_sw128(base + SH::Q_OFF), dk = smem_desc_sw128(base + SH::KV_OFF);
+        const uint64_t dv = smem_desc_mn(base + SH::KV_OFF, SH::PANEL);
+        const bool leader = elect_one();
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+          return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvb)) != 0;
         };
         auto wait_kv = [&](int item) {
-          return wait_bar(kv_full(item % kPreSlots), (uint32_t)(item / kPreSlots) & 1u, abort_flag, &s_err_kvb);
+          return wait_all(kv_full(item % kPreSlots), (uint32_t)(item / kPreSlots) & 1u);
         };
-        alive = alive && wait_kv(0);
+        auto scores = [&](int i, int n) {
+          const uint64_t da = dq + i * kTileDesc, db = dk + (uint64_t)((2 * n) % kPreSlots) * kTileDesc;
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = (k >> 2) * kPanelDesc + (k & 3) * 2;
+              tc_mma_f16(tmem + 128 * i, da + off, db + off, id_s, k > 0);
+            }
+            tc_commit(s_full(i));
+          }
+          __syncwarp();
+        };
+        bool alive = wait_all(q_full, 0) && wait_kv(0);
         if (alive) {
           tc_fence_after();
           for (int i = 0; i < M; ++i) scores(i, 0);
-          tc_commit(kv_empty(0));
+          if (leader) tc_commit(kv_empty(0));
+          __syncwarp();
         }
         for (int n = 0; n < N && alive; ++n) {
           alive = wait_kv(2 * n + 1);
-          const uint64_t dv = smem_desc_mn(slot_of(2 * n + 1), SH::PANEL);
+          const uint64_t db = dv + (uint64_t)((2 * n + 1) % kPreSlots) * kTileDesc;
           for (int i = 0; i < M && alive; ++i) {
-            alive = wait_bar(p_full(i), (uint32_t)n & 1u, abort_flag, &s_err_kvb);
+            alive = wait_all(p_full(i), (uint32_t)n & 1u);
             if (!alive) break;
             tc_fence_after();
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < kPreTile / 16; ++k)
-              tc_mma_f16_ta(tmem + 256 + D * i, tmem + 128 * i + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), id_o,
-                            n > 0 || k > 0);
+              for (int k = 0; k < kPreTile / 16; ++k)
+                tc_mma_f16_ta(tmem + 256 + D * i, tmem + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
+                              n > 0 || k > 0);
+            }
+            __syncwarp();
             if (n + 1 < N) {
               if (i == 0) alive = wait_kv(2 * n + 2);
               if (!alive) break;
@@ -421,16 +434,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
             }
           }
           if (!alive) break;
-          tc_commit(kv_empty((2 * n + 1) % kPreSlots));
-          if (n + 1 < N) tc_commit(kv_empty((2 * n + 2) % kPreSlots));
+          if (leader) {
+            tc_commit(kv_empty((2 * n + 1) % kPreSlots));
+            if (n + 1 < N) tc_commit(kv_empty((2 * n + 2) % kPreSlots));
+          }
+          __syncwarp();
         }
-        tc_commit(o_full);
-        // Nothing is left in flight when tensor memory is freed, on an abort either.
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(o_full, 0)) {
-          if (globaltimer() - t0 > kWaitLimitNs) {
-            atomicOr(&s_err_kvb, kErrTimeout);
-            break;
+        if (leader) {
+          tc_commit(o_full);
+          // Nothing is left in flight when tensor memory is freed, on an abort either.
+          const unsigned long long t0 = globaltimer();
+          while (!mbar_try_wait(o_full, 0)) {
+            if (globaltimer() - t0 > kWaitLimitNs) {
+              atomicOr(&s_err_kvb, kErrTimeout);
+              break;
+            }
           }
         }
       }
