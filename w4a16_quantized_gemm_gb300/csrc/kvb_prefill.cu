@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
   const View& V = P.V;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
   const int chunk = blockIdx.y % P.chunks;
   const int pair = (int)(gridDim.y / P.chunks) - 1 - blockIdx.y / P.chunks;  // the longest rows first
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
         constexpr uint64_t kTileDesc = SH::TILE >> 4, kPanelDesc = SH::PANEL >> 4;
         const uint64_t dq = smem_desc_sw128(base + SH::Q_OFF), dk = smem_desc_sw128(base + SH::KV_OFF);
         const uint64_t dv = smem_desc_mn(base + SH::KV_OFF, SH::PANEL);
-        const bool leader = elect_one();
+        const uint32_t lead = elect_one();
+        const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);  // known to be uniform
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
           return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvb)) != 0;
         };
@@ -395,22 +396,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
         };
         auto scores = [&](int i, int n) {
           const uint64_t da = dq + i * kTileDesc, db = dk + (uint64_t)((2 * n) % kPreSlots) * kTileDesc;
-          if (leader) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = (k >> 2) * kPanelDesc + (k & 3) * 2;
-              tc_mma_f16(tmem + 128 * i, da + off, db + off, id_s, k > 0);
-            }
-            tc_commit(s_full(i));
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (k >> 2) * kPanelDesc + (k & 3) * 2;
+            mma_ss_if(lead, tm0 + 128 * i, da + off, db + off, id_s, k > 0);
           }
-          __syncwarp();
+          commit_if(lead, s_full(i));
         };
         bool alive = wait_all(q_full, 0) && wait_kv(0);
         if (alive) {
           tc_fence_after();
           for (int i = 0; i < M; ++i) scores(i, 0);
-          if (leader) tc_commit(kv_empty(0));
-          __syncwarp();
+          commit_if(lead, kv_empty(0));
         }
         for (int n = 0; n < N && alive; ++n) {
           alive = wait_kv(2 * n + 1);
@@ -419,13 +416,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
             alive = wait_all(p_full(i), (uint32_t)n & 1u);
             if (!alive) break;
             tc_fence_after();
-            if (leader) {
 #pragma unroll
-              for (int k = 0; k < kPreTile / 16; ++k)
-                tc_mma_f16_ta(tmem + 256 + D * i, tmem + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
-                              n > 0 || k > 0);
-            }
-            __syncwarp();
+            for (int k = 0; k < kPreTile / 16; ++k)
+              mma_ts_if(lead, tm0 + 256 + D * i, tm0 + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
+                        n > 0 || k > 0);
             if (n + 1 < N) {
               if (i == 0) alive = wait_kv(2 * n + 2);
               if (!alive) break;
@@ -434,14 +428,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
             }
           }
           if (!alive) break;
-          if (leader) {
-            tc_commit(kv_empty((2 * n + 1) % kPreSlots));
-            if (n + 1 < N) tc_commit(kv_empty((2 * n + 2) % kPreSlots));
-          }
-          __syncwarp();
+          commit_if(lead, kv_empty((2 * n + 1) % kPreSlots));
+          if (n + 1 < N) commit_if(lead, kv_empty((2 * n + 2) % kPreSlots));
         }
-        if (leader) {
-          tc_commit(o_full);
+        commit_if(lead, o_full);
+        if (lead) {
           // Nothing is left in flight when tensor memory is freed, on an abort either.
           const unsigned long long t0 = globaltimer();
           while (!mbar_try_wait(o_full, 0)) {
