@@ -97,19 +97,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
   const uint32_t bars = base + SH::BARS;
   const uint32_t q_full = bars;
   auto s_full = [&](int i) { return bars + 8 + 8 * i; };
-  auto p_full = [&](int i) { return bars + 24 + 8 * i; };
-  const uint32_t o_full = bars + 40;
-  auto kv_full = [&](int i) { return bars + 48 + 8 * i; };
-  auto kv_empty = [&](int i) { return bars + 80 + 8 * i; };
-  auto meta_full = [&](int i) { return bars + 112 + 8 * i; };
-  auto meta_empty = [&](int i) { return bars + 144 + 8 * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 176);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 180);
+  auto p_full = [&](int i, int half) { return bars + 24 + 16 * i + 8 * half; };
+  const uint32_t o_full = bars + 56;
+  auto kv_full = [&](int i) { return bars + 64 + 8 * i; };
+  auto kv_empty = [&](int i) { return bars + 96 + 8 * i; };
+  auto meta_full = [&](int i) { return bars + 128 + 8 * i; };
+  auto meta_empty = [&](int i) { return bars + 160 + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 192);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 196);
   if (tid == 0) {
     mbar_init(q_full, 4 * M);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
+      mbar_init(p_full(i, 0), 4);
+      mbar_init(p_full(i, 1), 4);
     }
     mbar_init(o_full, 1);
     for (int i = 0; i < kPreSlots; ++i) {
@@ -209,9 +210,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const float4 mt = lds_f4(meta + 16 * g);
-          float a = __uint_as_float(v[g >> 1][16 * (g & 1)]);
+          auto val = [&](int c) { return __uint_as_float(v[g >> 1][16 * (g & 1) + c]); };
+          float a = max3(val(0), val(1), val(2)), a2 = max3(val(3), val(4), val(5));
 #pragma unroll
-          for (int c = 1; c < 16; ++c) a = fmaxf(a, __uint_as_float(v[g >> 1][16 * (g & 1) + c]));
+          for (int c = 6; c < 14; c += 4) {
+            a = max3(a, val(c), val(c + 1));
+            a2 = max3(a2, val(c + 2), val(c + 3));
+          }
+          a = max3(a, a2, fmaxf(val(14), val(15)));
           tm = fmaxf(tm, fmaf(a, fmaxf(mt.x * mul, 1e-35f), mt.y));
         }
         if (__any_sync(0xffffffffu, tm > m + kPreSlack)) {
@@ -238,25 +244,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
             const int g = 4 * half + k;
             const float4 mt = lds_f4(meta + 16 * g);
             const float cg = fmaxf(mt.x * mul, 1e-35f), off = mt.y + kPreBias - m;
-            float sum = 0.f;
+            const uint64_t cg2 = f32x2(cg, cg), off2 = f32x2(off, off);
+            uint64_t sum = 0ull;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              const float p0 = ex2(fmaf(__uint_as_float(v[g >> 1][16 * (g & 1) + c]), cg, off));
-              const float p1 = ex2(fmaf(__uint_as_float(v[g >> 1][16 * (g & 1) + c + 1]), cg, off));
-              sum += p0 + p1;
+              const float2 e = f32x2_get(fma_f32x2(f32x2(__uint_as_float(v[g >> 1][16 * (g & 1) + c]),
+                                                         __uint_as_float(v[g >> 1][16 * (g & 1) + c + 1])),
+                                                   cg2, off2));
+              const float p0 = ex2(e.x), p1 = ex2(e.y);
+              sum = add_f32x2(sum, f32x2(p0, p1));
               p[8 * k + c / 2] = pack_half2(p0, p1);
             }
-            l = fmaf(sum, mt.z, l);
+            const float2 part = f32x2_get(sum);
+            l = fmaf(part.x + part.y, mt.z, l);
           }
+          // The first half of the weights goes to the tensor cores while the second is computed.
           tc_st_32x32b_x32(ts + 32 * half, p);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(i, half));
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(p_full(i));
-          mbar_arrive(meta_empty(slot));
-        }
+        if (lane == 0) mbar_arrive(meta_empty(slot));
       }
       // ---- the row's output, or its state for the joining launch
       if (N > 0 && alive) {
@@ -413,13 +422,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           alive = wait_kv(2 * n + 1);
           const uint64_t db = dv + (uint64_t)((2 * n + 1) % kPreSlots) * kTileDesc;
           for (int i = 0; i < M && alive; ++i) {
-            alive = wait_all(p_full(i), (uint32_t)n & 1u);
-            if (!alive) break;
-            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kPreTile / 16; ++k)
-              mma_ts_if(lead, tm0 + 256 + D * i, tm0 + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
-                        n > 0 || k > 0);
+            for (int half = 0; half < 2; ++half) {
+              alive = alive && wait_all(p_full(i, half), (uint32_t)n & 1u);
+              if (!alive) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                mma_ts_if(lead, tm0 + 256 + D * i, tm0 + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
+                          n > 0 || k > 0);
+            }
+            if (!alive) break;
             if (n + 1 < N) {
               if (i == 0) alive = wait_kv(2 * n + 2);
               if (!alive) break;
