@@ -3,7 +3,7 @@
 //
 // One CTA per (page that new tokens fall into, head, K or V): the new values
 // are read once and stay in registers (at most T D = 16384 of them, 64 per
-// thread) across the maximum and the rounding.  A page that already holds
+// thread) across the maximum, taken on their bit patterns, and the rounding.  A page that already holds
 // tokens keeps the larger of its scale and the one that the new tokens need;
 // where it grows, the earlier codes are rounded anew (each page sees that a few
 // times while it fills: the maximum of a growing set rises ever more rarely).
@@ -13,7 +13,6 @@ namespace w4 {
 namespace kvb {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendVecs = 8;  // vectors of 8 values per thread: 256 x 8 x 8 = 128 tokens x 128
 
 struct AppendParams {
   View V;
@@ -29,10 +28,15 @@ struct AppendParams {
 __device__ __forceinline__ float finite(float x, float top) {
   return x != x ? 0.f : fminf(fmaxf(x, -top), top);
 }
+__device__ __forceinline__ uint64_t values(uint32_t w, int bf16, bool clean, float top) {
+  const float2 f = unpack(w, bf16);
+  return clean ? f32x2(f.x, f.y) : f32x2(finite(f.x, top), finite(f.y, top));
+}
 
-template <int FMT>
+// VECS: vectors of 8 values per thread, enough for the new tokens of one page.
+template <int FMT, int VECS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
-  __shared__ float warp_max[kAppendThreads / 32];
+  __shared__ uint32_t warp_max[kAppendThreads / 32];
   const View& V = P.V;
   const int b = blockIdx.z, h = blockIdx.y, sel = blockIdx.x & 1, tid = threadIdx.x;
   const Span s = span(V, b);
@@ -53,72 +57,94 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int total = (hi - lo) << vec_shift;
   const uint16_t* src = P.x[sel] + (s.row0 + (long long)(lo - s.old)) * P.stride[sel] + ((long long)h << P.d_shift);
   const float top = P.bf16 ? 3.3895313892515355e38f : 65504.f;
-  uint4 x[kAppendVecs];
-  float a = 0.f;
+  uint4 x[VECS];
 #pragma unroll
-  for (int i = 0; i < kAppendVecs; ++i) {
+  for (int i = 0; i < VECS; ++i) {
     const int v = tid + i * kAppendThreads;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (v < total)
       x[i] = *reinterpret_cast<const uint4*>(src + (v >> vec_shift) * P.stride[sel] +
                                              ((v & ((1 << vec_shift) - 1)) << 3));
   }
+  // The largest magnitude as a bit pattern: those of 16-bit floats are ordered, and the pattern
+  // of an infinity or NaN tells whether any value needs cleaning.
+  uint32_t m2 = 0u;
 #pragma unroll
-  for (int i = 0; i < kAppendVecs; ++i) {
-    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack(wd[k], P.bf16);
-      a = fmaxf(a, fmaxf(fabsf(finite(f.x, top)), fabsf(finite(f.y, top))));
-    }
+  for (int i = 0; i < VECS; ++i) {
+    m2 = __vmaxu2(m2, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+    m2 = __vmaxu2(m2, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  if ((tid & 31) == 0) warp_max[tid >> 5] = a;
+  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
   const size_t cell = (size_t)page * V.Hkv + h;
   float* scale = (sel ? V.vs : V.ks) + cell;
   const bool continued = s.old > begin;
   const float was = continued ? *scale : 0.f;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) a = fmaxf(a, warp_max[i]);
+  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
+  const bool clean = m < (P.bf16 ? 0x7f80u : 0x7c00u);
+  float a = unpack(m, P.bf16).x;
+  if (!clean) {  // uniform: the largest finite magnitude, an infinity counting as `top`
+    float f = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = f32x2_get(values(wd[k], P.bf16, false, top));
+        f = fmaxf(f, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+    }
+    m = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
+    __syncthreads();
+    if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
+    a = __uint_as_float(m);
+  }
   const float now = fmaxf(scale_for<FMT>(a), was);
+  const Divisor by = divisor(now);
   if (tid == 0) *scale = now;
 
   uint8_t* codes = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);
   uint8_t* dst = codes + ((size_t)(lo - begin) << P.d_shift);
 #pragma unroll
-  for (int i = 0; i < kAppendVecs; ++i) {
+  for (int i = 0; i < VECS; ++i) {
     const int v = tid + i * kAppendThreads;
     if (v >= total) break;
-    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t c[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack(wd[k], P.bf16);
-      c[k >> 1] |= (encode<FMT>(__fdiv_rn(finite(f.x, top), now)) |
-                    encode<FMT>(__fdiv_rn(finite(f.y, top), now)) << 8)
-                   << (16 * (k & 1));
-    }
-    *reinterpret_cast<uint2*>(dst + ((size_t)v << 3)) = make_uint2(c[0], c[1]);
+    uint2 c;
+    c.x = encode4<FMT>(values(x[i].x, P.bf16, clean, top), values(x[i].y, P.bf16, clean, top), by);
+    c.y = encode4<FMT>(values(x[i].z, P.bf16, clean, top), values(x[i].w, P.bf16, clean, top), by);
+    *reinterpret_cast<uint2*>(dst + ((size_t)v << 3)) = c;
   }
   if (continued && now > was) {
     const int earlier = (lo - begin) << vec_shift;
+    const uint64_t was2 = f32x2(was, was);
     for (int v = tid; v < earlier; v += kAppendThreads) {
       uint2* at = reinterpret_cast<uint2*>(codes + ((size_t)v << 3));
-      const uint2 c = *at;
-      uint32_t wd[2] = {c.x, c.y};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t r = 0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          r |= encode<FMT>(__fdiv_rn(__fmul_rn(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu), was), now)) << (8 * e);
-        wd[k] = r;
-      }
-      *at = make_uint2(wd[0], wd[1]);
+      uint2 c = *at;
+      uint64_t lo, hi;
+      decode4<FMT>(c.x, lo, hi);
+      c.x = encode4<FMT>(mul_f32x2(lo, was2), mul_f32x2(hi, was2), by);
+      decode4<FMT>(c.y, lo, hi);
+      c.y = encode4<FMT>(mul_f32x2(lo, was2), mul_f32x2(hi, was2), by);
+      *at = c;
     }
   }
+}
+
+template <int FMT>
+void launch_append(const AppendParams& P, dim3 grid, int vecs, cudaStream_t s) {
+  if (vecs <= 1)
+    append_kernel<FMT, 1><<<grid, kAppendThreads, 0, s>>>(P);
+  else if (vecs <= 2)
+    append_kernel<FMT, 2><<<grid, kAppendThreads, 0, s>>>(P);
+  else if (vecs <= 4)
+    append_kernel<FMT, 4><<<grid, kAppendThreads, 0, s>>>(P);
+  else
+    append_kernel<FMT, 8><<<grid, kAppendThreads, 0, s>>>(P);
 }
 
 }  // namespace kvb
@@ -152,10 +178,11 @@ extern "C" tm_status tm_kvb_append(const tm_kvb_cache* cache, const tm_kvb_batch
   const long long pages = ((long long)V.max_q + cache->T - 2) / cache->T + 1;
   const dim3 grid((unsigned)(2 * pages), (unsigned)V.Hkv, (unsigned)V.B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int vecs = ((cache->T < V.max_q ? cache->T : V.max_q) * cache->D / 8 + kAppendThreads - 1) / kAppendThreads;
   if (cache->format == TM_KVB_INT8)
-    append_kernel<TM_KVB_INT8><<<grid, kAppendThreads, 0, s>>>(P);
+    launch_append<TM_KVB_INT8>(P, grid, vecs, s);
   else
-    append_kernel<TM_KVB_E4M3><<<grid, kAppendThreads, 0, s>>>(P);
+    launch_append<TM_KVB_E4M3>(P, grid, vecs, s);
   if (cudaGetLastError() != cudaSuccess) return TM_ERR_CUDA;
   set_launch_count(1);
   return TM_OK;

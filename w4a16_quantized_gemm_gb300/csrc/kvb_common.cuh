@@ -115,18 +115,79 @@ __device__ __forceinline__ void codes_half_pairs(uint32_t a, uint32_t b, uint32_
   codes_half<FMT>(prmt(a, b, 0x7362u), out[2], out[3]);
 }
 
-// Code of y: to nearest, ties to even, saturating.
-template <int FMT>
-__device__ __forceinline__ uint32_t encode(float y) {
-  if (FMT == TM_KVB_INT8) return (uint32_t)(int)fminf(fmaxf(rintf(y), -127.f), 127.f) & 0xFFu;
-  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+// Packed pairs of binary32 (one instruction for two).
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
 }
-template <int FMT>
-__device__ __forceinline__ float decode(uint32_t c) {
-  if (FMT == TM_KVB_INT8) return (float)(int)(int8_t)c;
-  const uint32_t h = e4m3x2_half2((uint16_t)c);
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+__device__ __forceinline__ float2 f32x2_get(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
 }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Four codes of a word as binary32, exactly, in two pairs.
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, uint64_t& lo, uint64_t& hi) {
+  uint32_t a, b;
+  codes_half<FMT>(w, a, b);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = f32x2(x.x, x.y);
+  hi = f32x2(y.x, y.y);
+}
+
+// Division by a scale of many values: t = x i with i the rounded reciprocal,
+// then one correction by the remainder x - t s (Markstein's), which gives the
+// rounded quotient that the codes are defined by (the rounding to a code could
+// only see a miss next to a tie, where the remainder decides).
+struct Divisor {
+  uint64_t s, i;
+};
+__device__ __forceinline__ Divisor divisor(float s) {
+  const float i = __frcp_rn(s);
+  return {f32x2(-s, -s), f32x2(i, i)};
+}
+__device__ __forceinline__ uint64_t divide(uint64_t x, const Divisor& d) {
+  const uint64_t t = mul_f32x2(x, d.i);
+  return fma_f32x2(fma_f32x2(t, d.s, x), d.i, t);
+}
+
+// Codes of four quotients x / s with |x| at most the largest code times s (to
+// its rounding): to the nearest, ties to even.  int8: adding 1.5 2^23 leaves the
+// rounded integer in the low byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(uint64_t lo, uint64_t hi, const Divisor& d) {
+  const uint64_t ql = divide(lo, d), qh = divide(hi, d);
+  if (FMT == TM_KVB_INT8) {
+    const uint64_t magic = f32x2(12582912.f, 12582912.f);
+    const float2 a = f32x2_get(add_f32x2(ql, magic)), b = f32x2_get(add_f32x2(qh, magic));
+    return prmt(prmt(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040u),
+                prmt(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040u), 0x5410u);
+  }
+  // the correction loses the sign of a zero
+  const float2 a = f32x2_get(ql), b = f32x2_get(qh), xa = f32x2_get(lo), xb = f32x2_get(hi);
+  const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(copysignf(a.x, xa.x), copysignf(a.y, xa.y)), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(copysignf(b.x, xb.x), copysignf(b.y, xb.y)), __NV_SATFINITE, __NV_E4M3);
+  return l | (h << 16);
+}
+
 // The scale that values up to `a` need: a times the binary32 reciprocal of the
 // largest code, at least 2^-30.
 template <int FMT>

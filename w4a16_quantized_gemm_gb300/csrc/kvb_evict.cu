@@ -20,7 +20,7 @@ namespace kvb {
 
 constexpr int kEvictThreads = 256;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kKeyCap = 16384;  // keys of a CTA's slice held in shared memory (64 KB); the rest are read again
+constexpr int kKeyCap = 16384;  // most keys of a CTA's slice held in shared memory (64 KB); the rest are read again
 
 struct EvictParams {
   View V;
@@ -34,6 +34,7 @@ struct EvictParams {
   int* kept;
   int* new_len;
   int d_shift;
+  int key_cap;  // keys of a slice held in shared memory
 };
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
@@ -50,10 +51,11 @@ __device__ __forceinline__ void cluster_barrier() {
 template <int FMT>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams P) {
   extern __shared__ __align__(16) uint8_t smem[];  // keys, then the warps' tokens
-  __shared__ uint32_t hist[256], total[256];
+  __shared__ uint32_t hist[2][256], total[256];
   __shared__ uint32_t warp_gt[kEvictWarps], warp_eq[kEvictWarps], cta_count[2];
   __shared__ uint32_t found[2];
   __shared__ float row_scale[kEvictWarps][128];
+  __shared__ uint32_t row_at[kEvictWarps][128];
   const View& V = P.V;
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
@@ -78,31 +80,38 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       const uint32_t u = __float_as_uint(x);
       return (u >> 31) ? ~u : (u | 0x80000000u);
     };
-    for (int j = s0 + tid; j < s1 && j - s0 < kKeyCap; j += kEvictThreads) keys[j - s0] = key_of(j);
-    auto key = [&](int j) { return j - s0 < kKeyCap ? keys[j - s0] : key_of(j); };
+    for (int j = s0 + tid; j < s1 && j - s0 < P.key_cap; j += kEvictThreads) keys[j - s0] = key_of(j);
+    auto key = [&](int j) { return j - s0 < P.key_cap ? keys[j - s0] : key_of(j); };
     uint32_t prefix = 0u, mask = 0u, want = (uint32_t)count;
+    hist[0][tid] = hist[1][tid] = 0u;
+    __syncthreads();
     for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[tid] = 0u;
-      __syncthreads();
-      for (int j = s0 + tid; j < s1; j += kEvictThreads) {
-        const uint32_t k = key(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      uint32_t* mine = hist[(shift >> 3) & 1];
+      for (int j = s0 + warp * 32; j < s1; j += kEvictThreads) {
+        const uint32_t k = j + lane < s1 ? key(j + lane) : 0u;
+        const bool in = j + lane < s1 && (k & mask) == prefix;
+        // one addition per distinct digit in the warp: the leading digits are all alike
+        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        if (in && lane == __ffs(peers) - 1) atomicAdd(&mine[digit], (uint32_t)__popc(peers));
       }
       cluster_barrier();
       uint32_t sum = 0u;
-      for (int r = 0; r < C; ++r) sum += ld_cluster(smem_u32(&hist[tid]), r);
+      for (int r = 0; r < C; ++r) sum += ld_cluster(smem_u32(&mine[tid]), r);
       total[tid] = sum;
-      cluster_barrier();
+      // The other histogram was last read, by the whole cluster, before this round's barrier.
+      hist[1 - ((shift >> 3) & 1)][tid] = 0u;
+      __syncthreads();
       if (warp == 0) {
         // lane l holds bins 255 - 8 l .. 248 - 8 l: from the largest keys down
-        uint32_t mine = 0u;
-        for (int i = 0; i < 8; ++i) mine += total[255 - 8 * lane - i];
-        uint32_t upto = mine;
+        uint32_t own = 0u;
+        for (int i = 0; i < 8; ++i) own += total[255 - 8 * lane - i];
+        uint32_t upto = own;
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += v;
         }
-        uint32_t above = upto - mine;
+        uint32_t above = upto - own;
         if (above < want && want <= upto) {
           int bin = 255 - 8 * lane;
           while (above + total[bin] < want) above += total[bin--];
@@ -114,7 +123,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       prefix |= found[0] << shift;
       mask |= 255u << shift;
       want = found[1];
-      __syncthreads();
     }
     // The kept: every key above `prefix`, and the first `want` equal to it.
     const int sub = per / kEvictWarps;
@@ -170,6 +178,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   uint8_t* stage = smem + ((size_t)(warp << V.t_shift) << P.d_shift);
   const uint32_t stage_u = smem_u32(stage);
   float* rs = row_scale[warp];
+  uint32_t* ra = row_at[warp];
   const int units = 2 * ((count + T - 1) >> V.t_shift);
   for (int u0 = 0; u0 < units; u0 += C * kEvictWarps) {
     const int u = u0 + (int)rank * kEvictWarps + warp;
@@ -184,7 +193,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       same = kept[last] == last;
       from = page_of(V, V.table, b, V.table_stride, min(blk, V.table_stride - 1));
       to = page_of(V, P.dst_table, b, P.dst_stride, blk);
-      uint8_t* pool = sel ? V.v : V.k;
       const float* scales = sel ? V.vs : V.ks;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -193,19 +201,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
           const int pos = base + t;
           const int j = pos < count ? kept[pos] : -1;
           const int page = j >= 0 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
-          rs[t] = page >= 0 ? scales[(size_t)page * V.Hkv + h] : 0.f;
+          const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
+          rs[t] = page >= 0 ? scales[cell] : 0.f;
+          // the token's row of the pool (a pool of 2^32 rows of 64 bytes would be 256 GiB)
+          ra[t] = page >= 0 ? (uint32_t)((cell << V.t_shift) + (j & (T - 1))) : 0xffffffffu;
           kw[i] = j >= 0 ? w[j] : 0.f;
         }
       }
+      __syncwarp();
+      const uint8_t* pool = sel ? V.v : V.k;
       for (int c = lane; c < chunks; c += 32) {
-        const int pos = base + (c >> chunk_shift);
-        const int j = pos < count ? kept[pos] : -1;
-        const int page = j >= 0 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
-        const uint8_t* src = pool;
-        if (page >= 0)
-          src += ((((size_t)page * V.Hkv + h) << V.t_shift) + (j & (T - 1))) * D +
-                 ((c & ((1 << chunk_shift) - 1)) << 4);
-        cp16(stage_u + 16 * c, src, page >= 0);
+        const uint32_t at = ra[c >> chunk_shift];
+        const bool there = at != 0xffffffffu;
+        cp16(stage_u + 16 * c, pool + (there ? (size_t)at * D + ((c & ((1 << chunk_shift) - 1)) << 4) : 0), there);
       }
       cp_commit();
       cp_wait<0>();
@@ -217,28 +225,30 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         for (int c = lane; c < chunks; c += 32) {
           const uint4 q = *reinterpret_cast<const uint4*>(stage + 16 * c);
           const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
-          float m = 0.f;
+          __half2 m = __float2half2_rn(0.f);  // the codes are exact in fp16
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu)));
-          a = fmaxf(a, __fmul_rn(m, rs[c >> chunk_shift]));
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x, y;
+            codes_half<FMT>(wd[k], x, y);
+            m = __hmax2(m, __hmax2(__habs2(*reinterpret_cast<__half2*>(&x)), __habs2(*reinterpret_cast<__half2*>(&y))));
+          }
+          a = fmaxf(a, __fmul_rn(fmaxf(__low2float(m), __high2float(m)), rs[c >> chunk_shift]));
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         now = scale_for<FMT>(a);
+        const Divisor by = divisor(now);
         for (int c = lane; c < chunks; c += 32) {
           uint4* at = reinterpret_cast<uint4*>(stage + 16 * c);
           const uint4 q = *at;
           uint32_t wd[4] = {q.x, q.y, q.z, q.w};
           const float s = rs[c >> chunk_shift];
+          const uint64_t s2 = f32x2(s, s);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t r = 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              r |= encode<FMT>(__fdiv_rn(__fmul_rn(decode<FMT>((wd[k] >> (8 * e)) & 0xFFu), s), now)) << (8 * e);
-            wd[k] = r;
+            uint64_t lo, hi;
+            decode4<FMT>(wd[k], lo, hi);
+            wd[k] = encode4<FMT>(mul_f32x2(lo, s2), mul_f32x2(hi, s2), by);
           }
           *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
         }
@@ -270,17 +280,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
 }
 
 template <int FMT>
-tm_status launch_evict(const EvictParams& P, cudaStream_t stream) {
+tm_status launch_evict(EvictParams P, cudaStream_t stream) {
   const View& V = P.V;
-  const size_t stage = ((size_t)kEvictWarps << V.t_shift) << P.d_shift;
-  const size_t smem = stage > kKeyCap * 4 ? stage : (size_t)kKeyCap * 4;
   static std::atomic<unsigned long long> done{0};
   if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), 8 * 128 * 128)) return TM_ERR_CUDA;
+  // CTAs per cluster: as many as the pages or the keys can use, while all clusters fit the GPU at once.
+  const long long T = 1ll << V.t_shift, heads = (long long)V.B * V.Hkv;
+  const long long units = 2 * ((P.budget + T - 1) / T), room = 4ll * num_sms(current_device());
+  unsigned C = 1;
+  while (C < 8 && heads * 2 * C <= room && (units > C * kEvictWarps || V.max_len > (long long)C * 4096)) C *= 2;
+  const long long slice = (V.max_len + C - 1) / C + kEvictThreads;
+  P.key_cap = (int)(slice < kKeyCap ? slice : kKeyCap);
+  const size_t stage = ((size_t)kEvictWarps << V.t_shift) << P.d_shift, keys = (size_t)P.key_cap * 4;
   cudaLaunchConfig_t cfg = {};
-  const unsigned C = 8;
   cfg.gridDim = dim3(C, (unsigned)V.Hkv, (unsigned)V.B);
   cfg.blockDim = dim3(kEvictThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = stage > keys ? stage : keys;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
