@@ -18,8 +18,12 @@
 namespace w4 {
 namespace kvb {
 
-constexpr int kEvictThreads = 256;
+constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kStage = 131072;   // most bytes of tokens staged per CTA: a warp per page of up to 8 KB, 8 warps above
+constexpr int kLocalKeys = 8192;  // sequences up to this long: every CTA of the cluster selects for itself, which costs
+                                  // less than the cluster barriers of a shared selection
+constexpr int kMaxCluster = 8;
 constexpr int kKeyCap = 16384;  // most keys of a CTA's slice held in shared memory (64 KB); the rest are read again
 
 struct EvictParams {
@@ -34,6 +38,8 @@ struct EvictParams {
   int* kept;
   int* new_len;
   int d_shift;
+  int move_warps;
+  int list_off;  // shared memory: the list of a local selection, behind the keys and the tokens
   int key_cap;  // keys of a slice held in shared memory
 };
 
@@ -47,13 +53,22 @@ __device__ __forceinline__ void cluster_barrier() {
   __syncwarp();  // the barrier's aligned form wants whole warps
   cluster_sync_all();
 }
+// Word `addr` of the first n CTAs of the cluster (n <= kMaxCluster), all requested before the first is used.
+__device__ __forceinline__ uint32_t sum_cluster(uint32_t addr, int n) {
+  uint32_t v[kMaxCluster], sum = 0u;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) v[r] = r < n ? ld_cluster(addr, r) : 0u;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) sum += v[r];
+  return sum;
+}
 
 template <int FMT>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams P) {
   extern __shared__ __align__(16) uint8_t smem[];  // keys, then the warps' tokens
-  __shared__ uint32_t hist[2][256], total[256];
+  __shared__ uint32_t hist[2][256], total[8];
   __shared__ uint32_t warp_gt[kEvictWarps], warp_eq[kEvictWarps], cta_count[2];
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t found[3];
   __shared__ float row_scale[kEvictWarps][128];
   __shared__ uint32_t row_at[kEvictWarps][128];
   const View& V = P.V;
@@ -67,68 +82,90 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   const float* w = P.w + head * P.w_stride;
   int* kept = P.kept + head * P.budget;
 
+  const bool local = L <= kLocalKeys;
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + P.list_off);  // the kept, of a local selection
   if (L > count) {
     // ---------------- selection ----------------
-    const int per = ((L + C - 1) / C + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
-    const int s0 = min(L, (int)rank * per), s1 = min(L, s0 + per);
+    const int SC = local ? 1 : C, sr = local ? 0 : (int)rank;  // CTAs that share the keys, and this one's place
+    auto barrier = [&] { local ? __syncthreads() : cluster_barrier(); };
+    const int per = ((L + SC - 1) / SC + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+    const int s0 = min(L, sr * per), s1 = min(L, s0 + per);
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-    auto key_of = [&](int j) -> uint32_t {
+    auto rank_of = [&](int j, float x, int page) -> uint32_t {
       if (j < P.first || j >= L - P.recent) return 0xFFFFFFFFu;
-      if (page_of(V, V.table, b, V.table_stride, j >> V.t_shift) < 0) return 0u;
-      const float x = w[j] + 0.f;  // -0 counts as 0
-      if (x != x) return 0u;
+      x += 0.f;  // -0 counts as 0
+      if ((unsigned)page >= (unsigned)V.pages || x != x) return 0u;
       const uint32_t u = __float_as_uint(x);
       return (u >> 31) ? ~u : (u | 0x80000000u);
     };
-    for (int j = s0 + tid; j < s1 && j - s0 < P.key_cap; j += kEvictThreads) keys[j - s0] = key_of(j);
-    auto key = [&](int j) { return j - s0 < P.key_cap ? keys[j - s0] : key_of(j); };
+    const int* table = V.table + (size_t)b * V.table_stride;
+    const int cached = min(s1, s0 + P.key_cap);
+    for (int j0 = s0 + tid; j0 < cached; j0 += 8 * kEvictThreads) {
+      float x[8];
+      int page[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i * kEvictThreads;
+        x[i] = j < cached ? w[j] : 0.f;
+        page[i] = j < cached ? table[j >> V.t_shift] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i * kEvictThreads;
+        if (j < cached) keys[j - s0] = rank_of(j, x[i], page[i]);
+      }
+    }
+    auto key = [&](int j) { return j < cached ? keys[j - s0] : rank_of(j, w[j], table[j >> V.t_shift]); };
     uint32_t prefix = 0u, mask = 0u, want = (uint32_t)count;
-    hist[0][tid] = hist[1][tid] = 0u;
+    if (tid < 256) hist[0][tid] = hist[1][tid] = 0u;
     __syncthreads();
     for (int shift = 24; shift >= 0; shift -= 8) {
       uint32_t* mine = hist[(shift >> 3) & 1];
+#pragma unroll 4
       for (int j = s0 + warp * 32; j < s1; j += kEvictThreads) {
         const uint32_t k = j + lane < s1 ? key(j + lane) : 0u;
         const bool in = j + lane < s1 && (k & mask) == prefix;
-        // one addition per distinct digit in the warp: the leading digits are all alike
-        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(peers) - 1) atomicAdd(&mine[digit], (uint32_t)__popc(peers));
+        if (in) atomicAdd(&mine[(k >> shift) & 255u], 1u);
       }
-      cluster_barrier();
-      uint32_t sum = 0u;
-      for (int r = 0; r < C; ++r) sum += ld_cluster(smem_u32(&mine[tid]), r);
-      total[tid] = sum;
-      // The other histogram was last read, by the whole cluster, before this round's barrier.
-      hist[1 - ((shift >> 3) & 1)][tid] = 0u;
-      __syncthreads();
-      if (warp == 0) {
-        // lane l holds bins 255 - 8 l .. 248 - 8 l: from the largest keys down
-        uint32_t own = 0u;
-        for (int i = 0; i < 8; ++i) own += total[255 - 8 * lane - i];
-        uint32_t upto = own;
+      barrier();
+      // Thread t < 256 holds digit 255 - t: from the largest keys down.
+      uint32_t n = 0u, upto = 0u;
+      if (tid < 256) {
+        n = upto = local ? mine[255 - tid] : sum_cluster(smem_u32(&mine[255 - tid]), C);
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += v;
         }
-        uint32_t above = upto - own;
-        if (above < want && want <= upto) {
-          int bin = 255 - 8 * lane;
-          while (above + total[bin] < want) above += total[bin--];
-          found[0] = (uint32_t)bin;
-          found[1] = want - above;
+        if (lane == 31) total[warp] = upto;
+        // The other histogram was last read, by the whole cluster, before this round's barrier.
+        hist[1 - ((shift >> 3) & 1)][tid] = 0u;
+      }
+      __syncthreads();
+      if (tid < 256) {
+        for (int i = 0; i < warp; ++i) upto += total[i];
+        if (upto - n < want && want <= upto) {
+          found[0] = 255u - (uint32_t)tid;
+          found[1] = want - (upto - n);
+          found[2] = n;
         }
       }
       __syncthreads();
       prefix |= found[0] << shift;
       mask |= 255u << shift;
       want = found[1];
+      if (want == found[2]) {  // all of these digits are kept: no further ones decide
+        --prefix;
+        want = 0u;
+        break;
+      }
     }
     // The kept: every key above `prefix`, and the first `want` equal to it.
     const int sub = per / kEvictWarps;
     const int w0 = min(s1, s0 + warp * sub), w1 = min(s1, w0 + sub);
     const uint32_t before = (1u << lane) - 1u;
     uint32_t gt = 0u, eq = 0u;
+#pragma unroll 4
     for (int j = w0; j < w1; j += 32) {
       const uint32_t k = j + lane < w1 ? key(j + lane) : 0u;
       gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > prefix));
@@ -144,24 +181,25 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       for (int i = 0; i < kEvictWarps; ++i) v += tid ? warp_eq[i] : warp_gt[i];
       cta_count[tid] = v;
     }
-    cluster_barrier();
-    gt = eq = 0u;
-    for (uint32_t r = 0; r < rank; ++r) {
-      gt += ld_cluster(smem_u32(&cta_count[0]), r);
-      eq += ld_cluster(smem_u32(&cta_count[1]), r);
-    }
+    barrier();
+    gt = sum_cluster(smem_u32(&cta_count[0]), sr);
+    eq = sum_cluster(smem_u32(&cta_count[1]), sr);
     for (int i = 0; i < warp; ++i) {
       gt += warp_gt[i];
       eq += warp_eq[i];
     }
+#pragma unroll 4
     for (int j = w0; j < w1; j += 32) {
       const bool in = j + lane < w1;
       const uint32_t k = in ? key(j + lane) : 0u;
       const uint32_t mg = __ballot_sync(0xffffffffu, in && k > prefix);
       const uint32_t me = __ballot_sync(0xffffffffu, in && k == prefix);
       const uint32_t g = gt + __popc(mg & before), e = eq + __popc(me & before);
-      if (in && k > prefix) kept[g + min(e, want)] = j + lane;
-      if (in && k == prefix && e < want) kept[g + e] = j + lane;
+      if (in && (k > prefix || (k == prefix && e < want))) {
+        const uint32_t pos = g + min(e, want);
+        if (sr == (int)rank) kept[pos] = j + lane;
+        if (local) list[pos] = (uint16_t)(j + lane);
+      }
       gt += __popc(mg);
       eq += __popc(me);
     }
@@ -170,18 +208,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   }
   for (int j = count + (int)rank * kEvictThreads + tid; j < P.budget; j += C * kEvictThreads) kept[j] = -1;
   if (rank == 0 && h == 0 && tid == 0) P.new_len[b] = count;
-  cluster_barrier();
+  if (local)
+    __syncthreads();
+  else
+    cluster_barrier();
+  auto kept_at = [&](int pos) { return L == count ? pos : local ? (int)list[pos] : kept[pos]; };
 
   // ---------------- move ----------------
   const int chunk_shift = P.d_shift - 4;  // 16-byte chunks per token
   const int chunks = T << chunk_shift;
-  uint8_t* stage = smem + ((size_t)(warp << V.t_shift) << P.d_shift);
+  uint8_t* stage = smem + ((size_t)(warp << V.t_shift) << P.d_shift);  // of the first move_warps warps
   const uint32_t stage_u = smem_u32(stage);
   float* rs = row_scale[warp];
   uint32_t* ra = row_at[warp];
-  const int units = 2 * ((count + T - 1) >> V.t_shift);
-  for (int u0 = 0; u0 < units; u0 += C * kEvictWarps) {
-    const int u = u0 + (int)rank * kEvictWarps + warp;
+  const int units = 2 * ((count + T - 1) >> V.t_shift), wave = C * P.move_warps;
+  for (int u0 = 0; u0 < units; u0 += wave) {
+    const int u = warp < P.move_warps ? u0 + (int)rank * P.move_warps + warp : units;
     const int blk = u >> 1, sel = u & 1;
     const int base = blk << V.t_shift;
     bool same = false;
@@ -190,7 +232,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     float kw[4];
     if (u < units) {
       const int last = min(count, base + T) - 1;
-      same = kept[last] == last;
+      same = kept_at(last) == last;
       from = page_of(V, V.table, b, V.table_stride, min(blk, V.table_stride - 1));
       to = page_of(V, P.dst_table, b, P.dst_stride, blk);
       const float* scales = sel ? V.vs : V.ks;
@@ -199,7 +241,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         const int t = lane + 32 * i;
         if (t < T) {
           const int pos = base + t;
-          const int j = pos < count ? kept[pos] : -1;
+          const int j = pos < count ? kept_at(pos) : -1;
           const int page = j >= 0 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
           const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
           rs[t] = page >= 0 ? scales[cell] : 0.f;
@@ -210,6 +252,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       }
       __syncwarp();
       const uint8_t* pool = sel ? V.v : V.k;
+#pragma unroll 4
       for (int c = lane; c < chunks; c += 32) {
         const uint32_t at = ra[c >> chunk_shift];
         const bool there = at != 0xffffffffu;
@@ -222,6 +265,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         if (from >= 0) now = scales[(size_t)from * V.Hkv + h];
       } else {
         float a = 0.f;
+#pragma unroll 4
         for (int c = lane; c < chunks; c += 32) {
           const uint4 q = *reinterpret_cast<const uint4*>(stage + 16 * c);
           const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
@@ -238,6 +282,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         now = scale_for<FMT>(a);
         const Divisor by = divisor(now);
+#pragma unroll 2
         for (int c = lane; c < chunks; c += 32) {
           uint4* at = reinterpret_cast<uint4*>(stage + 16 * c);
           const uint4 q = *at;
@@ -266,6 +311,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       if (to >= 0 && !(same && to == from)) {
         const size_t cell = (size_t)to * V.Hkv + h;
         uint8_t* dst = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);
+#pragma unroll 4
         for (int c = lane; c < chunks; c += 32)
           *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(stage + 16 * c);
         if (lane == 0) (sel ? V.vs : V.ks)[cell] = now;
@@ -283,23 +329,28 @@ template <int FMT>
 tm_status launch_evict(EvictParams P, cudaStream_t stream) {
   const View& V = P.V;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), 8 * 128 * 128)) return TM_ERR_CUDA;
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), kStage + 2 * kLocalKeys)) return TM_ERR_CUDA;
   // CTAs per cluster: as many as the pages or the keys can use, while all clusters fit the GPU at once.
   const long long T = 1ll << V.t_shift, heads = (long long)V.B * V.Hkv;
   const long long units = 2 * ((P.budget + T - 1) / T), room = 4ll * num_sms(current_device());
-  unsigned C = 1;
-  while (C < 8 && heads * 2 * C <= room && (units > C * kEvictWarps || V.max_len > (long long)C * 4096)) C *= 2;
-  const long long slice = (V.max_len + C - 1) / C + kEvictThreads;
-  P.key_cap = (int)(slice < kKeyCap ? slice : kKeyCap);
-  const size_t stage = ((size_t)kEvictWarps << V.t_shift) << P.d_shift, keys = (size_t)P.key_cap * 4;
+  const int page = (int)T << P.d_shift;
+  P.move_warps = kStage / page < kEvictWarps ? kStage / page : kEvictWarps;
+  int C = 1;
+  while (C < kMaxCluster && heads * 2 * C <= room && (units > C * 8 || V.max_len > C * 4096ll)) C *= 2;
+  if (units < P.move_warps * C) P.move_warps = (int)((units + C - 1) / C);
+  const long long slice = (V.max_len + C - 1) / C + kEvictThreads, alone = V.max_len < kLocalKeys ? V.max_len : kLocalKeys;
+  const long long most = V.max_len <= kLocalKeys || slice < alone ? alone : slice;
+  P.key_cap = (int)(most < kKeyCap ? most : kKeyCap);
+  const size_t stage = (size_t)P.move_warps * page, keys = (size_t)P.key_cap * 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C, (unsigned)V.Hkv, (unsigned)V.B);
+  cfg.gridDim = dim3((unsigned)C, (unsigned)V.Hkv, (unsigned)V.B);
   cfg.blockDim = dim3(kEvictThreads, 1, 1);
-  cfg.dynamicSmemBytes = stage > keys ? stage : keys;
+  P.list_off = (int)(stage > keys ? stage : (keys + 15) / 16 * 16);
+  cfg.dynamicSmemBytes = P.list_off + 2 * (size_t)(P.budget < alone ? P.budget : alone);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.x = (unsigned)C;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
