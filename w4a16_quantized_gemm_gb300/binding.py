@@ -180,7 +180,7 @@ def packed_bytes(K: int, N: int, g: int) -> int:
 def _dev(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -762,6 +762,7 @@ class KVBlocks:
         self.k, self.v, self.ks, self.vs = k, v, ks, vs
         self.pages, self.Hkv, self.T, self.D = pages, Hkv, T, D
         self.device = k.device
+        self.index = self.device.index
         self._c = KVBCacheStruct(_dev(k, k.dtype, "k"), _dev(v, k.dtype, "v"), _dev(ks, torch.float32, "ks"),
                            _dev(vs, torch.float32, "vs"), pages, Hkv, T, D, _KVB_FORMATS[k.dtype])
         self._ref = ctypes.byref(self._c)
@@ -812,28 +813,31 @@ class KVBatch:
 
 
 def _kvb_rows(t: torch.Tensor, heads, D: int, name: str):
-    """Device pointer and token stride of [rows][heads][D] whose heads lie together."""
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or not t.is_cuda:
+    """Device pointer, token stride, dtype code and shape of [rows][heads][D] whose heads lie together."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [rows][heads][{D}]")
-    if t.dtype not in _KVB_DTYPES:
+    dtype = _KVB_DTYPES.get(t.dtype)
+    if dtype is None:
         raise ValueError(f"{name} must be fp16 or bf16")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    if stride[2] != 1 or (stride[1] != D and shape[1] > 1):
         raise ValueError(f"{name}'s heads must be contiguous (its rows may have a stride)")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * D, dtype, shape
 
 
 def _kvb_weights(t: Optional[torch.Tensor], B: int, Hkv: int, name: str):
     if t is None:
         return None, 0
-    if t.dim() != 3 or t.shape[:2] != (B, Hkv):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != Hkv:
         raise ValueError(f"{name} must be fp32 [B][Hkv][tokens]")
-    return _dev(t, torch.float32, name), t.shape[2]
+    return _dev(t, torch.float32, name), shape[2]
 
 
-def _kvb_stream(device, stream, *made):
+def _kvb_stream(cache, stream, *made):
     """The call's stream; what the call allocated is kept for it."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(cache.index)
     for t in made:
         if t is not None:
             t.record_stream(stream)
@@ -846,13 +850,16 @@ def kvb_append(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.Tensor
     be strided), into the pages of the last tokens of each sequence
     (tm_kvb_append).  w: token weights fp32 [B][Hkv][tokens], set to 0 for the
     new tokens."""
-    kp, ks = _kvb_rows(K, cache.Hkv, cache.D, "K")
-    vp, vs = _kvb_rows(V, cache.Hkv, cache.D, "V")
-    if V.shape != K.shape or V.dtype != K.dtype:
+    Hkv, D = cache.Hkv, cache.D
+    kp, ks, dtype, shape = _kvb_rows(K, Hkv, D, "K")
+    vp, vs, vdtype, vshape = _kvb_rows(V, Hkv, D, "V")
+    if vshape != shape or vdtype != dtype:
         raise ValueError("V must have the shape and dtype of K")
-    wp, wn = _kvb_weights(w, batch.B, cache.Hkv, "w")
-    _check(load().tm_kvb_append(cache._ref, batch._rows(K.shape[0]), kp, ks, vp, vs, _KVB_DTYPES[K.dtype], wp, wn,
-                                _kvb_stream(cache.device, stream)), "tm_kvb_append")
+    wp, wn = _kvb_weights(w, batch.B, Hkv, "w")
+    st = (_lib or load()).tm_kvb_append(cache._ref, batch._rows(shape[0]), kp, ks, vp, vs, dtype, wp, wn,
+                                        _kvb_stream(cache, stream))
+    if st:
+        raise TMError(st, "tm_kvb_append")
 
 
 def kvb_attention_workspace(cache: KVBlocks, batch: KVBatch, Hq: int, rows: int, weights: bool = False) -> int:
@@ -876,31 +883,32 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
     w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
            token drew in this call; may be w_in
     workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
-    qp, qs = _kvb_rows(Q, None, cache.D, "Q")
-    rows, Hq = Q.shape[:2]
+    qp, qs, dtype, shape = _kvb_rows(Q, None, cache.D, "Q")
+    rows, Hq = shape[0], shape[1]
     made_out = made_ws = None
     if out is None:
-        out = made_out = torch.empty((rows, Hq, cache.D), dtype=Q.dtype, device=Q.device)
-    elif out.shape != Q.shape:
+        out = made_out = torch.empty(shape, dtype=Q.dtype, device=Q.device)
+    elif out.shape != shape:
         raise ValueError("out must have the shape of Q")
-    if lse is not None and lse.shape != (rows, Hq):
-        raise ValueError("lse must be fp32 [rows][Hq]")
+    lp = None
+    if lse is not None:
+        if lse.shape != shape[:2]:
+            raise ValueError("lse must be fp32 [rows][Hq]")
+        lp = _dev(lse, torch.float32, "lse")
     wi, ni = _kvb_weights(w_in, batch.B, cache.Hkv, "w_in")
     wo, no = _kvb_weights(w_out, batch.B, cache.Hkv, "w_out")
     if wi is not None and (wo is None or ni != no):
         raise ValueError("w_in comes with a w_out of its shape")
-    ref = batch._rows(rows)
-    lib = load()
     if workspace is None:
         size = kvb_attention_workspace(cache, batch, Hq, rows, wo is not None)
         if size:
             workspace = made_ws = torch.empty(size, dtype=torch.uint8, device=Q.device)
-    st = lib.tm_kvb_attention(cache._ref, ref, qp, qs, Hq, _KVB_DTYPES[Q.dtype], 0.0 if scale is None else scale,
-                              _dev(out, Q.dtype, "out"), None if lse is None else _dev(lse, torch.float32, "lse"),
-                              wi, wo, no, None if workspace is None else _dev(workspace, torch.uint8, "workspace"),
-                              0 if workspace is None else workspace.numel(),
-                              _kvb_stream(cache.device, stream, made_out, made_ws))
-    _check(st, "tm_kvb_attention")
+    sp, size = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    st = (_lib or load()).tm_kvb_attention(cache._ref, batch._rows(rows), qp, qs, Hq, dtype,
+                                           0.0 if scale is None else scale, _dev(out, Q.dtype, "out"), lp, wi, wo, no,
+                                           sp, size, _kvb_stream(cache, stream, made_out, made_ws))
+    if st:
+        raise TMError(st, "tm_kvb_attention")
     return out
 
 
@@ -932,6 +940,6 @@ def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, fir
         raise ValueError("dst_table must be int32 [B][n]")
     st = load().tm_kvb_evict(cache._ref, batch._ref, _dev(dst, torch.int32, "dst_table"), dst.shape[1], wp, wn, op, on,
                              budget, first, recent, _dev(kept, torch.int32, "kept"),
-                             _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache.device, stream, *made))
+                             _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache, stream, *made))
     _check(st, "tm_kvb_evict")
     return kept, new_len
