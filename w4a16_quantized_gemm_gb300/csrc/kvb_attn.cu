@@ -10,12 +10,13 @@
 // from fp16's subnormals; m only moves when the maximum has grown by more
 // than 8, so w < 2^14 and the accumulators are rarely rescaled.
 //
-// A CTA takes one (sequence, KV head), RT x 16 rows (query token, query head of
-// the group) and a slice of the tokens, in tiles of 64: 4 RT warps, each 16
-// rows x 16 tokens of the tile, with a running softmax of its own; the tile
-// comes by 16-byte asynchronous copies, several tiles ahead.  Rows
-// of different tokens of a draft share the tile's codes.  The slices' partial
-// states go through a workspace and a second launch joins them.
+// A CTA takes one (sequence, KV head), up to 8, 16 or 32 rows (query token,
+// query head of the group) and a slice of the tokens.  Its four warps take steps of 32
+// tokens in turn, each with a running softmax and a TMA ring of its own (a
+// 16-token group of a page and head is one swizzled box), so that no warp
+// waits for another before the end.  All rows share the conversion of the codes,
+// which is most of the arithmetic.  The slices' partial states go through a
+// workspace, and a second launch joins them and sums the tokens' weights.
 //
 // Order of tokens and dimensions: the K fragment's column n holds token
 // sigma(n) of an 8-token group, a lane's 16-byte chunk holds 16 dimensions that
@@ -27,11 +28,15 @@
 namespace w4 {
 namespace kvb {
 
-constexpr int kTile = 64;    // tokens per tile
-constexpr int kWarpTok = 16;  // tokens of a tile per warp
-constexpr float kBias = 6.f;  // log2 of the largest weight right after m moved
+static __device__ uint32_t s_err_kvbd;
+
+constexpr int kFewWarps = 4;
+constexpr int kStep = 32;                      // tokens per step of a warp
+constexpr int kTile = kFewWarps * kStep;       // tokens per round of the warps
+constexpr float kBias = 6.f;                   // log2 of the largest weight right after m moved
 constexpr float kSlack = 8.f;
-constexpr float kNone = -1e30f;  // m of a row that has seen nothing
+constexpr float kNone = -1e30f;                // m of a row that has seen nothing
+constexpr float kLn2 = 0.693147180559945f;
 
 template <int D>
 __device__ __forceinline__ int sigma(int n) {
@@ -39,410 +44,584 @@ __device__ __forceinline__ int sigma(int n) {
   const int m = n >> 1;
   return ((m & 1) | ((m >> 1) << 2)) ^ ((n & 1) * 3);
 }
-// Byte offset of 16-byte chunk c of tile row r.
+// Byte offset of 16-byte chunk c of row r of a 16-token box (the TMA's 128- or 64-byte swizzle).
 template <int D>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+// RT: 16-row tiles; 0: one half tile (rows 8 .. 15 of the products stay empty).
 template <int D, int RT>
-struct AttnShape {
-  static constexpr int THREADS = 128 * RT;
-  static constexpr uint32_t K_BYTES = kTile * D;
-  static constexpr uint32_t META = 2 * K_BYTES;       // ks[4], vs[4], page[4]
-  static constexpr uint32_t SLOT = 2 * K_BYTES + 64;  // multiple of 64
-  static constexpr int STAGES = 4;
-  static constexpr uint32_t JOIN = 2 * RT * (16 * D + 32) * 4;  // two warps' states per row tile
-  static constexpr uint32_t SMEM = STAGES * SLOT > JOIN ? STAGES * SLOT : JOIN;
+struct FewShape {
+  static constexpr int TILES = RT == 0 ? 1 : RT;
+  static constexpr int E = RT == 0 ? 1 : 2;  // rows per lane and tile
+  static constexpr int ROWS = TILES * 8 * E;
+  static constexpr uint32_t BOX = 16 * D;
+  static constexpr uint32_t STAGE = 4 * BOX;  // K of two groups, V of two groups
+  static constexpr int STAGES = D == 128 && RT < 2 ? 2 : 3;
+  static constexpr uint32_t RING = kFewWarps * STAGES * STAGE;
+  static constexpr int STATE = TILES * E * (8 * D + 16);  // floats of a warp's state
+  static constexpr uint32_t BODY = RING > 2 * STATE * 4 ? RING : 2 * STATE * 4;
+  static constexpr uint32_t Q_OFF = BODY;  // RT == 2: query fragments
+  static constexpr uint32_t BARS = Q_OFF + (RT == 2 ? TILES * (D / 16) * 512 : 0);
+  static constexpr uint32_t SMEM = BARS + kFewWarps * STAGES * 8 + 16 + 1024;
 };
 
+// d (rows 0 .. 7 of the tile) += a . b with rows 8 .. 15 of a zero.
+__device__ __forceinline__ void mma_top(float& d0, float& d1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  float x, y;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};\n"
+      : "+f"(d0), "+f"(d1), "=f"(x), "=f"(y)
+      : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+  (void)x;
+  (void)y;
+}
+
 template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(128 * RT) attn_kernel(const AttnParams P) {
-  using SH = AttnShape<D, RT>;
+__global__ void __launch_bounds__(32 * kFewWarps)
+    attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
+  using SH = FewShape<D, RT>;
+  constexpr int TILES = SH::TILES, E = SH::E, S = SH::STAGES;
   constexpr int NV = D / 8;   // n-tiles of the output
   constexpr int KS = D / 16;  // k-steps of the scores
-  constexpr int CPR = D / 16;  // 16-byte chunks per token
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t base = smem_u32(smem);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
   const View& V = P.V;
   const int b = blockIdx.z, chunk = blockIdx.x;
   const int h = blockIdx.y % V.Hkv, rg = blockIdx.y / V.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
-  const int rt = warp >> 2, ts = warp & 3;
   const Span s = span(V, b);
   const int rows = s.n * P.G;
-  const int row_base = rg * RT * 16;
+  const int row_base = rg * SH::ROWS;
   if (row_base >= rows) return;
-  // Tokens [j0, j1) that some row of the group sees.
-  const int last_i = (min(row_base + RT * 16, rows) - 1) / P.G;
+  // Tokens [j0, j1) that some row of the group sees; all rows see those up to `all`.
+  const int last_i = (min(row_base + SH::ROWS, rows) - 1) / P.G;
   const int j0 = chunk * P.chunk;
   const int j1 = min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
-  if (j0 >= j1 && chunk > 0) return;  // chunk 0 still writes what an empty row gives
-  const int tiles = j1 > j0 ? (j1 - j0 + kTile - 1) / kTile : 0;
+  const int all = min(s.old + row_base / P.G, j1 - 1);
+  if (j0 >= j1 && chunk > 0) return;  // slice 0 still writes what an empty row gives
+  const int steps = j1 > j0 ? (j1 - j0 + kStep - 1) / kStep : 0;
+  const int mine = steps > warp ? (steps - warp + kFewWarps - 1) / kFewWarps : 0;
 
-  // ---- copies: thread -> chunk c of tokens 16 r + ..., the page of each 16-token group ahead of its use
-  const int c16 = tid % CPR, r16 = (tid / CPR);
-  constexpr int ROWS_PER_PASS = SH::THREADS / CPR;
-  constexpr int PASSES = kTile / ROWS_PER_PASS > 0 ? kTile / ROWS_PER_PASS : 1;
-  auto issue = [&](int it) {
-    if (it < tiles) {
-      const uint32_t slot = base + (it % SH::STAGES) * SH::SLOT;
-      const int tok0 = j0 + it * kTile;
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int r = r16 + p * ROWS_PER_PASS;
-        if (r < kTile) {
-          const int j = tok0 + r;
-          const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
-          const size_t off = ((((size_t)max(page, 0) * V.Hkv + h) << V.t_shift) + (j & ((1 << V.t_shift) - 1))) * D + c16 * 16;
-          const uint32_t at = swz<D>(r, c16);
-          cp16(slot + at, V.k + (page >= 0 ? off : 0), page >= 0);
-          cp16(slot + SH::K_BYTES + at, V.v + (page >= 0 ? off : 0), page >= 0);
-          if (c16 == 0 && (r & 15) == 0) {
-            const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
-            cp4(slot + SH::META + (r >> 4) * 4, V.ks + (page >= 0 ? cell : 0), page >= 0);
-            cp4(slot + SH::META + 16 + (r >> 4) * 4, V.vs + (page >= 0 ? cell : 0), page >= 0);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + SH::META + 32 + (r >> 4) * 4), "r"(page) : "memory");
-          }
-        }
-      }
-    }
-    cp_commit();
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + kFewWarps * S * 8);
+  if (tid == 0) {
+    for (int i = 0; i < kFewWarps * S; ++i) mbar_init(base + SH::BARS + 8 * i, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  launch_dependents();
+
+  // ---- pages and scales, 16 steps at a time and one batch ahead: lane 2 k + g has group g of the batch's step k
+  struct Meta {
+    int cell, slot;
+    float ks, lv;
+  };
+  auto load_meta = [&](int batch) {
+    const int j = j0 + ((batch * 16 + (lane >> 1)) * kFewWarps + warp) * kStep + 16 * (lane & 1);
+    const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+    Meta m;
+    m.cell = page >= 0 ? page * V.Hkv + h : -1;
+    m.slot = j & ((1 << V.t_shift) - 1);
+    m.ks = page >= 0 ? V.ks[m.cell] : 1.f;
+    // 2^lv stands for vs (to 2^-21 of it); its own inverse takes it out of l again.
+    m.lv = page >= 0 ? __log2f(fmaxf(V.vs[m.cell], kScaleFloor)) : 0.f;
+    return m;
+  };
+  Meta cur = load_meta(0), nxt = load_meta(1);
+  const uint32_t ring = base + warp * S * SH::STAGE, bars = base + SH::BARS + warp * S * 8;
+  auto issue = [&](int i, int batch) {  // batch: of `cur`
+    if (i >= mine) return;
+    const bool ahead = (i >> 4) != batch;
+    const int from = (2 * i & 31) + (lane & 1);
+    const int cell = __shfl_sync(0xffffffffu, ahead ? nxt.cell : cur.cell, from);
+    const int slot = __shfl_sync(0xffffffffu, ahead ? nxt.slot : cur.slot, from);
+    const uint32_t there = __popc(__ballot_sync(0xffffffffu, cell >= 0 && lane < 2));
+    const uint32_t bar = bars + 8 * (i % S);
+    if (lane == 0) mbar_expect_tx(bar, there * 2 * SH::BOX);
+    __syncwarp();
+    if (lane < 4 && cell >= 0)
+      tma_load_3d(ring + (i % S) * SH::STAGE + lane * SH::BOX, lane < 2 ? &tmK : &tmV, 0, slot, cell, bar);
   };
 #pragma unroll
-  for (int i = 0; i < SH::STAGES - 1; ++i) issue(i);
+  for (int i = 0; i < S; ++i) issue(i, 0);
 
   // ---- the queries, once, in the k order of the codes; bf16 rows are scaled by a
   // power of two into fp16's range (exact down to 2^-39 of the row's maximum)
-  uint32_t qa[KS][4];
-  float qscale[2];
-  int lastv[2];  // last visible token of the lane's two rows (-1: none)
-  size_t hr[2];  // row index of the outputs
+  uint32_t qa[RT == 2 ? 1 : KS][RT == 0 ? 2 : 4];
+  float mul[TILES][E];
+  int last[TILES][E];  // last visible token (-1: no row)
+  size_t hr[TILES][E];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int row = row_base + rt * 16 + gr + 8 * e;
-    const bool ok = row < rows;
-    const int i = ok ? row / P.G : 0;
-    const int hq = h * P.G + (ok ? row - i * P.G : 0);
-    lastv[e] = ok ? min(s.old + i, s.len - 1) : -1;
-    hr[e] = (size_t)(s.row0 + i) * P.Hq + hq;
-    const uint16_t* q = P.Q + (s.row0 + i) * P.q_stride + (long long)hq * D;
-    uint32_t raw[KS][2];
+  for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-    for (int j = 0; j < KS / 4; ++j)
+    for (int e = 0; e < E; ++e) {
+      const int row = row_base + rt * 16 + gr + 8 * e;
+      const bool ok = row < rows;
+      const int i = ok ? row / P.G : 0;
+      const int hq = h * P.G + (ok ? row - i * P.G : 0);
+      last[rt][e] = ok ? min(s.old + i, s.len - 1) : -1;
+      hr[rt][e] = (size_t)(s.row0 + i) * P.Hq + hq;
+      const uint16_t* q = P.Q + (s.row0 + i) * P.q_stride + (long long)hq * D;
+      uint32_t raw[KS][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 16 * (t + 4 * j) + 8 * k) : make_uint4(0, 0, 0, 0);
-        raw[4 * j + 2 * k][0] = x.x;
-        raw[4 * j + 2 * k][1] = x.y;
-        raw[4 * j + 2 * k + 1][0] = x.z;
-        raw[4 * j + 2 * k + 1][1] = x.w;
+      for (int j = 0; j < KS / 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 16 * (t + 4 * j) + 8 * k) : make_uint4(0, 0, 0, 0);
+          raw[4 * j + 2 * k][0] = x.x;
+          raw[4 * j + 2 * k][1] = x.y;
+          raw[4 * j + 2 * k + 1][0] = x.z;
+          raw[4 * j + 2 * k + 1][1] = x.w;
+        }
+      float qs = 1.f;
+      if (P.bf16) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack(raw[k][x], true);
+            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);  // m < 2^(e2 + 1)
+        const float up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
+        qs = __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack(raw[k][x], true);
+            raw[k][x] = pack_half2(f.x * up, f.y * up);
+          }
       }
-    qscale[e] = 1.f;
-    if (P.bf16) {
-      float m = 0.f;
+      mul[rt][e] = qs * P.scale_log2;
+      if constexpr (RT == 2) {
+        if ((warp & 1) == rt) {  // two warps write the same values for each tile: no exchange needed
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 f = unpack(raw[k][x], true);
-          m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t at = base + SH::Q_OFF + ((rt * KS + k) * 32 + lane) * 16 + 4 * e;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(raw[k][0]) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8), "r"(raw[k][1]) : "memory");
+          }
         }
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);  // m < 2^(e2 + 1)
-      const float up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
-      qscale[e] = __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
+      } else {
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 f = unpack(raw[k][x], true);
-          raw[k][x] = pack_half2(f.x * up, f.y * up);
+        for (int k = 0; k < KS; ++k) {
+          qa[k][e] = raw[k][0];
+          qa[k][E + e] = raw[k][1];
         }
+      }
     }
+  if constexpr (RT == 2) __syncthreads();
+
+  float o[TILES][NV][2 * E];
+  float m[TILES][E], l[TILES][E];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      qa[k][e] = raw[k][0];
-      qa[k][2 + e] = raw[k][1];
+  for (int rt = 0; rt < TILES; ++rt) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int x = 0; x < 2 * E; ++x) o[rt][i][x] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      m[rt][e] = kNone;
+      l[rt][e] = 0.f;
     }
   }
-
-  float o[NV][4];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
   const int sg[2] = {sigma<D>(2 * t), sigma<D>(2 * t + 1)};
   const int kr = sigma<D>(gr);
 
-  for (int it = 0; it < tiles; ++it) {
-    cp_wait<SH::STAGES - 2>();
-    __syncthreads();
-    issue(it + SH::STAGES - 1);
-    const uint32_t slot = base + (it % SH::STAGES) * SH::SLOT;
-    const int tok0 = j0 + it * kTile + ts * kWarpTok;
-    if (tok0 >= j1) continue;  // the warp's tokens lie past the end (warp-uniform)
-    const int page = (int)lds32(slot + SH::META + 32 + ts * 4);
-    const float ks = __uint_as_float(lds32(slot + SH::META + ts * 4));
-    const float vs = fmaxf(__uint_as_float(lds32(slot + SH::META + 16 + ts * 4)), kScaleFloor);
-    // ---- scores: 16 rows x 16 tokens
-    float sc[2][4] = {};
+  for (int i = 0; i < mine; ++i) {
+    const int batch = i >> 4;
+    if (i > 0 && (i & 15) == 0) {
+      cur = nxt;
+      nxt = load_meta(batch + 1);
+    }
+    const bool alive = mbar_wait(bars + 8 * (i % S), (uint32_t)(i / S) & 1u, abort_flag, &s_err_kvbd);
+    if (!__all_sync(0xffffffffu, alive)) break;
+    const uint32_t kt = ring + (i % S) * SH::STAGE, vt = kt + 2 * SH::BOX;
+    const int tok0 = j0 + (i * kFewWarps + warp) * kStep;
+    float ks[2], lv[2];
+    bool there[2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int g = 0; g < 2; ++g) {
+      const int from = (2 * i & 31) + g;
+      ks[g] = __shfl_sync(0xffffffffu, cur.ks, from);
+      lv[g] = __shfl_sync(0xffffffffu, cur.lv, from);
+      there[g] = __shfl_sync(0xffffffffu, cur.cell, from) >= 0;
+    }
+    // Whether some row does not see some token (warp-uniform).
+    const bool part = tok0 + kStep - 1 > all || !there[0] || !there[1];
+    // ---- scores: rows x 32 tokens
+    float sc[TILES][4][2 * E];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+#pragma unroll
+      for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+        for (int x = 0; x < 2 * E; ++x) sc[rt][a][x] = 0.f;
 #pragma unroll
       for (int j = 0; j < KS / 4; ++j) {
-        const uint4 kw = lds128(slot + swz<D>(ts * kWarpTok + 8 * a + kr, t + 4 * j));
+        const uint4 kw = lds128(kt + (a >> 1) * SH::BOX + swz<D>(8 * (a & 1) + kr, t + 4 * j));
         const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int k = 0; k < 4; ++k) {
           uint32_t b0, b1;
-          codes_half<FMT>(wd[i], b0, b1);
-          mma_16816(sc[a], qa[4 * j + i], b0, b1);
+          codes_half<FMT>(wd[k], b0, b1);
+          if constexpr (RT == 0) {
+            mma_top(sc[0][a][0], sc[0][a][1], qa[4 * j + k][0], qa[4 * j + k][1], b0, b1);
+          } else if constexpr (RT == 1) {
+            mma_16816(sc[0][a], qa[4 * j + k], b0, b1);
+          } else {
+#pragma unroll
+            for (int rt = 0; rt < TILES; ++rt) {
+              const uint4 f = lds128(base + SH::Q_OFF + ((rt * KS + 4 * j + k) * 32 + lane) * 16);
+              const uint32_t fa[4] = {f.x, f.y, f.z, f.w};
+              mma_16816(sc[rt][a], fa, b0, b1);
+            }
+          }
         }
       }
+    }
     // ---- softmax
-    // 2^lv stands for vs (to 2^-21 of it); its own inverse takes it out of l again.
-    const float lv = __log2f(vs), inv = ex2(-lv);
-    uint32_t pa[4];
-    float tm[2] = {-INFINITY, -INFINITY};
+    uint32_t pa[TILES][2][2 * E];  // per 16-token group: A fragment
+    const float inv[2] = {ex2(-lv[0]), ex2(-lv[1])};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float c = ks * qscale[e] * P.scale_log2;
+    for (int rt = 0; rt < TILES; ++rt) {
+      float tm[E];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int e = 0; e < E; ++e) {
+        float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = tok0 + 8 * a + sg[x];
-          float v = sc[a][2 * e + x] * c;
-          v = (page >= 0 && j <= lastv[e]) ? v : -INFINITY;
-          sc[a][2 * e + x] = v;
-          tm[e] = fmaxf(tm[e], v);
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float v = sc[rt][a][2 * e + x] * (ks[a >> 1] * mul[rt][e]);
+            if (part && (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e])) v = -INFINITY;
+            sc[rt][a][2 * e + x] = v;
+            if (a < 2)
+              g0 = fmaxf(g0, v);
+            else
+              g1 = fmaxf(g1, v);
+          }
+        if (P.scores && last[rt][e] >= 0) {
+          float* row = P.scores + hr[rt][e] * P.score_stride + tok0;
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[rt][a][2 * e + x];
         }
-      if (P.scores && lastv[e] >= 0) {
-        float* row = P.scores + hr[e] * P.score_stride + tok0;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[a][2 * e + x];
+        tm[e] = fmaxf(g0 + lv[0], g1 + lv[1]);
+        tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
+        tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
       }
-      tm[e] += lv;
-      tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
-      tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
-    }
-    if (__any_sync(0xffffffffu, tm[0] > m[0] + kSlack || tm[1] > m[1] + kSlack)) {
+      if (__any_sync(0xffffffffu, tm[0] > m[rt][0] + kSlack || tm[E - 1] > m[rt][E - 1] + kSlack)) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[e], tm[e]);
-        const float f = ex2(m[e] - mn);
-        m[e] = mn;
-        l[e] *= f;
+        for (int e = 0; e < E; ++e) {
+          const float mn = fmaxf(m[rt][e], tm[e]);
+          const float f = ex2(m[rt][e] - mn);
+          m[rt][e] = mn;
+          l[rt][e] *= f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          o[i][2 * e] *= f;
-          o[i][2 * e + 1] *= f;
+          for (int k = 0; k < NV; ++k) {
+            o[rt][k][2 * e] *= f;
+            o[rt][k][2 * e + 1] *= f;
+          }
         }
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float off = lv[g] + kBias - m[rt][e];
+          float sum = 0.f;
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const float p0 = ex2(sc[rt][2 * g + a][2 * e] + off), p1 = ex2(sc[rt][2 * g + a][2 * e + 1] + off);
+            sum += p0 + p1;
+            pa[rt][g][E * a + e] = pack_half2(p0, p1);
+          }
+          l[rt][e] = fmaf(sum, inv[g], l[rt][e]);
+        }
     }
+    // ---- values: rows x 32 tokens x D
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float off = lv + kBias - m[e];
-      float sum = 0.f;
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float p0 = ex2(sc[a][2 * e] + off), p1 = ex2(sc[a][2 * e + 1] + off);
-        sum += p0 + p1;
-        pa[2 * a + e] = pack_half2(p0, p1);
-      }
-      l[e] = fmaf(sum, inv, l[e]);
-    }
-    // ---- values: 16 rows x 16 tokens x D
-    const uint32_t vb = slot + SH::K_BYTES;
-    const int r0 = ts * kWarpTok;
-    if constexpr (D == 128) {
-      const uint4 v0 = lds128(vb + swz<D>(r0 + sg[0], gr)), v1 = lds128(vb + swz<D>(r0 + sg[1], gr));
-      const uint4 v2 = lds128(vb + swz<D>(r0 + 8 + sg[0], gr)), v3 = lds128(vb + swz<D>(r0 + 8 + sg[1], gr));
-      const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-      const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t b0[4], b1[4];
-        codes_half_pairs<FMT>(w0[i], w1[i], b0);
-        codes_half_pairs<FMT>(w2[i], w3[i], b1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_16816(o[4 * i + k], pa, b0[k], b1[k]);
-      }
-    } else {
-      uint32_t wv[4][2];
+    for (int g = 0; g < 2; ++g) {
+      constexpr int W = D / 32;  // words of codes per lane and token
+      uint32_t wv[4][W];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t at = vb + swz<D>(r0 + 8 * (q >> 1) + sg[q & 1], gr >> 1) + 8 * (gr & 1);
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wv[q][0]), "=r"(wv[q][1]) : "r"(at));
+        const int r = 8 * (q >> 1) + sg[q & 1];
+        if constexpr (D == 128) {
+          const uint4 x = lds128(vt + g * SH::BOX + swz<D>(r, gr));
+          wv[q][0] = x.x;
+          wv[q][1] = x.y;
+          wv[q][2] = x.z;
+          wv[q][3] = x.w;
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(wv[q][0]), "=r"(wv[q][1])
+                       : "r"(vt + g * SH::BOX + swz<D>(r, gr >> 1) + 8 * (gr & 1)));
+        }
+        // Slots past the end and the boxes of holes hold anything, NaN codes too.
+        if (part && (!there[g] || tok0 + 16 * g + r >= j1))
+#pragma unroll
+          for (int k = 0; k < W; ++k) wv[q][k] = 0u;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < W; ++k) {
         uint32_t b0[4], b1[4];
-        codes_half_pairs<FMT>(wv[0][i], wv[1][i], b0);
-        codes_half_pairs<FMT>(wv[2][i], wv[3][i], b1);
+        codes_half_pairs<FMT>(wv[0][k], wv[1][k], b0);
+        codes_half_pairs<FMT>(wv[2][k], wv[3][k], b1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_16816(o[4 * i + k], pa, b0[k], b1[k]);
+        for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (RT == 0)
+              mma_top(o[0][4 * k + c][0], o[0][4 * k + c][1], pa[0][g][0], pa[0][g][1], b0[c], b1[c]);
+            else
+              mma_16816(o[rt][4 * k + c], pa[rt][g], b0[c], b1[c]);
+          }
       }
     }
+    __syncwarp();  // the stage is read: it may be filled again
+    issue(i + S, batch);
   }
-  cp_wait<0>();
+  if (*abort_flag) {
+    // A wait gave up: no copy may land in memory that the join is about to use.
+    const unsigned long long t0 = globaltimer();
+    for (int i = 0; i < S && i < mine; ++i)
+      while (!mbar_try_wait(bars + 8 * i, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+  }
   __syncthreads();
 
-  // ---- join the four warps of a row tile: 2, 3 into 0, 1, then 1 into 0
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-  }
+  // ---- join the four warps: 2, 3 into 0, 1, then 1 into 0
   float* st = reinterpret_cast<float*>(smem);
-  constexpr int STATE = 16 * D + 32;
+#pragma unroll
+  for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      l[rt][e] += __shfl_xor_sync(0xffffffffu, l[rt][e], 1);
+      l[rt][e] += __shfl_xor_sync(0xffffffffu, l[rt][e], 2);
+    }
 #pragma unroll
   for (int step = 2; step >= 1; step >>= 1) {
-    if (ts >= step && ts < 2 * step) {
-      float* dst = st + (size_t)(rt * 2 + ts - step) * STATE;
+    if (warp >= step && warp < 2 * step) {
+      float* dst = st + (size_t)(warp - step) * SH::STATE;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) dst[(i * 4 + x) * 32 + lane] = o[i][x];
-      if (t == 0) {
-        dst[16 * D + gr] = m[0];
-        dst[16 * D + 8 + gr] = m[1];
-        dst[16 * D + 16 + gr] = l[0];
-        dst[16 * D + 24 + gr] = l[1];
-      }
+        for (int e = 0; e < E; ++e) {
+          float* part = dst + (rt * E + e) * (8 * D + 16);
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            part[(2 * k) * 32 + lane] = o[rt][k][2 * e];
+            part[(2 * k + 1) * 32 + lane] = o[rt][k][2 * e + 1];
+          }
+          if (t == 0) {
+            part[8 * D + gr] = m[rt][e];
+            part[8 * D + 8 + gr] = l[rt][e];
+          }
+        }
     }
     __syncthreads();
-    if (ts < step) {
-      const float* src = st + (size_t)(rt * 2 + ts) * STATE;
+    if (warp < step) {
+      const float* src = st + (size_t)warp * SH::STATE;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float m2 = src[16 * D + 8 * e + gr], l2 = src[16 * D + 16 + 8 * e + gr];
-        const float mn = fmaxf(m[e], m2), f1 = ex2(m[e] - mn), f2 = ex2(m2 - mn);
-        m[e] = mn;
-        l[e] = l[e] * f1 + l2 * f2;
+      for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int e = 0; e < E; ++e) {
+          const float* part = src + (rt * E + e) * (8 * D + 16);
+          const float m2 = part[8 * D + gr], l2 = part[8 * D + 8 + gr];
+          const float mn = fmaxf(m[rt][e], m2), f1 = ex2(m[rt][e] - mn), f2 = ex2(m2 - mn);
+          m[rt][e] = mn;
+          l[rt][e] = l[rt][e] * f1 + l2 * f2;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            o[i][2 * e + x] = o[i][2 * e + x] * f1 + src[(i * 4 + 2 * e + x) * 32 + lane] * f2;
-      }
+          for (int k = 0; k < NV; ++k) {
+            o[rt][k][2 * e] = o[rt][k][2 * e] * f1 + part[(2 * k) * 32 + lane] * f2;
+            o[rt][k][2 * e + 1] = o[rt][k][2 * e + 1] * f1 + part[(2 * k + 1) * 32 + lane] * f2;
+          }
+        }
     }
     __syncthreads();
   }
-  if (ts != 0) return;
-  // ---- one slice: the output; several: the state, for the joining launch
+  if (warp != 0) return;
+  // ---- one slice: the output; several: the state, for the second launch
   constexpr int SPAN = D / 8;  // dimensions of one column: column n of n-tile i is dimension SPAN n + i
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int row = row_base + rt * 16 + gr + 8 * e;
-    if (row >= rows) continue;
-    if (P.chunks == 1) {
-      const float r = l[e] > 0.f || l[e] != l[e] ? __fdividef(1.f, l[e]) : 0.f;
-      uint16_t* out = P.out + hr[e] * D + 2 * t * SPAN;
+  for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+    for (int e = 0; e < E; ++e) {
+      if (row_base + rt * 16 + gr + 8 * e >= rows) continue;
+      const size_t at = hr[rt][e];
+      const float lsum = l[rt][e];
+      if (P.chunks == 1) {
+        const float r = lsum > 0.f || lsum != lsum ? __fdividef(1.f, lsum) : 0.f;
+        uint16_t* out = P.out + at * D + 2 * t * SPAN;
 #pragma unroll
-        for (int i = 0; i < NV; i += 8) {
-          uint32_t wd[4];
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float f0 = o[i + 2 * k][2 * e + x] * r, f1 = o[i + 2 * k + 1][2 * e + x] * r;
-            wd[k] = P.bf16 ? pack_bf162(f0, f1) : pack_half2(f0, f1);
+          for (int i = 0; i < NV; i += 8) {
+            uint32_t wd[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float f0 = o[rt][i + 2 * k][2 * e + x] * r, f1 = o[rt][i + 2 * k + 1][2 * e + x] * r;
+              wd[k] = P.bf16 ? pack_bf162(f0, f1) : pack_half2(f0, f1);
+            }
+            *reinterpret_cast<uint4*>(out + x * SPAN + i) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
           }
-          *reinterpret_cast<uint4*>(out + x * SPAN + i) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-        }
-      if (t == 0 && P.lse) P.lse[hr[e]] = l[e] == 0.f ? -INFINITY : (log2f(l[e]) + m[e] - kBias) * 0.693147180559945f;
-    } else {
-      float* dst = P.part + (hr[e] * P.chunks + chunk) * D + 2 * t * SPAN;
+        if (t == 0 && P.lse) P.lse[at] = lsum == 0.f ? -INFINITY : (log2f(lsum) + m[rt][e] - kBias) * kLn2;
+      } else {
+        float* dst = P.part + (at * P.chunks + chunk) * D + 2 * t * SPAN;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < NV; i += 4)
-          *reinterpret_cast<float4*>(dst + x * SPAN + i) =
-              make_float4(o[i][2 * e + x], o[i + 1][2 * e + x], o[i + 2][2 * e + x], o[i + 3][2 * e + x]);
-      if (t == 0) P.part_ml[hr[e] * P.chunks + chunk] = make_float2(m[e] - kBias, l[e]);
+          for (int i = 0; i < NV; i += 4)
+            *reinterpret_cast<float4*>(dst + x * SPAN + i) = make_float4(o[rt][i][2 * e + x], o[rt][i + 1][2 * e + x],
+                                                                         o[rt][i + 2][2 * e + x], o[rt][i + 3][2 * e + x]);
+      }
+      if (t == 0 && P.part_ml) P.part_ml[at * P.chunks + chunk] = make_float2(m[rt][e] - kBias, lsum);
     }
-  }
 }
 
-// ---- the slices' states of one row into its output: one warp per (row, head)
-template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttnParams P) {
-  const View& V = P.V;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const Span s = span(V, b);
-  const int at = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int i = at / P.Hq;
-  if (i >= s.n) return;
-  const size_t hr = (size_t)(s.row0 + i) * P.Hq + (at - i * P.Hq);
-  // Slices that the row's group of rows wrote: those before its last row's last token, and slice 0.
-  const int g = P.rows_per_cta, head = (at - i * P.Hq) % P.G;
-  const int row = i * P.G + head;
-  const int last_i = (min((row / g + 1) * g, s.n * P.G) - 1) / P.G;
+// Slices that the CTAs of row (query i, head g of the group) wrote: up to the
+// last token that the rows they share see, and slice 0.
+__device__ __forceinline__ int slices_of(const AttnParams& P, const Span& s, int i, int g) {
+  const int per = P.rows_per_cta;
+  const int last_i = (min(((i * P.G + g) / per + 1) * per, s.n * P.G) - 1) / P.G;
   const int end = min(s.len, s.old + last_i + 1);
-  const int n = end > 0 ? (end + P.chunk - 1) / P.chunk : 1;
-  const float2* ml = P.part_ml + hr * P.chunks;
-  float m = kNone;
-  for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  constexpr int E = D / 32;
-  float acc[E] = {};
-  for (int c = 0; c < n; ++c) {
-    const float2 v = ml[c];
-    const float f = ex2(v.x - m);
-    l = fmaf(v.y, f, l);
-    const float* src = P.part + (hr * P.chunks + c) * D + lane * E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] = fmaf(src[k], f, acc[k]);
-  }
-  const float r = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;
-  uint32_t* out = reinterpret_cast<uint32_t*>(P.out + hr * D + lane * E);
-#pragma unroll
-  for (int k = 0; k < E; k += 2)
-    out[k / 2] = P.bf16 ? pack_bf162(acc[k] * r, acc[k + 1] * r) : pack_half2(acc[k] * r, acc[k + 1] * r);
-  if (lane == 0 && P.lse) P.lse[hr] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945f;
+  return end > 0 ? (end + P.chunk - 1) / P.chunk : 1;
 }
 
-// ---- the weight that each token drew, from the scores and the rows' lse:
-// one thread per (token, KV head), rows in order
-__global__ void __launch_bounds__(256) score_weights_kernel(const AttnParams P) {
+// ---- second launch: blocks below `joins` join the slices of their rows
+// (P.wpr warps per row), the others sum the weights that tokens drew, one thread per four
+// tokens of a (sequence, KV head), rows in order.
+constexpr int kFinishThreads = 256;
+constexpr int kWeightTokens = 4 * kFinishThreads;
+
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams P, int joins) {
+  constexpr int E = D / 32;
+  __shared__ float acc_s[8][D], l_s[8];
+  __shared__ float lse_s[kFewRows];
   const View& V = P.V;
-  const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= P.w_stride) return;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Span s = span(V, b);
-  const size_t at = ((size_t)b * V.Hkv + h) * P.w_stride + j;
-  float sum = 0.f;
-  for (int i = 0; i < s.n; ++i) {
-    // The scores that the row's CTAs wrote end with its group's last visible tile;
-    // what the row itself does not see is -inf there.
-    if (j >= s.len || j > s.old + i) continue;
-    for (int g = 0; g < P.G; ++g) {
-      const size_t hr = (size_t)(s.row0 + i) * P.Hq + h * P.G + g;
-      const float lse = P.lse[hr];
-      sum += lse == -INFINITY ? 0.f : ex2(P.scores[hr * P.score_stride + j] - lse * 1.44269504088896f);
+  grid_dependency_wait();
+  if ((int)blockIdx.x < joins) {
+    const int wpr = P.wpr, sub = warp % wpr;
+    const int at = blockIdx.x * (8 / wpr) + warp / wpr;
+    const int i = at / P.Hq;
+    const bool ok = i < s.n;
+    const size_t hr = (size_t)(s.row0 + (ok ? i : 0)) * P.Hq + (at - i * P.Hq);
+    const int n = ok ? slices_of(P, s, i, (at - i * P.Hq) % P.G) : 0;
+    const float2* ml = P.part_ml + hr * P.chunks;
+    float m = kNone;
+    for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, acc[E] = {};
+#pragma unroll 4
+    for (int c = sub; c < n; c += wpr) {
+      const float2 v = ml[c];
+      const float f = ex2(v.x - m);
+      l = fmaf(v.y, f, l);
+      const float* src = P.part + (hr * P.chunks + c) * D + lane * E;
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc[k] = fmaf(src[k], f, acc[k]);
     }
+    if (wpr > 1) {  // the row's warps, in order
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc_s[warp][lane * E + k] = acc[k];
+      if (lane == 0) l_s[warp] = l;
+      __syncthreads();
+      if (sub) return;
+      for (int x = 1; x < wpr; ++x) {
+        l += l_s[warp + x];
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] += acc_s[warp + x][lane * E + k];
+      }
+    }
+    if (!ok) return;
+    const float r = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(P.out + hr * D + lane * E);
+#pragma unroll
+    for (int k = 0; k < E; k += 2)
+      out[k / 2] = P.bf16 ? pack_bf162(acc[k] * r, acc[k + 1] * r) : pack_half2(acc[k] * r, acc[k + 1] * r);
+    if (lane == 0 && P.lse) P.lse[hr] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
+    return;
   }
-  P.w_out[at] = (P.w_in ? P.w_in[at] : 0.f) + sum;
+  // ---- weights
+  const int blocks = (int)((P.w_stride + kWeightTokens - 1) / kWeightTokens);
+  const int h = ((int)blockIdx.x - joins) / blocks, part = ((int)blockIdx.x - joins) - h * blocks;
+  const int rows = s.n * P.G;  // at most kFewRows
+  if (part * kWeightTokens < s.len)
+    for (int row = warp; row < rows; row += 8) {
+      const int i = row / P.G, g = row - i * P.G;
+      const size_t hr = (size_t)(s.row0 + i) * P.Hq + h * P.G + g;
+      const int n = slices_of(P, s, i, g);
+      const float2* ml = P.part_ml + hr * P.chunks;
+      float m = kNone, l = 0.f;
+      for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int c = lane; c < n; c += 32) l = fmaf(ml[c].y, ex2(ml[c].x - m), l);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
+    }
+  __syncthreads();
+  const size_t head = ((size_t)b * V.Hkv + h) * P.w_stride;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = part * kWeightTokens + k * kFinishThreads + tid;
+    if (j >= P.w_stride) break;
+    float sum = 0.f;
+    // The rows' CTAs wrote every score up to the row's last visible token; what the row does not see
+    // before that (holes) is -inf.
+    const int i0 = max(j - s.old, 0);
+    if (j < s.len) {
+      const float* sc = P.scores + ((size_t)(s.row0 + i0) * P.Hq + h * P.G) * P.score_stride + j;
+      int row = i0 * P.G;
+      for (int i = i0; i < s.n; ++i, sc += (size_t)(P.Hq - P.G) * P.score_stride)
+#pragma unroll 4
+        for (int g = 0; g < P.G; ++g, sc += P.score_stride) sum += ex2(*sc - lse_s[row++]);
+    }
+    P.w_out[head + j] = (P.w_in ? P.w_in[head + j] : 0.f) + sum;
+  }
 }
 
 template <int FMT, int D, int RT>
-tm_status launch_attn(const AttnParams& P, int groups, cudaStream_t s) {
-  using SH = AttnShape<D, RT>;
+tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int groups, cudaStream_t s) {
+  using SH = FewShape<D, RT>;
   static std::atomic<unsigned long long> done{0};
   if (!smem_attr_once(done, reinterpret_cast<const void*>(attn_kernel<FMT, D, RT>), SH::SMEM)) return TM_ERR_CUDA;
   const dim3 grid((unsigned)P.chunks, (unsigned)(P.V.Hkv * groups), (unsigned)P.V.B);
-  attn_kernel<FMT, D, RT><<<grid, SH::THREADS, SH::SMEM, s>>>(P);
+  attn_kernel<FMT, D, RT><<<grid, 32 * kFewWarps, SH::SMEM, s>>>(tmK, tmV, P);
   return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+// A 16-token box of a pool [cells][T][D]; inner rows of D bytes, swizzled over their width.
+static bool pool_map(CUtensorMap* map, void* pool, const View& V, int D) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t cells = (cuuint64_t)(V.pages > 0 ? V.pages : 1) * V.Hkv, T = 1ull << V.t_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, T, cells};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, T * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, 16, 1}, ones[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launch settings and the workspace's layout, from the host fields alone.
 struct Plan {
-  int rt;            // 16-row tiles per CTA of the kernel for few rows; 0: the tcgen05 kernel
+  int rt;            // the kernel for few rows: its row tiles (0, 1, 2; see FewShape); -1: the tcgen05 kernel
   int rows_per_cta;  // rows that share a CTA
   int groups;        // CTAs along the rows
   int chunk, chunks;
@@ -450,23 +629,21 @@ struct Plan {
   size_t part, part_ml, lse, score, bytes;  // offsets, total
 };
 
-constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows
-
 static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   Plan p = {};
   const int G = Hq / V.Hkv;
   const long long rows = (long long)V.max_q * G;
   const long long sms = num_sms(current_device());
-  p.rt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= kFewRows ? 4 : 0;
-  p.rows_per_cta = p.rt ? 16 * p.rt : 256;
+  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= kFewRows ? 2 : -1;
+  p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
   const long long ctas = (long long)V.B * V.Hkv * p.groups;
   long long chunk, least, unit;
-  if (p.rt) {
-    // Enough slices for two waves of CTAs, none shorter than four tiles.
-    const long long slots = sms * (p.rt == 1 ? 3 : p.rt == 2 ? 2 : 1);
+  if (p.rt >= 0) {
+    // Slices for two waves of CTAs, none shorter than two steps per warp.
+    const long long slots = sms * (p.rt < 2 ? 3 : 2);
     unit = kTile;
-    least = 4 * kTile;
+    least = 2 * kTile;
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
   } else {
     // Slices only where the rows alone leave SMs idle.
@@ -483,19 +660,22 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
   const size_t hr = (size_t)V.rows * Hq;
   size_t at = 0;
+  p.scores = weights && p.rt >= 0;
   if (chunks > 1) {
     p.part = at;
     at = al(at + hr * chunks * D * 4);
+  }
+  if (chunks > 1 || p.scores) {
     p.part_ml = at;
     at = al(at + hr * chunks * 8);
   }
   if (weights) {
-    p.lse = at;
-    at = al(at + hr * 4);
-    p.scores = p.rt != 0;
     if (p.scores) {
       p.score = at;
       at = al(at + hr * (((size_t)V.max_len + kTile - 1) / kTile * kTile) * 4);
+    } else {
+      p.lse = at;
+      at = al(at + hr * 4);
     }
   }
   p.bytes = at;
@@ -503,6 +683,19 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
 }
 
 }  // namespace kvb
+
+cudaError_t kvb_attn_error_bits(uint32_t* bits, bool clear) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, kvb::s_err_kvbd, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (clear && v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(kvb::s_err_kvbd, &zero, sizeof(zero));
+  }
+  *bits = v;
+  return e;
+}
+
 }  // namespace w4
 
 using namespace w4;
@@ -529,30 +722,45 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
 }
 
 template <int FMT, int D>
-static tm_status run(const AttnParams& P, const Plan& p, cudaStream_t s, int* launches) {
-  tm_status st = p.rt == 0   ? launch_prefill_attn(P, FMT, D, p.groups, s)
-                 : p.rt == 1 ? launch_attn<FMT, D, 1>(P, p.groups, s)
-                 : p.rt == 2 ? launch_attn<FMT, D, 2>(P, p.groups, s)
-                             : launch_attn<FMT, D, 4>(P, p.groups, s);
+static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cudaStream_t s, int* launches) {
+  const View& V = P.V;
+  tm_status st;
+  if (p.rt < 0) {
+    st = launch_prefill_attn(P, FMT, D, p.groups, s);
+  } else {
+    CUtensorMap tmK, tmV;
+    if (!pool_map(&tmK, cache->k, V, D) || !pool_map(&tmV, cache->v, V, D)) return TM_ERR_CUDA;
+    st = p.rt == 0   ? launch_attn<FMT, D, 0>(tmK, tmV, P, p.groups, s)
+         : p.rt == 1 ? launch_attn<FMT, D, 1>(tmK, tmV, P, p.groups, s)
+                     : launch_attn<FMT, D, 2>(tmK, tmV, P, p.groups, s);
+  }
   if (st != TM_OK) return st;
   *launches = 1;
-  const View& V = P.V;
-  if (P.chunks > 1) {
-    const long long warps = (long long)V.max_q * P.Hq;
-    join_kernel<D><<<dim3((unsigned)((warps + 3) / 4), (unsigned)V.B), 128, 0, s>>>(P);
+  // The second launch: the joins of several slices, and the weights from kept scores.
+  P.wpr = P.chunks >= 16 ? 8 : P.chunks >= 8 ? 4 : 1;
+  const long long per = 8 / P.wpr;
+  const long long joins = P.chunks > 1 ? ((long long)V.max_q * P.Hq + per - 1) / per : 0;
+  const long long sums = p.scores ? (P.w_stride + kWeightTokens - 1) / kWeightTokens * V.Hkv : 0;
+  if (joins + sums > 0x7fffffffll) return TM_ERR_UNSUPPORTED;
+  if (joins + sums > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(joins + sums), (unsigned)V.B, 1);
+    cfg.blockDim = dim3(kFinishThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, finish_kernel<D>, P, (int)joins) != cudaSuccess) return TM_ERR_CUDA;
     ++*launches;
   }
-  if (P.w_out) {
-    if (p.scores) {
-      const dim3 grid((unsigned)((P.w_stride + 255) / 256), (unsigned)V.Hkv, (unsigned)V.B);
-      score_weights_kernel<<<grid, 256, 0, s>>>(P);
-    } else {
-      st = launch_row_weights(P, FMT, D, s);
-      if (st != TM_OK) return st;
-    }
+  if (P.w_out && !p.scores) {
+    st = launch_row_weights(P, FMT, D, s);
+    if (st != TM_OK) return st;
     ++*launches;
   }
-  return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+  return TM_OK;
 }
 
 extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
@@ -583,17 +791,15 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   P.bf16 = dtype == TM_KVB_BF16;
   P.scale_log2 = (scale != 0.f ? scale : cache->D == 64 ? 0.125f : 0.08838834764831845f) * 1.4426950408889634f;
   P.out = static_cast<uint16_t*>(out);
-  P.lse = lse ? lse : w_out ? reinterpret_cast<float*>(ws + p.lse) : nullptr;
+  P.lse = lse ? lse : w_out && !p.scores ? reinterpret_cast<float*>(ws + p.lse) : nullptr;
   P.w_in = w_in;
   P.w_out = w_out;
   P.w_stride = w_stride;
   P.chunk = p.chunk;
   P.chunks = p.chunks;
   P.rows_per_cta = p.rows_per_cta;
-  if (p.chunks > 1) {
-    P.part = reinterpret_cast<float*>(ws + p.part);
-    P.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);
-  }
+  if (p.chunks > 1) P.part = reinterpret_cast<float*>(ws + p.part);
+  if (p.chunks > 1 || p.scores) P.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);
   if (p.scores) {
     P.scores = reinterpret_cast<float*>(ws + p.score);
     P.score_stride = ((long long)V.max_len + kTile - 1) / kTile * kTile;
@@ -601,9 +807,11 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int launches = 0;
   if (cache->format == TM_KVB_INT8)
-    st = cache->D == 64 ? run<TM_KVB_INT8, 64>(P, p, s, &launches) : run<TM_KVB_INT8, 128>(P, p, s, &launches);
+    st = cache->D == 64 ? run<TM_KVB_INT8, 64>(P, p, cache, s, &launches)
+                        : run<TM_KVB_INT8, 128>(P, p, cache, s, &launches);
   else
-    st = cache->D == 64 ? run<TM_KVB_E4M3, 64>(P, p, s, &launches) : run<TM_KVB_E4M3, 128>(P, p, s, &launches);
+    st = cache->D == 64 ? run<TM_KVB_E4M3, 64>(P, p, cache, s, &launches)
+                        : run<TM_KVB_E4M3, 128>(P, p, cache, s, &launches);
   if (st == TM_OK) set_launch_count(launches);
   return st;
 }

@@ -6,6 +6,8 @@
 namespace w4 {
 namespace kvb {
 
+constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows
+
 struct AttnParams {
   View V;
   const uint16_t* Q;
@@ -19,6 +21,7 @@ struct AttnParams {
   long long w_stride;
   int chunk, chunks;  // tokens per slice, slices (by max_len)
   int rows_per_cta;   // rows that share a CTA, and with it their slices
+  int wpr;            // warps per row of the joining launch
   float* part;        // [rows][Hq][chunks][D]
   float2* part_ml;    // [rows][Hq][chunks]: m, l
   float* scores;      // [rows][Hq][score_stride], base-2 logarithms of the unnormalised weights

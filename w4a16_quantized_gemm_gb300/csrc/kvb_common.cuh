@@ -40,7 +40,8 @@ inline tm_status check(const tm_kvb_cache* c, const tm_kvb_batch* b, bool pointe
     return TM_ERR_INVALID_ARG;
   // Row and token indices are 32-bit in the kernels; products with sizes are 64-bit.
   const long long room = (long long)b->table_stride * c->T;
-  if (room > 0x7fffff00ll || b->rows > 0x7fffff00ll) return TM_ERR_UNSUPPORTED;
+  if (room > 0x40000000ll || b->rows > 0x7fffff00ll || (long long)c->pages * c->Hkv > 0x7fffffffll)
+    return TM_ERR_UNSUPPORTED;
   if (b->B > 0 && pointers) {
     if (!c->k || !c->v || !c->ks || !c->vs || !b->table || !b->kv_len) return TM_ERR_INVALID_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->ks, 4) || !aligned(c->vs, 4) ||
