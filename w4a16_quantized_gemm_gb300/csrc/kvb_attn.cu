@@ -59,6 +59,7 @@ struct FewShape {
   static constexpr uint32_t BOX = 16 * D;
   static constexpr uint32_t STAGE = 4 * BOX;  // K of two groups, V of two groups
   static constexpr int STAGES = D == 128 && RT < 2 ? 2 : 3;
+  static constexpr int CTAS = RT == 2 ? 2 : 3;  // per SM, by registers and shared memory
   static constexpr uint32_t RING = kFewWarps * STAGES * STAGE;
   static constexpr int STATE = TILES * E * (8 * D + 16);  // floats of a warp's state
   static constexpr uint32_t BODY = RING > 2 * STATE * 4 ? RING : 2 * STATE * 4;
@@ -69,16 +70,14 @@ struct FewShape {
 
 // d (rows 0 .. 7 of the tile) += a . b with rows 8 .. 15 of a zero.
 __device__ __forceinline__ void mma_top(float& d0, float& d1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  float x, y;
+  [[maybe_unused]] float x, y;
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};\n"
       : "+f"(d0), "+f"(d1), "=f"(x), "=f"(y)
       : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
-  (void)x;
-  (void)y;
 }
 
 template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(32 * kFewWarps)
+__global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
   using SH = FewShape<D, RT>;
   constexpr int TILES = SH::TILES, E = SH::E, S = SH::STAGES;
@@ -234,6 +233,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   }
   const int sg[2] = {sigma<D>(2 * t), sigma<D>(2 * t + 1)};
   const int kr = sigma<D>(gr);
+  float* srow = P.scores + ((size_t)h * V.rows * P.G + (size_t)s.row0 * P.G + row_base + gr) * P.score_stride;
 
   for (int i = 0; i < mine; ++i) {
     const int batch = i >> 4;
@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     }
     const bool alive = mbar_wait(bars + 8 * (i % S), (uint32_t)(i / S) & 1u, abort_flag, &s_err_kvbd);
     if (!__all_sync(0xffffffffu, alive)) break;
-    const uint32_t kt = ring + (i % S) * SH::STAGE, vt = kt + 2 * SH::BOX;
+    // plain shared loads, so that the compiler may bring them forward
+    const uint8_t* kt = smem + (ring - base) + (i % S) * SH::STAGE;
+    const uint8_t* vt = kt + 2 * SH::BOX;
     const int tok0 = j0 + (i * kFewWarps + warp) * kStep;
     float ks[2], lv[2];
     bool there[2];
@@ -259,34 +261,95 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     // ---- scores: rows x 32 tokens
     float sc[TILES][4][2 * E];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-      for (int rt = 0; rt < TILES; ++rt)
+      for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int x = 0; x < 2 * E; ++x) sc[rt][a][x] = 0.f;
+    if constexpr (RT < 2) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int j = 0; j < KS / 4; ++j) {
+          const uint4 x =
+              *reinterpret_cast<const uint4*>(kt + (a >> 1) * SH::BOX + swz<D>(8 * (a & 1) + kr, t + 4 * j));
+          const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t b0, b1;
+            codes_half<FMT>(kw[k], b0, b1);
+            if constexpr (RT == 0)
+              mma_top(sc[0][a][0], sc[0][a][1], qa[4 * j + k][0], qa[4 * j + k][1], b0, b1);
+            else
+              mma_16816(sc[0][a], qa[4 * j + k], b0, b1);
+          }
+        }
+    } else {
+      // the queries' fragments come from shared memory: once for the four 8-token groups
 #pragma unroll
       for (int j = 0; j < KS / 4; ++j) {
-        const uint4 kw = lds128(kt + (a >> 1) * SH::BOX + swz<D>(8 * (a & 1) + kr, t + 4 * j));
-        const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+        uint32_t kw[4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const uint4 x =
+              *reinterpret_cast<const uint4*>(kt + (a >> 1) * SH::BOX + swz<D>(8 * (a & 1) + kr, t + 4 * j));
+          kw[a][0] = x.x;
+          kw[a][1] = x.y;
+          kw[a][2] = x.z;
+          kw[a][3] = x.w;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t b0, b1;
-          codes_half<FMT>(wd[k], b0, b1);
-          if constexpr (RT == 0) {
-            mma_top(sc[0][a][0], sc[0][a][1], qa[4 * j + k][0], qa[4 * j + k][1], b0, b1);
-          } else if constexpr (RT == 1) {
-            mma_16816(sc[0][a], qa[4 * j + k], b0, b1);
-          } else {
+          uint32_t fa[TILES][4];
 #pragma unroll
-            for (int rt = 0; rt < TILES; ++rt) {
-              const uint4 f = lds128(base + SH::Q_OFF + ((rt * KS + 4 * j + k) * 32 + lane) * 16);
-              const uint32_t fa[4] = {f.x, f.y, f.z, f.w};
-              mma_16816(sc[rt][a], fa, b0, b1);
-            }
+          for (int rt = 0; rt < TILES; ++rt) {
+            const uint4 f =
+                *reinterpret_cast<const uint4*>(smem + SH::Q_OFF + ((rt * KS + 4 * j + k) * 32 + lane) * 16);
+            fa[rt][0] = f.x;
+            fa[rt][1] = f.y;
+            fa[rt][2] = f.z;
+            fa[rt][3] = f.w;
+          }
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            uint32_t b0, b1;
+            codes_half<FMT>(kw[a][k], b0, b1);
+#pragma unroll
+            for (int rt = 0; rt < TILES; ++rt) mma_16816(sc[rt][a], fa[rt], b0, b1);
           }
         }
       }
     }
+#pragma unroll
+    for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) sc[rt][a][2 * e + x] *= ks[a >> 1] * mul[rt][e];
+    if (part)
+#pragma unroll
+      for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e]) sc[rt][a][2 * e + x] = -INFINITY;
+    if (P.scores)
+#pragma unroll
+      for (int rt = 0; rt < TILES; ++rt)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (last[rt][e] >= 0) {
+            float* row = srow + (size_t)(rt * 16 + 8 * e) * P.score_stride + tok0;
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[rt][a][2 * e + x];
+          }
     // ---- softmax
     uint32_t pa[TILES][2][2 * E];  // per 16-token group: A fragment
     const float inv[2] = {ex2(-lv[0]), ex2(-lv[1])};
@@ -295,27 +358,9 @@ __global__ void __launch_bounds__(32 * kFewWarps)
       float tm[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        float g0 = -INFINITY, g1 = -INFINITY;
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float v = sc[rt][a][2 * e + x] * (ks[a >> 1] * mul[rt][e]);
-            if (part && (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e])) v = -INFINITY;
-            sc[rt][a][2 * e + x] = v;
-            if (a < 2)
-              g0 = fmaxf(g0, v);
-            else
-              g1 = fmaxf(g1, v);
-          }
-        if (P.scores && last[rt][e] >= 0) {
-          float* row = P.scores + hr[rt][e] * P.score_stride + tok0;
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[rt][a][2 * e + x];
-        }
-        tm[e] = fmaxf(g0 + lv[0], g1 + lv[1]);
+        auto v = [&](int a, int x) { return sc[rt][a][2 * e + x]; };
+        tm[e] = fmaxf(fmaxf(fmaxf(v(0, 0), v(0, 1)), fmaxf(v(1, 0), v(1, 1))) + lv[0],
+                      fmaxf(fmaxf(v(2, 0), v(2, 1)), fmaxf(v(3, 0), v(3, 1))) + lv[1]);
         tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
         tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
       }
@@ -357,15 +402,16 @@ __global__ void __launch_bounds__(32 * kFewWarps)
       for (int q = 0; q < 4; ++q) {
         const int r = 8 * (q >> 1) + sg[q & 1];
         if constexpr (D == 128) {
-          const uint4 x = lds128(vt + g * SH::BOX + swz<D>(r, gr));
+          const uint4 x = *reinterpret_cast<const uint4*>(vt + g * SH::BOX + swz<D>(r, gr));
           wv[q][0] = x.x;
           wv[q][1] = x.y;
           wv[q][2] = x.z;
           wv[q][3] = x.w;
         } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(wv[q][0]), "=r"(wv[q][1])
-                       : "r"(vt + g * SH::BOX + swz<D>(r, gr >> 1) + 8 * (gr & 1)));
+          const uint2 x =
+              *reinterpret_cast<const uint2*>(vt + g * SH::BOX + swz<D>(r, gr >> 1) + 8 * (gr & 1));
+          wv[q][0] = x.x;
+          wv[q][1] = x.y;
         }
         // Slots past the end and the boxes of holes hold anything, NaN codes too.
         if (part && (!there[g] || tok0 + 16 * g + r >= j1))
@@ -576,24 +622,38 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
       if (lane == 0) lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
     }
   __syncthreads();
+  // Four tokens per thread.  The rows' CTAs wrote every score up to the row's last visible token;
+  // what the row does not see before that (holes) is -inf.
   const size_t head = ((size_t)b * V.Hkv + h) * P.w_stride;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int j = part * kWeightTokens + k * kFinishThreads + tid;
-    if (j >= P.w_stride) break;
-    float sum = 0.f;
-    // The rows' CTAs wrote every score up to the row's last visible token; what the row does not see
-    // before that (holes) is -inf.
-    const int i0 = max(j - s.old, 0);
-    if (j < s.len) {
-      const float* sc = P.scores + ((size_t)(s.row0 + i0) * P.Hq + h * P.G) * P.score_stride + j;
-      int row = i0 * P.G;
-      for (int i = i0; i < s.n; ++i, sc += (size_t)(P.Hq - P.G) * P.score_stride)
-#pragma unroll 4
-        for (int g = 0; g < P.G; ++g, sc += P.score_stride) sum += ex2(*sc - lse_s[row++]);
+  const int j = part * kWeightTokens + 4 * tid;
+  if (j >= P.w_stride) return;
+  float sum[4] = {};
+  if (j < s.len) {
+    const int r0 = max(j + 3 - s.old, 0) * P.G;  // rows from here on see all four
+    const float* sc = P.scores + ((size_t)h * V.rows + s.row0) * P.G * P.score_stride + j;
+    if (j + 3 < s.len) {
+      for (int row = max(j - s.old, 0) * P.G; row < min(r0, rows); ++row) {
+        const int seen = s.old + row / P.G - j;  // the last of the four that the row sees
+        for (int k = 0; k <= seen && k < 4; ++k) sum[k] += ex2(sc[row * P.score_stride + k] - lse_s[row]);
+      }
+#pragma unroll 8
+      for (int row = r0; row < rows; ++row) {
+        const float4 x = *reinterpret_cast<const float4*>(sc + row * P.score_stride);
+        const float y = lse_s[row];
+        sum[0] += ex2(x.x - y);
+        sum[1] += ex2(x.y - y);
+        sum[2] += ex2(x.z - y);
+        sum[3] += ex2(x.w - y);
+      }
+    } else {
+      for (int k = 0; k < s.len - j; ++k)
+        for (int row = max(j + k - s.old, 0) * P.G; row < rows; ++row)
+          sum[k] += ex2(sc[row * P.score_stride + k] - lse_s[row]);
     }
-    P.w_out[head + j] = (P.w_in ? P.w_in[head + j] : 0.f) + sum;
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (j + k < P.w_stride) P.w_out[head + j + k] = (P.w_in ? P.w_in[head + j + k] : 0.f) + sum[k];
 }
 
 template <int FMT, int D, int RT>

@@ -24,7 +24,7 @@ struct AttnParams {
   int wpr;            // warps per row of the joining launch
   float* part;        // [rows][Hq][chunks][D]
   float2* part_ml;    // [rows][Hq][chunks]: m, l
-  float* scores;      // [rows][Hq][score_stride], base-2 logarithms of the unnormalised weights
+  float* scores;      // [Hkv][rows x G][score_stride], base-2 logarithms of the unnormalised weights
   long long score_stride;
 };
 

@@ -9,7 +9,7 @@
 //     thread: scores from tensor memory, the running maximum (which moves only
 //     when it has grown by more than 8, so that the output is rarely rescaled), weights
 //     as fp16 back into the columns of the scores;
-//   warps 8-11: codes -> fp16 numbers (exact) in shared memory, K and V tiles in
+//   warps 8-11, 14, 15: codes -> fp16 numbers (exact) in shared memory, K and V tiles in
 //     turn through a ring of four; the next tile's codes are requested while
 //     this one's are converted;
 //   warp 12: S_i = Q_i K^T (A, B in shared memory) and O_i += P_i V (A in tensor
@@ -19,6 +19,8 @@
 // The scales stay out of the products as in the kernel for few rows: ks
 // multiplies the scores, log2 vs joins the exponent and leaves l again.
 // All waits are bounded.
+#include <type_traits>
+
 #include "kvb_attn.h"
 
 namespace w4 {
@@ -28,6 +30,7 @@ static __device__ uint32_t s_err_kvb;
 
 constexpr int kPreThreads = 512;
 constexpr int kPreTile = 128;   // tokens per tile, rows per row tile
+constexpr int kPreConv = 6;     // converting warps
 constexpr int kPreSlots = 4;    // K and V tiles in flight
 constexpr int kPreMeta = 4;     // tiles whose scales are in flight
 constexpr float kPreBias = 6.f;
@@ -114,12 +117,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     }
     mbar_init(o_full, 1);
     for (int i = 0; i < kPreSlots; ++i) {
-      mbar_init(kv_full(i), 4);
+      mbar_init(kv_full(i), kPreConv);
       mbar_init(kv_empty(i), 1);
     }
     for (int i = 0; i < kPreMeta; ++i) {
       mbar_init(meta_full(i), 1);
-      mbar_init(meta_empty(i), 4 + 4 * M);
+      mbar_init(meta_empty(i), kPreConv + 4 * M);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -133,9 +136,81 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // S_0, S_1 (P_i over S_i), then O_0, O_1
 
+  // ---------------- codes -> fp16 tiles ----------------
+  // A converting warp's passes of 4 (D = 64: 8) rows: rows `first`, `first` + `stride`, ...  Warps 8-11 take
+  // three quarters of a tile's rows, warps 14 and 15 the rest.
+  constexpr int kWarpRows = 512 / D;
+  auto convert = [&](auto passes, int first, int stride) {
+    constexpr int PASSES = decltype(passes)::value;
+    // Eight lanes write two rows of one 64-dimension panel: no bank conflicts.
+    const int c4 = lane & 3;
+    const int panel = D == 128 ? (lane >> 3) & 1 : 0;
+    const int r0 = first + ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
+    const int code_off = panel * 64 + c4 * 16;
+    const int items = 2 * N;  // K_0, V_0, K_1, V_1, ...
+    uint4 x[PASSES];
+    int grp[PASSES];  // 16-token groups of the pool that the thread's rows of the tile lie in
+    auto groups = [&](int n) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        grp[p] = (int)lds32(base + SH::META + (n % kPreMeta) * 128 + ((r0 + p * stride) >> 4) * 16 + 12);
+    };
+    auto fetch = [&](int item, int p) {
+      // Rows past the end read as zeros: stale codes may be NaN.
+      const int r = r0 + p * stride;
+      const uint8_t* src = (item & 1 ? V.v : V.k) + (size_t)(unsigned)max(grp[p], 0) * (16 * D) + (r & 15) * D + code_off;
+      x[p] = ldg_or_zero(src, grp[p] >= 0 && j0 + (item >> 1) * kPreTile + r < j1);
+    };
+    bool alive = true;
+    if (items) {
+      alive = wait_bar(meta_full(0), 0, abort_flag, &s_err_kvb);
+      if (__all_sync(0xffffffffu, alive)) {
+        groups(0);
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) fetch(0, p);
+      } else {
+        alive = false;
+      }
+    }
+    for (int item = 0; item < items && alive; ++item) {
+      const int slot = item % kPreSlots;
+      alive = wait_bar(kv_empty(slot), ((uint32_t)(item / kPreSlots) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+      const bool more = item + 1 < items;
+      if (more && !((item + 1) & 1))
+        alive = alive && wait_bar(meta_full(((item + 1) >> 1) % kPreMeta), (uint32_t)(((item + 1) >> 1) / kPreMeta) & 1u,
+                                   abort_flag, &s_err_kvb);
+      if (!__all_sync(0xffffffffu, alive)) {
+        alive = false;
+        break;
+      }
+      if (more && (item & 1)) groups((item + 1) >> 1);
+      const uint32_t dst = base + SH::KV_OFF + slot * SH::TILE + panel * SH::PANEL;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = r0 + p * stride;
+        uint32_t o[8];
+        codes_half<FMT>(x[p].x, o[0], o[1]);
+        codes_half<FMT>(x[p].y, o[2], o[3]);
+        codes_half<FMT>(x[p].z, o[4], o[5]);
+        codes_half<FMT>(x[p].w, o[6], o[7]);
+        if (more) fetch(item + 1, p);
+        const uint32_t at = dst + r * 128;
+        sts128(at + (((2 * c4) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        sts128(at + (((2 * c4 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(kv_full(slot));
+        // Tile n's groups were read into registers before K_n was fetched.
+        if (!(item & 1)) mbar_arrive(meta_empty((item >> 1) % kPreMeta));
+      }
+    }
+  };
+
   if (warp < 8) {
     // ---------------- softmax: one row per thread ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = row_base + i * kPreTile + r;
@@ -149,25 +224,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       // scale is taken into their sign.
       const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;
       const uint16_t* q = P.Q + (s.row0 + qi) * P.q_stride + (long long)(h * P.G + (ok ? row - qi * P.G : 0)) * D;
+      uint4 x[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        x[c] = ok ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
       float up = 1.f;
       if (P.bf16) {
         float m = 0.f;
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
-          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 f = unpack(wd[k], true);
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            m = max3(m, fabsf(f.x), fabsf(f.y));
           }
         }
         const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);
         up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
         mul *= __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
       }
+#pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = ok ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
-        uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+        uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
         if (P.bf16)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -315,77 +394,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       tc_fence_before();
     }
   } else if (warp < 12) {
-    // ---------------- codes -> fp16 tiles ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // A warp's 16-byte chunks of one pass: 2 (or 4) rows x 4 chunks x panels, so that eight lanes
-    // write two rows of one panel (no bank conflicts).
-    constexpr int RPP = D == 128 ? 16 : 32;  // rows per pass of the four warps
-    constexpr int PASSES = kPreTile / RPP;
-    const int c4 = lane & 3;
-    const int panel = D == 128 ? (lane >> 3) & 1 : 0;
-    const int r0 = (warp - 8) * (RPP / 4) + ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
-    const int code_off = panel * 64 + c4 * 16;
-    const int items = 2 * N;  // K_0, V_0, K_1, V_1, ...
-    uint4 x[PASSES];
-    int grp[PASSES];  // 16-token groups of the pool that the thread's rows of the tile lie in
-    auto groups = [&](int n) {
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p)
-        grp[p] = (int)lds32(base + SH::META + (n % kPreMeta) * 128 + ((r0 + p * RPP) >> 4) * 16 + 12);
-    };
-    auto fetch = [&](int item, int p) {
-      // Rows past the end read as zeros: stale codes may be NaN.
-      const int r = r0 + p * RPP;
-      const uint8_t* src = (item & 1 ? V.v : V.k) + (size_t)(unsigned)max(grp[p], 0) * (16 * D) + (r & 15) * D + code_off;
-      x[p] = ldg_or_zero(src, grp[p] >= 0 && j0 + (item >> 1) * kPreTile + r < j1);
-    };
-    bool alive = true;
-    if (items) {
-      alive = wait_bar(meta_full(0), 0, abort_flag, &s_err_kvb);
-      if (__all_sync(0xffffffffu, alive)) {
-        groups(0);
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) fetch(0, p);
-      } else {
-        alive = false;
-      }
-    }
-    for (int item = 0; item < items && alive; ++item) {
-      const int slot = item % kPreSlots;
-      alive = wait_bar(kv_empty(slot), ((uint32_t)(item / kPreSlots) & 1u) ^ 1u, abort_flag, &s_err_kvb);
-      const bool more = item + 1 < items;
-      if (more && !((item + 1) & 1))
-        alive = alive && wait_bar(meta_full(((item + 1) >> 1) % kPreMeta), (uint32_t)(((item + 1) >> 1) / kPreMeta) & 1u,
-                                   abort_flag, &s_err_kvb);
-      if (!__all_sync(0xffffffffu, alive)) {
-        alive = false;
-        break;
-      }
-      if (more && (item & 1)) groups((item + 1) >> 1);
-      const uint32_t dst = base + SH::KV_OFF + slot * SH::TILE + panel * SH::PANEL;
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int r = r0 + p * RPP;
-        uint32_t o[8];
-        codes_half<FMT>(x[p].x, o[0], o[1]);
-        codes_half<FMT>(x[p].y, o[2], o[3]);
-        codes_half<FMT>(x[p].z, o[4], o[5]);
-        codes_half<FMT>(x[p].w, o[6], o[7]);
-        if (more) fetch(item + 1, p);
-        const uint32_t at = dst + r * 128;
-        sts128(at + (((2 * c4) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-        sts128(at + (((2 * c4 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(kv_full(slot));
-        // Tile n's groups were read into registers before K_n was fetched.
-        if (!(item & 1)) mbar_arrive(meta_empty((item >> 1) % kPreMeta));
-      }
-    }
+    convert(std::integral_constant<int, D == 128 ? 6 : 3>{}, (warp - 8) * kWarpRows, 4 * kWarpRows);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
       // ---------------- MMA issuer ----------------
       // The whole warp walks the loop, so that descriptors and addresses stay uniform; one lane issues.
@@ -457,6 +469,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
         }
       }
       __syncwarp();
+    } else if (warp >= 14) {
+      convert(std::integral_constant<int, D == 128 ? 4 : 2>{}, 96 + (warp - 14) * kWarpRows, 2 * kWarpRows);
     } else if (warp == 13) {
       // ---------------- pages and scales ----------------
       for (int n = 0; n < N; ++n) {
