@@ -606,21 +606,31 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
   const int blocks = (int)((P.w_stride + kWeightTokens - 1) / kWeightTokens);
   const int h = ((int)blockIdx.x - joins) / blocks, part = ((int)blockIdx.x - joins) - h * blocks;
   const int rows = s.n * P.G;  // at most kFewRows
-  if (part * kWeightTokens < s.len)
-    for (int row = warp; row < rows; row += 8) {
-      const int i = row / P.G, g = row - i * P.G;
-      const size_t hr = (size_t)(s.row0 + i) * P.Hq + h * P.G + g;
-      const int n = slices_of(P, s, i, g);
-      const float2* ml = P.part_ml + hr * P.chunks;
+  if (part * kWeightTokens < s.len) {
+    // lse of every row at once: eight threads per row, 32 rows at a time
+    for (int row = tid >> 3; row < (rows + 31) / 32 * 32; row += 32) {
       float m = kNone, l = 0.f;
-      for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
+      if (row < rows) {
+        const int i = row / P.G, g = row - i * P.G;
+        const int n = slices_of(P, s, i, g);
+        const float2* ml = P.part_ml + ((size_t)(s.row0 + i) * P.Hq + h * P.G + g) * P.chunks;
+        for (int c = tid & 7; c < n; c += 8) {
+          const float2 v = ml[c];
+          const float mn = fmaxf(m, v.x);
+          l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
+          m = mn;
+        }
+      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      for (int c = lane; c < n; c += 32) l = fmaf(ml[c].y, ex2(ml[c].x - m), l);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
+      for (int o = 1; o < 8; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        const float mn = fmaxf(m, m2);
+        l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
+        m = mn;
+      }
+      if ((tid & 7) == 0 && row < rows) lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
     }
+  }
   __syncthreads();
   // Four tokens per thread.  The rows' CTAs wrote every score up to the row's last visible token;
   // what the row does not see before that (holes) is -inf.
@@ -766,7 +776,7 @@ static tm_status check_heads(const View& V, const tm_kvb_batch* batch, int Hq) {
   const bool one_each = batch->q_start == nullptr;
   if (one_each && (batch->rows != batch->B || (batch->B > 0 && batch->max_q < 1))) return TM_ERR_INVALID_ARG;
   const long long rows = (long long)V.max_q * (Hq / V.Hkv);
-  if (rows > 4000000ll || (long long)V.B * V.Hkv > 0x7fffffffll) return TM_ERR_UNSUPPORTED;  // the grid's limits
+  if (rows > 4000000ll || (long long)V.B * V.Hkv > 0x1fffffffll) return TM_ERR_UNSUPPORTED;  // the grid's limits
   return TM_OK;
 }
 

@@ -22,6 +22,7 @@ struct AttnParams {
   int chunk, chunks;  // tokens per slice, slices (by max_len)
   int rows_per_cta;   // rows that share a CTA, and with it their slices
   int wpr;            // warps per row of the joining launch
+  int split;          // CTAs that share a token tile's rows (kvb_weights.cu)
   float* part;        // [rows][Hq][chunks][D]
   float2* part_ml;    // [rows][Hq][chunks]: m, l
   float* scores;      // [Hkv][rows x G][score_stride], base-2 logarithms of the unnormalised weights

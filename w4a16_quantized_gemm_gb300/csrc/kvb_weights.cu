@@ -1,13 +1,14 @@
 // The weight that each token of the paged 8-bit KV cache drew from many rows:
 // w_j += sum over rows of 2^(s_j - lse), the scores once more, on tcgen05.
 //
-// The scores stand transposed: a CTA takes 128 tokens of one (sequence, KV
+// The scores stand transposed: a cluster takes 128 tokens of one (sequence, KV
 // head), their codes exact in fp16 (or bf16, after the queries' type) as the A
 // operand in tensor memory, and all rows that see them, 128 at a time as the B
-// operand in shared memory -- the queries' own bits, no scaling.  A thread of
-// the epilogue owns one token and half of the rows' columns, so the sum needs no
-// exchange but one at the end and has a fixed order; a compensated sum joins the
-// row tiles (a long prompt adds tens of thousands of terms).
+// operand in shared memory -- the queries' own bits, no scaling -- its CTAs
+// taking the row tiles in turn.  A thread of the epilogue owns one token and
+// half of the rows' columns, so the sum needs no exchange but one at the end and
+// has a fixed order; a compensated sum joins the row tiles (a long prompt adds
+// tens of thousands of terms).
 //   warps 0-7: epilogue, warps w and w + 4 on the same tokens;
 //   warps 8-11: query rows by 16-byte asynchronous copies, three tiles ahead, and their lse;
 //   warp 12: the products, scores double-buffered in tensor memory.
@@ -22,12 +23,13 @@ static __device__ uint32_t s_err_kvbw;
 constexpr int kWtThreads = 416;
 constexpr int kWtTile = 128;  // tokens per CTA, rows per tile
 constexpr int kWtSlots = 3;
+constexpr int kWtSplit = 2;   // CTAs that share a token tile's rows: early tokens are seen by all, late ones by few
 
 template <int D>
 struct WtShape {
   static constexpr uint32_t PANEL = kWtTile * 128;
   static constexpr uint32_t TILE = D / 64 * PANEL;
-  static constexpr uint32_t ROWS = kWtSlots * TILE;              // [slots][128] x lse (base 2; +inf: no row)
+  static constexpr uint32_t ROWS = kWtSlots * TILE;              // [slots][128] x -lse (base 2; -inf: no row)
   static constexpr uint32_t LAST = ROWS + kWtSlots * 128 * 4;    // [slots][128] x last visible token
   static constexpr uint32_t SUMS = LAST + kWtSlots * 128 * 4;    // [128]
   static constexpr uint32_t BARS = SUMS + 128 * 4;
@@ -41,14 +43,17 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
   const View& V = P.V;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int bh = blockIdx.x / P.split, b = bh / V.Hkv, h = bh - b * V.Hkv;
+  const int share = blockIdx.x - bh * P.split;  // this CTA's place in its cluster
   const int tok0 = blockIdx.y * kWtTile;
   const Span s = span(V, b);
   const int rows = s.n * P.G;
   const int first = max(tok0 - s.old, 0);  // the first query that sees a token of the tile
   const int r0 = first < s.n ? first * P.G : rows;
-  const int N = tok0 < s.len && r0 < rows ? (rows - r0 + kWtTile - 1) / kWtTile : 0;
+  const int tiles = tok0 < s.len && r0 < rows ? (rows - r0 + kWtTile - 1) / kWtTile : 0;
+  const int N = (tiles - share + P.split - 1) / P.split;  // tiles share, share + split, ... are this CTA's
+  auto first_row = [&](int n) { return r0 + (n * P.split + share) * kWtTile; };
 
   const uint32_t bars = base + SH::BARS;
   auto q_full = [&](int i) { return bars + 8 * i; };
@@ -59,9 +64,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 96);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 100);
   const size_t out = ((size_t)b * V.Hkv + h) * P.w_stride;
-  if (N == 0) {  // nothing is added here
+  if (tiles == 0) {  // nothing is added here (the whole cluster leaves)
     const int j = tok0 + tid;
-    if (tid < kWtTile && j < P.w_stride) P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
+    if (share == 0 && tid < kWtTile && j < P.w_stride) P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
     return;
   }
   if (tid == 0) {
@@ -120,6 +125,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       if (lane == 0) mbar_arrive(a_full);
     }
     const float c = page >= 0 ? V.ks[cell] * P.scale_log2 : 0.f;
+    const uint64_t c2 = f32x2(c, c);
     float sum = 0.f, lost = 0.f;
     for (int n = 0; n < N; ++n) {
       const int slot = n % kWtSlots;
@@ -134,29 +140,34 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_empty(n & 1));
-      const uint32_t row = base + SH::ROWS + slot * 512 + 256 * half;
-      float part[4] = {};
-      if (s.old + (r0 + n * kWtTile) / P.G >= tok0 + kWtTile - 1) {
+      const uint8_t* row = smem + SH::ROWS + slot * 512 + 256 * half;
+      uint64_t part[4] = {};
+      if (s.old + first_row(n) / P.G >= tok0 + kWtTile - 1) {
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
-          const uint4 l = lds128(row + 4 * k);
-          part[0] += ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, -__uint_as_float(l.x)));
-          part[1] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, -__uint_as_float(l.y)));
-          part[2] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 2]), c, -__uint_as_float(l.z)));
-          part[3] += ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 3]), c, -__uint_as_float(l.w)));
+          const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
+          const uint32_t* x = &v[k >> 5][k & 31];
+          const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, l.x));
+          const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, l.y));
+          part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
+          part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
         }
       } else {
-        const uint32_t last = base + SH::LAST + slot * 512 + 256 * half;
+        const uint8_t* last = smem + SH::LAST + slot * 512 + 256 * half;
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float p = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, -__uint_as_float(lds32(row + 4 * k))));
-          part[k & 3] += j <= (int)lds32(last + 4 * k) ? p : 0.f;
+        for (int k = 0; k < 64; k += 2) {
+          const float2 l = *reinterpret_cast<const float2*>(row + 4 * k);
+          const int2 see = *reinterpret_cast<const int2*>(last + 4 * k);
+          const float p0 = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x));
+          const float p1 = ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y));
+          part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(j <= see.x ? p0 : 0.f, j <= see.y ? p1 : 0.f));
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty(slot));
       // sum += the tile's, with what rounding drops carried along (Kahan)
-      const float y = __fadd_rn(__fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])), -lost);
+      const float2 all = f32x2_get(add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3])));
+      const float y = __fadd_rn(__fadd_rn(all.x, all.y), -lost);
       const float t = __fadd_rn(sum, y);
       lost = __fadd_rn(__fadd_rn(t, -sum), -y);
       sum = t;
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     float* sums = reinterpret_cast<float*>(smem + SH::SUMS);
     if (half == 1) sums[r] = sum;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (half == 0 && j < P.w_stride) P.w_out[out + j] = (P.w_in ? P.w_in[out + j] : 0.f) + (page >= 0 ? sum + sums[r] : 0.f);
+    if (half == 0) sums[r] += sum;
     tc_fence_before();
   } else if (warp < 12) {
     // ---------------- query rows ----------------
@@ -175,10 +186,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     // A thread's rows are RPP apart: (query, head) and its address move by constants, with a carry.
     const int G = P.G, dq = RPP / G, dg = RPP - dq * G;
     const long long step = dq * P.q_stride + (long long)dg * D, carry = P.q_stride - (long long)G * D;
-    int row = r0 + rr, g = row % G;
+    int row = first_row(0) + rr, g = row % G;
     const uint16_t* src = P.Q + (long long)(s.row0 + row / G) * P.q_stride + (long long)(h * G + g) * D + 8 * c;
-    int lrow = r0 + t, li = lrow / G, lg = lrow - li * G;  // the row whose lse the thread fetches
-    const int ldq = kWtTile / G, ldg = kWtTile - ldq * G;
+    int lrow = first_row(0) + t, li = lrow / G, lg = lrow - li * G;  // the row whose lse the thread fetches
+    const int hop = P.split * kWtTile, ldq = hop / G, ldg = hop - ldq * G;
+    const int jump = hop - kWtTile, jq = jump / G, jg = jump - jq * G;  // from a tile's end to the next one's start
     bool alive = true;
     auto issue = [&](int n) {
       if (n < N) {
@@ -200,12 +212,19 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
               src += carry;
             }
           }
+          row += jump;
+          g += jg;
+          src += jq * P.q_stride + (long long)jg * D;
+          if (g >= G) {
+            g -= G;
+            src += carry;
+          }
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + SH::ROWS + slot * 512 + 4 * t),
-                       "f"(x != -INFINITY ? x * 1.44269504088896f : INFINITY)
+                       "f"(x != -INFINITY ? x * -1.44269504088896f : -INFINITY)
                        : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::LAST + slot * 512 + 4 * t), "r"(last) : "memory");
         }
-        lrow += kWtTile;
+        lrow += hop;
         li += ldq;
         lg += ldg;
         if (lg >= G) {
@@ -226,37 +245,65 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       issue(n + 2);
     }
     cp_wait<0>();
-  } else if (lane == 0) {
+  } else {
     // ---------------- products ----------------
     constexpr uint32_t id = idesc_f16_f32(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
-    bool alive = wait_bar(a_full, 0, abort_flag, &s_err_kvbw);
+    const uint32_t lead = elect_one(), tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq = smem_desc_sw128(base);
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvbw)) != 0;
+    };
+    bool alive = wait_all(a_full, 0);
     for (int n = 0; n < N && alive; ++n) {
       const int slot = n % kWtSlots;
-      alive = wait_bar(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
-              wait_bar(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
+      alive = wait_all(q_full(slot), (uint32_t)(n / kWtSlots) & 1u) &&
+              wait_all(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u);
       if (!alive) break;
       tc_fence_after();
+      const uint64_t db = dq + (uint64_t)slot * (SH::TILE >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        tc_mma_f16_ta(tmem + 128 + 128 * (n & 1), tmem + 8 * k,
-                      smem_desc_sw128(base + slot * SH::TILE + (k >> 2) * SH::PANEL + (k & 3) * 32), id, k > 0);
-      tc_commit(s_full(n & 1));
-      tc_commit(q_empty(slot));
+        mma_ts_if(lead, tm0 + 128 + 128 * (n & 1), tm0 + 8 * k,
+                  db + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
+      commit_if(lead, s_full(n & 1));
+      commit_if(lead, q_empty(slot));
     }
-    tc_commit(done);
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(done, 0)) {
-      if (globaltimer() - t0 > kWaitLimitNs) {
-        atomicOr(&s_err_kvbw, kErrTimeout);
-        break;
+    commit_if(lead, done);
+    if (lead) {
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try_wait(done, 0)) {
+        if (globaltimer() - t0 > kWaitLimitNs) {
+          atomicOr(&s_err_kvbw, kErrTimeout);
+          break;
+        }
       }
     }
+    __syncwarp();
   }
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // ---- the cluster's sums, in order
+  __syncwarp();
+  cluster_sync_all();
+  const int j = tok0 + tid;
+  if (share == 0 && tid < kWtTile && j < P.w_stride) {
+    const bool there = j < s.len && page_of(V, V.table, b, V.table_stride, j >> V.t_shift) >= 0;
+    float sum = 0.f;
+    for (int c = 0; c < P.split; ++c) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(v)
+                   : "r"(map_shared_rank(base + SH::SUMS + 4 * tid, c))
+                   : "memory");
+      sum += v;
+    }
+    P.w_out[out + j] = (P.w_in ? P.w_in[out + j] : 0.f) + (there ? sum : 0.f);
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
 template <int FMT, int D, bool BF16>
@@ -264,9 +311,21 @@ static tm_status launch(const AttnParams& P, cudaStream_t stream) {
   using SH = WtShape<D>;
   static std::atomic<unsigned long long> done{0};
   if (!smem_attr_once(done, reinterpret_cast<const void*>(weights_kernel<FMT, D, BF16>), SH::SMEM)) return TM_ERR_CUDA;
-  const dim3 grid((unsigned)(P.V.B * P.V.Hkv), (unsigned)((P.w_stride + kWtTile - 1) / kWtTile));
-  weights_kernel<FMT, D, BF16><<<grid, kWtThreads, SH::SMEM, stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+  AttnParams Q = P;
+  Q.split = kWtSplit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(P.V.B * P.V.Hkv * Q.split), (unsigned)((P.w_stride + kWtTile - 1) / kWtTile), 1);
+  cfg.blockDim = dim3(kWtThreads, 1, 1);
+  cfg.dynamicSmemBytes = SH::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)Q.split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_kernel<FMT, D, BF16>, Q) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
 }
 
 template <int FMT, int D>
