@@ -125,11 +125,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     for (int v = tid; v < earlier; v += kAppendThreads) {
       uint2* at = reinterpret_cast<uint2*>(codes + ((size_t)v << 3));
       uint2 c = *at;
-      uint64_t lo, hi;
-      decode4<FMT>(c.x, lo, hi);
-      c.x = encode4<FMT>(mul_f32x2(lo, was2), mul_f32x2(hi, was2), by);
-      decode4<FMT>(c.y, lo, hi);
-      c.y = encode4<FMT>(mul_f32x2(lo, was2), mul_f32x2(hi, was2), by);
+      c.x = recode4<FMT>(c.x, was2, by);
+      c.y = recode4<FMT>(c.y, was2, by);
       *at = c;
     }
   }

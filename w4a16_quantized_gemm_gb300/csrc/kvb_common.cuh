@@ -170,6 +170,12 @@ __device__ __forceinline__ uint64_t divide(uint64_t x, const Divisor& d) {
   return fma_f32x2(fma_f32x2(t, d.s, x), d.i, t);
 }
 
+// To the nearest e4m3 codes, ties to even, saturating.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
 // Codes of four quotients x / s with |x| at most the largest code times s (to
 // its rounding): to the nearest, ties to even.  int8: adding 1.5 2^23 leaves the
 // rounded integer in the low byte.
@@ -184,9 +190,19 @@ __device__ __forceinline__ uint32_t encode4(uint64_t lo, uint64_t hi, const Divi
   }
   // the correction loses the sign of a zero
   const float2 a = f32x2_get(ql), b = f32x2_get(qh), xa = f32x2_get(lo), xb = f32x2_get(hi);
-  const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(copysignf(a.x, xa.x), copysignf(a.y, xa.y)), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(copysignf(b.x, xb.x), copysignf(b.y, xb.y)), __NV_SATFINITE, __NV_E4M3);
-  return l | (h << 16);
+  return e4m3x4(make_float2(copysignf(a.x, xa.x), copysignf(a.y, xa.y)),
+                make_float2(copysignf(b.x, xb.x), copysignf(b.y, xb.y)));
+}
+
+// Codes of (c s) / s' for the four codes c of a word: a page's new scale.  e4m3
+// goes by magnitude, the signs stay.
+template <int FMT>
+__device__ __forceinline__ uint32_t recode4(uint32_t w, uint64_t s, const Divisor& d) {
+  uint64_t lo, hi;
+  decode4<FMT>(FMT == TM_KVB_INT8 ? w : w & 0x7f7f7f7fu, lo, hi);
+  if (FMT == TM_KVB_INT8) return encode4<FMT>(mul_f32x2(lo, s), mul_f32x2(hi, s), d);
+  const float2 a = f32x2_get(divide(mul_f32x2(lo, s), d)), b = f32x2_get(divide(mul_f32x2(hi, s), d));
+  return e4m3x4(a, b) | (w & 0x80808080u);
 }
 
 // The scale that values up to `a` need: a times the binary32 reciprocal of the

@@ -115,18 +115,27 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
         if (j < cached) keys[j - s0] = rank_of(j, x[i], page[i]);
       }
     }
-    auto key = [&](int j) { return j < cached ? keys[j - s0] : rank_of(j, w[j], table[j >> V.t_shift]); };
+    // A slice's keys in shared memory first, then those that are computed again each time.
+    auto far_key = [&](int j) { return rank_of(j, w[j], table[j >> V.t_shift]); };
+    auto key = [&](int j) { return j < cached ? keys[j - s0] : far_key(j); };
+    const bool near = cached == s1;  // all in shared memory
     uint32_t prefix = 0u, mask = 0u, want = (uint32_t)count;
     if (tid < 256) hist[0][tid] = hist[1][tid] = 0u;
     __syncthreads();
     for (int shift = 24; shift >= 0; shift -= 8) {
       uint32_t* mine = hist[(shift >> 3) & 1];
-#pragma unroll 4
-      for (int j = s0 + warp * 32; j < s1; j += kEvictThreads) {
-        const uint32_t k = j + lane < s1 ? key(j + lane) : 0u;
-        const bool in = j + lane < s1 && (k & mask) == prefix;
-        if (in) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+      auto count_key = [&](uint32_t k) {
+        if ((k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+      };
+      const int whole = (cached - s0) / 4 * 4;
+      for (int j = 4 * tid; j < whole; j += 4 * kEvictThreads) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
+        count_key(k.x);
+        count_key(k.y);
+        count_key(k.z);
+        count_key(k.w);
       }
+      for (int j = s0 + whole + tid; j < s1; j += kEvictThreads) count_key(key(j));
       barrier();
       // Thread t < 256 holds digit 255 - t: from the largest keys down.
       uint32_t n = 0u, upto = 0u;
@@ -165,11 +174,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     const int w0 = min(s1, s0 + warp * sub), w1 = min(s1, w0 + sub);
     const uint32_t before = (1u << lane) - 1u;
     uint32_t gt = 0u, eq = 0u;
-#pragma unroll 4
-    for (int j = w0; j < w1; j += 32) {
-      const uint32_t k = j + lane < w1 ? key(j + lane) : 0u;
+    auto tally = [&](int j, uint32_t k) {
       gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > prefix));
       eq += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k == prefix));
+    };
+    if (near) {
+#pragma unroll 4
+      for (int j = w0; j < w1; j += 32) tally(j, j + lane < w1 ? keys[j + lane - s0] : 0u);
+    } else {
+      for (int j = w0; j < w1; j += 32) tally(j, j + lane < w1 ? key(j + lane) : 0u);
     }
     if (lane == 0) {
       warp_gt[warp] = gt;
@@ -188,10 +201,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       gt += warp_gt[i];
       eq += warp_eq[i];
     }
-#pragma unroll 4
-    for (int j = w0; j < w1; j += 32) {
+    auto emit = [&](int j, uint32_t k) {
       const bool in = j + lane < w1;
-      const uint32_t k = in ? key(j + lane) : 0u;
       const uint32_t mg = __ballot_sync(0xffffffffu, in && k > prefix);
       const uint32_t me = __ballot_sync(0xffffffffu, in && k == prefix);
       const uint32_t g = gt + __popc(mg & before), e = eq + __popc(me & before);
@@ -202,6 +213,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       }
       gt += __popc(mg);
       eq += __popc(me);
+    };
+    if (near) {
+#pragma unroll 4
+      for (int j = w0; j < w1; j += 32) emit(j, j + lane < w1 ? keys[j + lane - s0] : 0u);
+    } else {
+      for (int j = w0; j < w1; j += 32) emit(j, j + lane < w1 ? key(j + lane) : 0u);
     }
   } else {
     for (int j = (int)rank * kEvictThreads + tid; j < L; j += C * kEvictThreads) kept[j] = j;
@@ -291,9 +308,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
           const uint64_t s2 = f32x2(s, s);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint64_t lo, hi;
-            decode4<FMT>(wd[k], lo, hi);
-            wd[k] = encode4<FMT>(mul_f32x2(lo, s2), mul_f32x2(hi, s2), by);
+            wd[k] = recode4<FMT>(wd[k], s2, by);
           }
           *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
         }
