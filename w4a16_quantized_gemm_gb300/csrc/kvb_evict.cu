@@ -20,11 +20,13 @@ namespace kvb {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kStage = 131072;   // most bytes of tokens staged per CTA: a warp per page of up to 8 KB, 8 warps above
+constexpr int kStage = 65536;  // bytes of tokens staged per CTA: a warp per page (two CTAs fit an SM; 128 KB was slower)
 constexpr int kLocalKeys = 8192;  // sequences up to this long: every CTA of the cluster selects for itself, which costs
                                   // less than the cluster barriers of a shared selection
 constexpr int kMaxCluster = 8;
 constexpr int kKeyCap = 16384;  // most keys of a CTA's slice held in shared memory (64 KB); the rest are read again
+
+static_assert(kKeyCap * 4 <= kStage, "the keys and the tokens share their place");
 
 struct EvictParams {
   View V;
@@ -347,7 +349,7 @@ tm_status launch_evict(EvictParams P, cudaStream_t stream) {
   if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), kStage + 2 * kLocalKeys)) return TM_ERR_CUDA;
   // CTAs per cluster: as many as the pages or the keys can use, while all clusters fit the GPU at once.
   const long long T = 1ll << V.t_shift, heads = (long long)V.B * V.Hkv;
-  const long long units = 2 * ((P.budget + T - 1) / T), room = 4ll * num_sms(current_device());
+  const long long units = 2 * ((P.budget + T - 1) / T), room = 2ll * num_sms(current_device());
   const int page = (int)T << P.d_shift;
   P.move_warps = kStage / page < kEvictWarps ? kStage / page : kEvictWarps;
   int C = 1;
