@@ -12,7 +12,8 @@
 // In place: kept tokens move to lower slots in their order, so a new page reads
 // only from pages at or after itself.  Pages go in waves of increasing index;
 // within a wave every read comes before the barrier and every write after it,
-// and no later wave reads what an earlier one wrote.  No workspace, one launch.
+// and no later wave reads what an earlier one wrote.  Into fresh
+// pages nothing waits.  No workspace, one launch.
 #include "kvb_common.cuh"
 
 namespace w4 {
@@ -241,6 +242,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   float* rs = row_scale[warp];
   uint32_t* ra = row_at[warp];
   const int units = 2 * ((count + T - 1) >> V.t_shift), wave = C * P.move_warps;
+  // In place: a new page that is the old page of its block, or the weights over themselves.  (A page that
+  // serves another block of the call may not be a destination.)  Otherwise no wave has to wait.
+  bool shared_place = P.w_out == P.w;
+  for (int i = tid; i < units / 2 && i < V.table_stride; i += kEvictThreads)
+    shared_place |= V.table[(size_t)b * V.table_stride + i] == P.dst_table[(size_t)b * P.dst_stride + i];
+  shared_place = __syncthreads_or(shared_place);
   for (int u0 = 0; u0 < units; u0 += wave) {
     const int u = warp < P.move_warps ? u0 + (int)rank * P.move_warps + warp : units;
     const int blk = u >> 1, sel = u & 1;
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       }
       __syncwarp();
     }
-    cluster_barrier();
+    if (shared_place) cluster_barrier();
     if (u < units) {
       if (sel == 0)
 #pragma unroll

@@ -1,17 +1,16 @@
 // The weight that each token of the paged 8-bit KV cache drew from many rows:
 // w_j += sum over rows of 2^(s_j - lse), the scores once more, on tcgen05.
 //
-// The scores stand transposed: a cluster takes 128 tokens of one (sequence, KV
-// head), their codes exact in fp16 (or bf16, after the queries' type) as the A
-// operand in tensor memory, and all rows that see them, 128 at a time as the B
+// The scores stand transposed: a cluster takes 2 x 128 tokens of one (sequence,
+// KV head), their codes exact in fp16 (or bf16, after the queries' type) as the A
+// operands in tensor memory, and all rows that see them, 128 at a time as the B
 // operand in shared memory -- the queries' own bits, no scaling -- its CTAs
-// taking the row tiles in turn.  A thread of the epilogue owns one token and
-// half of the rows' columns, so the sum needs no exchange but one at the end and
-// has a fixed order; a compensated sum joins the row tiles (a long prompt adds
-// tens of thousands of terms).
-//   warps 0-7: epilogue, warps w and w + 4 on the same tokens;
+// taking the row tiles in turn.  A thread of the epilogue owns one token, so
+// the sum needs no exchange but the cluster's at the end and has a fixed order;
+// a compensated sum joins the row tiles (a long prompt adds tens of thousands of terms).
+//   warps 0-3, 4-7: epilogue of the first and the second token tile;
 //   warps 8-11: query rows by 16-byte asynchronous copies, three tiles ahead, and their lse;
-//   warp 12: the products, scores double-buffered in tensor memory.
+//   warp 12: the products: one token tile's scores while the other's are summed.
 // Bound by the exponentials and the tensor cores about equally.
 #include "kvb_attn.h"
 
@@ -21,7 +20,8 @@ namespace kvb {
 static __device__ uint32_t s_err_kvbw;
 
 constexpr int kWtThreads = 416;
-constexpr int kWtTile = 128;  // tokens per CTA, rows per tile
+constexpr int kWtTile = 128;    // tokens per token tile, rows per row tile
+constexpr int kWtTokens = 256;  // tokens per CTA: two tiles, so that a row tile is fetched for both
 constexpr int kWtSlots = 3;
 constexpr int kWtSplit = 2;   // CTAs that share a token tile's rows: early tokens are seen by all, late ones by few
 
@@ -31,8 +31,8 @@ struct WtShape {
   static constexpr uint32_t TILE = D / 64 * PANEL;
   static constexpr uint32_t ROWS = kWtSlots * TILE;              // [slots][128] x -lse (base 2; -inf: no row)
   static constexpr uint32_t LAST = ROWS + kWtSlots * 128 * 4;    // [slots][128] x last visible token
-  static constexpr uint32_t SUMS = LAST + kWtSlots * 128 * 4;    // [128]
-  static constexpr uint32_t BARS = SUMS + 128 * 4;
+  static constexpr uint32_t SUMS = LAST + kWtSlots * 128 * 4;    // [256]
+  static constexpr uint32_t BARS = SUMS + kWtTokens * 4;
   static constexpr uint32_t SMEM = BARS + 128 + 1024;
 };
 
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int bh = blockIdx.x / P.split, b = bh / V.Hkv, h = bh - b * V.Hkv;
   const int share = blockIdx.x - bh * P.split;  // this CTA's place in its cluster
-  const int tok0 = blockIdx.y * kWtTile;
+  const int tok0 = blockIdx.y * kWtTokens;
   const Span s = span(V, b);
   const int rows = s.n * P.G;
   const int first = max(tok0 - s.old, 0);  // the first query that sees a token of the tile
@@ -54,6 +54,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   const int tiles = tok0 < s.len && r0 < rows ? (rows - r0 + kWtTile - 1) / kWtTile : 0;
   const int N = (tiles - share + P.split - 1) / P.split;  // tiles share, share + split, ... are this CTA's
   auto first_row = [&](int n) { return r0 + (n * P.split + share) * kWtTile; };
+  // Whether some row of tile n sees the second token tile at all; once it does, later ones do.
+  auto second = [&](int n) {
+    const int last_i = (min(first_row(n) + kWtTile, rows) - 1) / P.G;
+    return tok0 + kWtTile < s.len && s.old + last_i >= tok0 + kWtTile;
+  };
 
   const uint32_t bars = base + SH::BARS;
   auto q_full = [&](int i) { return bars + 8 * i; };
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   const size_t out = ((size_t)b * V.Hkv + h) * P.w_stride;
   if (tiles == 0) {  // nothing is added here (the whole cluster leaves)
     const int j = tok0 + tid;
-    if (share == 0 && tid < kWtTile && j < P.w_stride) P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
+    if (share == 0 && tid < kWtTokens && j < P.w_stride) P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
     return;
   }
   if (tid == 0) {
@@ -76,9 +81,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(s_empty(i), 8);
+      mbar_init(s_empty(i), 4);
     }
-    mbar_init(a_full, 4);
+    mbar_init(a_full, 8);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -90,15 +95,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // A in columns 0 .. D/2 - 1, scores from 128 and 256
+  const uint32_t tmem = *tmem_slot;  // A_0, A_1 (D/2 columns each) from 0 and 64, scores from 128 and 256
 
   if (warp < 8) {
-    // ---------------- one token per thread, columns 64 half .. 64 half + 63 ----------------
-    const int half = warp >> 2, r = tid & 127, j = tok0 + r;
+    // ---------------- one token per thread: warps 0-3 the first tile's, 4-7 the second's ----------------
+    const int half = warp >> 2, j = tok0 + tid;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int page = j < s.len ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
     const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
-    if (half == 0) {
+    {
       const uint8_t* src = V.k + ((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) * D;
 #pragma unroll
       for (int c = 0; c < D; c += 64) {
@@ -117,7 +122,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
             const float2 f = unpack(o[k], false);
             o[k] = pack_bf162(f.x, f.y);
           }
-        tc_st_32x32b_x32(tmem + lanes + c / 2, o);
+        tc_st_32x32b_x32(tmem + lanes + 64 * half + c / 2, o);
       }
       tc_wait_st();
       tc_fence_before();
@@ -127,40 +132,53 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
     const float c = page >= 0 ? V.ks[cell] * P.scale_log2 : 0.f;
     const uint64_t c2 = f32x2(c, c);
     float sum = 0.f, lost = 0.f;
+    int seen = 0;  // row tiles that this token tile took part in
     for (int n = 0; n < N; ++n) {
       const int slot = n % kWtSlots;
-      bool alive = wait_bar(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw) &&
-                   wait_bar(s_full(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag, &s_err_kvbw);
+      bool alive = wait_bar(q_full(slot), (uint32_t)(n / kWtSlots) & 1u, abort_flag, &s_err_kvbw);
+      const bool mine = half == 0 || second(n);
+      if (mine) alive = alive && wait_bar(s_full(half), (uint32_t)seen & 1u, abort_flag, &s_err_kvbw);
       if (!__all_sync(0xffffffffu, alive)) break;
+      if (!mine) {
+        if (lane == 0) mbar_arrive(q_empty(slot));
+        continue;
+      }
+      ++seen;
       tc_fence_after();
-      uint32_t v[2][32];
-      tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * (n & 1) + 64 * half, v[0]);
-      tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * (n & 1) + 64 * half + 32, v[1]);
-      tc_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_empty(n & 1));
-      const uint8_t* row = smem + SH::ROWS + slot * 512 + 256 * half;
+      const bool whole = s.old + first_row(n) / P.G >= tok0 + kWtTile * half + kWtTile - 1;  // every row sees every token
       uint64_t part[4] = {};
-      if (s.old + first_row(n) / P.G >= tok0 + kWtTile - 1) {
-#pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
-          const uint32_t* x = &v[k >> 5][k & 31];
-          const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, l.x));
-          const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, l.y));
-          part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
-          part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
+#pragma unroll 1
+      for (int x0 = 0; x0 < 128; x0 += 64) {  // 64 rows at a time: 128 scores would not fit the registers
+        uint32_t v[2][32];
+        tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * half + x0, v[0]);
+        tc_ld_32x32b_x32(tmem + lanes + 128 + 128 * half + x0 + 32, v[1]);
+        tc_wait_ld();
+        if (x0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_empty(half));
         }
-      } else {
-        const uint8_t* last = smem + SH::LAST + slot * 512 + 256 * half;
+        const uint8_t* row = smem + SH::ROWS + slot * 512 + 4 * x0;
+        if (whole) {
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          const float2 l = *reinterpret_cast<const float2*>(row + 4 * k);
-          const int2 see = *reinterpret_cast<const int2*>(last + 4 * k);
-          const float p0 = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x));
-          const float p1 = ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y));
-          part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(j <= see.x ? p0 : 0.f, j <= see.y ? p1 : 0.f));
+          for (int k = 0; k < 64; k += 4) {
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
+            const uint32_t* x = &v[k >> 5][k & 31];
+            const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, l.x));
+            const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, l.y));
+            part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
+            part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
+          }
+        } else {
+          const uint8_t* last = smem + SH::LAST + slot * 512 + 4 * x0;
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            const float2 l = *reinterpret_cast<const float2*>(row + 4 * k);
+            const int2 see = *reinterpret_cast<const int2*>(last + 4 * k);
+            const float p0 = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x));
+            const float p1 = ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y));
+            part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(j <= see.x ? p0 : 0.f, j <= see.y ? p1 : 0.f));
+          }
         }
       }
       __syncwarp();
@@ -172,10 +190,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       lost = __fadd_rn(__fadd_rn(t, -sum), -y);
       sum = t;
     }
-    float* sums = reinterpret_cast<float*>(smem + SH::SUMS);
-    if (half == 1) sums[r] = sum;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (half == 0) sums[r] += sum;
+    reinterpret_cast<float*>(smem + SH::SUMS)[tid] = sum;
     tc_fence_before();
   } else if (warp < 12) {
     // ---------------- query rows ----------------
@@ -254,18 +269,24 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvbw)) != 0;
     };
     bool alive = wait_all(a_full, 0);
+    int seen[2] = {0, 0};
     for (int n = 0; n < N && alive; ++n) {
       const int slot = n % kWtSlots;
-      alive = wait_all(q_full(slot), (uint32_t)(n / kWtSlots) & 1u) &&
-              wait_all(s_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u);
-      if (!alive) break;
-      tc_fence_after();
+      alive = wait_all(q_full(slot), (uint32_t)(n / kWtSlots) & 1u);
       const uint64_t db = dq + (uint64_t)slot * (SH::TILE >> 4);
+      const int tiles_here = second(n) ? 2 : 1;
+      for (int i = 0; i < tiles_here && alive; ++i) {
+        alive = wait_all(s_empty(i), ((uint32_t)seen[i] & 1u) ^ 1u);
+        if (!alive) break;
+        ++seen[i];
+        tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ts_if(lead, tm0 + 128 + 128 * (n & 1), tm0 + 8 * k,
-                  db + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
-      commit_if(lead, s_full(n & 1));
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts_if(lead, tm0 + 128 + 128 * i, tm0 + 64 * i + 8 * k,
+                    db + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
+        commit_if(lead, s_full(i));
+      }
+      if (!alive) break;
       commit_if(lead, q_empty(slot));
     }
     commit_if(lead, done);
@@ -289,7 +310,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   __syncwarp();
   cluster_sync_all();
   const int j = tok0 + tid;
-  if (share == 0 && tid < kWtTile && j < P.w_stride) {
+  if (share == 0 && tid < kWtTokens && j < P.w_stride) {
     const bool there = j < s.len && page_of(V, V.table, b, V.table_stride, j >> V.t_shift) >= 0;
     float sum = 0.f;
     for (int c = 0; c < P.split; ++c) {
@@ -314,7 +335,7 @@ static tm_status launch(const AttnParams& P, cudaStream_t stream) {
   AttnParams Q = P;
   Q.split = kWtSplit;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(P.V.B * P.V.Hkv * Q.split), (unsigned)((P.w_stride + kWtTile - 1) / kWtTile), 1);
+  cfg.gridDim = dim3((unsigned)(P.V.B * P.V.Hkv * Q.split), (unsigned)((P.w_stride + kWtTokens - 1) / kWtTokens), 1);
   cfg.blockDim = dim3(kWtThreads, 1, 1);
   cfg.dynamicSmemBytes = SH::SMEM;
   cfg.stream = stream;
