@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
 
   if (warp < 8) {
     // ---------------- softmax: one row per thread ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = row_base + i * kPreTile + r;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       tc_fence_before();
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     convert(std::integral_constant<int, D == 128 ? 6 : 3>{}, (warp - 8) * kWarpRows, 4 * kWarpRows);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
