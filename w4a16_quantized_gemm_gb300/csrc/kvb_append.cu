@@ -7,6 +7,8 @@
 // tokens keeps the larger of its scale and the one that the new tokens need;
 // where it grows, the earlier codes are rounded anew (each page sees that a few
 // times while it fills: the maximum of a growing set rises ever more rarely).
+#include <type_traits>
+
 #include "kvb_common.cuh"
 
 namespace w4 {
@@ -19,7 +21,6 @@ struct AppendParams {
   const uint16_t* x[2];  // keys, values
   long long stride[2];   // elements per token
   int d_shift;           // log2 D
-  int bf16;
   float* w;
   long long w_stride;
 };
@@ -28,13 +29,27 @@ struct AppendParams {
 __device__ __forceinline__ float finite(float x, float top) {
   return x != x ? 0.f : fminf(fmaxf(x, -top), top);
 }
-__device__ __forceinline__ uint64_t values(uint32_t w, int bf16, bool clean, float top) {
-  const float2 f = unpack(w, bf16);
-  return clean ? f32x2(f.x, f.y) : f32x2(finite(f.x, top), finite(f.y, top));
+
+// Codes of the four values of two words.  CLEAN: none is an infinity or NaN.
+// e4m3 goes by magnitude: the signs are the high bits of the four high bytes.
+template <int FMT, bool BF16, bool CLEAN>
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, const Divisor& by, float top) {
+  const uint32_t signs = FMT == TM_KVB_E4M3 ? prmt(a, b, 0x7531u) & 0x80808080u : 0u;
+  if (FMT == TM_KVB_E4M3) {
+    a &= 0x7fff7fffu;
+    b &= 0x7fff7fffu;
+  }
+  float2 x = unpack(a, BF16), y = unpack(b, BF16);
+  if (!CLEAN) {
+    x = make_float2(finite(x.x, top), finite(x.y, top));
+    y = make_float2(finite(y.x, top), finite(y.y, top));
+  }
+  if (FMT == TM_KVB_INT8) return encode4<FMT>(f32x2(x.x, x.y), f32x2(y.x, y.y), by);
+  return e4m3x4(f32x2_get(divide(f32x2(x.x, x.y), by)), f32x2_get(divide(f32x2(y.x, y.y), by))) | signs;
 }
 
 // VECS: vectors of 8 values per thread, enough for the new tokens of one page.
-template <int FMT, int VECS>
+template <int FMT, bool BF16, int VECS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
   __shared__ uint32_t warp_max[kAppendThreads / 32];
   const View& V = P.V;
@@ -56,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int vec_shift = P.d_shift - 3;  // vectors of 8 values per token
   const int total = (hi - lo) << vec_shift;
   const uint16_t* src = P.x[sel] + (s.row0 + (long long)(lo - s.old)) * P.stride[sel] + ((long long)h << P.d_shift);
-  const float top = P.bf16 ? 3.3895313892515355e38f : 65504.f;
+  const float top = BF16 ? 3.3895313892515355e38f : 65504.f;
   uint4 x[VECS];
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
@@ -83,8 +98,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
-  const bool clean = m < (P.bf16 ? 0x7f80u : 0x7c00u);
-  float a = unpack(m, P.bf16).x;
+  const bool clean = m < (BF16 ? 0x7f80u : 0x7c00u);
+  float a = unpack(m, BF16).x;
   if (!clean) {  // uniform: the largest finite magnitude, an infinity counting as `top`
     float f = 0.f;
 #pragma unroll
@@ -92,8 +107,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = f32x2_get(values(wd[k], P.bf16, false, top));
-        f = fmaxf(f, fmaxf(fabsf(v.x), fabsf(v.y)));
+        const float2 v = unpack(wd[k], BF16);
+        f = fmaxf(f, fmaxf(fabsf(finite(v.x, top)), fabsf(finite(v.y, top))));
       }
     }
     m = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
@@ -110,15 +125,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 
   uint8_t* codes = (sel ? V.v : V.k) + ((cell << V.t_shift) << P.d_shift);
   uint8_t* dst = codes + ((size_t)(lo - begin) << P.d_shift);
+  auto store = [&](auto is_clean) {
 #pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    const int v = tid + i * kAppendThreads;
-    if (v >= total) break;
-    uint2 c;
-    c.x = encode4<FMT>(values(x[i].x, P.bf16, clean, top), values(x[i].y, P.bf16, clean, top), by);
-    c.y = encode4<FMT>(values(x[i].z, P.bf16, clean, top), values(x[i].w, P.bf16, clean, top), by);
-    *reinterpret_cast<uint2*>(dst + ((size_t)v << 3)) = c;
-  }
+    for (int i = 0; i < VECS; ++i) {
+      const int v = tid + i * kAppendThreads;
+      if (v >= total) break;
+      uint2 c;
+      c.x = codes4<FMT, BF16, decltype(is_clean)::value>(x[i].x, x[i].y, by, top);
+      c.y = codes4<FMT, BF16, decltype(is_clean)::value>(x[i].z, x[i].w, by, top);
+      *reinterpret_cast<uint2*>(dst + ((size_t)v << 3)) = c;
+    }
+  };
+  if (clean)
+    store(std::true_type{});
+  else
+    store(std::false_type{});
   if (continued && now > was) {
     const int earlier = (lo - begin) << vec_shift;
     const uint64_t was2 = f32x2(was, was);
@@ -132,16 +153,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
 }
 
-template <int FMT>
+template <int FMT, bool BF16>
 void launch_append(const AppendParams& P, dim3 grid, int vecs, cudaStream_t s) {
   if (vecs <= 1)
-    append_kernel<FMT, 1><<<grid, kAppendThreads, 0, s>>>(P);
+    append_kernel<FMT, BF16, 1><<<grid, kAppendThreads, 0, s>>>(P);
   else if (vecs <= 2)
-    append_kernel<FMT, 2><<<grid, kAppendThreads, 0, s>>>(P);
+    append_kernel<FMT, BF16, 2><<<grid, kAppendThreads, 0, s>>>(P);
   else if (vecs <= 4)
-    append_kernel<FMT, 4><<<grid, kAppendThreads, 0, s>>>(P);
+    append_kernel<FMT, BF16, 4><<<grid, kAppendThreads, 0, s>>>(P);
   else
-    append_kernel<FMT, 8><<<grid, kAppendThreads, 0, s>>>(P);
+    append_kernel<FMT, BF16, 8><<<grid, kAppendThreads, 0, s>>>(P);
 }
 
 }  // namespace kvb
@@ -168,7 +189,6 @@ extern "C" tm_status tm_kvb_append(const tm_kvb_cache* cache, const tm_kvb_batch
   P.stride[0] = k_stride;
   P.stride[1] = v_stride;
   P.d_shift = cache->D == 64 ? 6 : 7;
-  P.bf16 = dtype == TM_KVB_BF16;
   P.w = w;
   P.w_stride = w_stride;
   // Pages that max_q consecutive tokens can touch.
@@ -176,10 +196,11 @@ extern "C" tm_status tm_kvb_append(const tm_kvb_cache* cache, const tm_kvb_batch
   const dim3 grid((unsigned)(2 * pages), (unsigned)V.Hkv, (unsigned)V.B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int vecs = ((cache->T < V.max_q ? cache->T : V.max_q) * cache->D / 8 + kAppendThreads - 1) / kAppendThreads;
+  const bool bf16 = dtype == TM_KVB_BF16;
   if (cache->format == TM_KVB_INT8)
-    launch_append<TM_KVB_INT8>(P, grid, vecs, s);
+    bf16 ? launch_append<TM_KVB_INT8, true>(P, grid, vecs, s) : launch_append<TM_KVB_INT8, false>(P, grid, vecs, s);
   else
-    launch_append<TM_KVB_E4M3>(P, grid, vecs, s);
+    bf16 ? launch_append<TM_KVB_E4M3, true>(P, grid, vecs, s) : launch_append<TM_KVB_E4M3, false>(P, grid, vecs, s);
   if (cudaGetLastError() != cudaSuccess) return TM_ERR_CUDA;
   set_launch_count(1);
   return TM_OK;

@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
   __shared__ float lse_s[kFewRows];
   const View& V = P.V;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Span s = span(V, b);
+  const Span s = span(V, b);  // written before the first launch began
   grid_dependency_wait();
   if ((int)blockIdx.x < joins) {
     const int wpr = P.wpr, sub = warp % wpr;

@@ -178,7 +178,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
 
 // Codes of four quotients x / s with |x| at most the largest code times s (to
 // its rounding): to the nearest, ties to even.  int8: adding 1.5 2^23 leaves the
-// rounded integer in the low byte.
+// rounded integer in the low byte.  e4m3: of magnitudes (the correction loses a zero's sign).
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(uint64_t lo, uint64_t hi, const Divisor& d) {
   const uint64_t ql = divide(lo, d), qh = divide(hi, d);
@@ -188,10 +188,7 @@ __device__ __forceinline__ uint32_t encode4(uint64_t lo, uint64_t hi, const Divi
     return prmt(prmt(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040u),
                 prmt(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040u), 0x5410u);
   }
-  // the correction loses the sign of a zero
-  const float2 a = f32x2_get(ql), b = f32x2_get(qh), xa = f32x2_get(lo), xb = f32x2_get(hi);
-  return e4m3x4(make_float2(copysignf(a.x, xa.x), copysignf(a.y, xa.y)),
-                make_float2(copysignf(b.x, xb.x), copysignf(b.y, xb.y)));
+  return e4m3x4(f32x2_get(ql), f32x2_get(qh));
 }
 
 // Codes of (c s) / s' for the four codes c of a word: a page's new scale.  e4m3
