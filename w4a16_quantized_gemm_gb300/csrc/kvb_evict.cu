@@ -14,6 +14,11 @@
 // within a wave every read comes before the barrier and every write after it,
 // and no later wave reads what an earlier one wrote.  Into fresh
 // pages nothing waits.  No workspace, one launch.
+//
+// Measured: 8 heads, 2304 -> 2048 tokens 18.6 us (a chain of latencies: key loads 1 us, four
+// rounds of histogram and scan 5 us, gather 4 us, requantising 4 us on 64 SMs); 32 x 8 heads, up
+// to 4001 -> 1000 tokens, e4m3, 50 us, 2.7 TB/s of what has to move (issue slots 62 %: arithmetic on
+// codes); 2 x 8 heads, 131072 -> 4096, 48 us (16 k keys per CTA through shared-memory histograms).
 #include "kvb_common.cuh"
 
 namespace w4 {
@@ -22,8 +27,11 @@ namespace kvb {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kStage = 65536;  // bytes of tokens staged per CTA: a warp per page (two CTAs fit an SM; 128 KB was slower)
-constexpr int kLocalKeys = 8192;  // sequences up to this long: every CTA of the cluster selects for itself, which costs
-                                  // less than the cluster barriers of a shared selection
+// Every CTA of a cluster selects for itself up to half of this many tokens, a
+// cluster of one up to all: that costs less than the cluster barriers of a shared selection (8 heads, to
+// 2048 kept, alone against shared: 2304 tokens 18.7 / 20.7 us, 8192 tokens 22.8 / 20.8, 16000 tokens
+// 28.8 / 22.8; 32 x 8 heads of 8000 tokens in clusters of one 55.6 / 58.3).
+constexpr int kLocalKeys = 8192;
 constexpr int kMaxCluster = 8;
 constexpr int kKeyCap = 16384;  // most keys of a CTA's slice held in shared memory (64 KB); the rest are read again
 
@@ -43,7 +51,8 @@ struct EvictParams {
   int d_shift;
   int move_warps;
   int list_off;  // shared memory: the list of a local selection, behind the keys and the tokens
-  int key_cap;  // keys of a slice held in shared memory
+  int key_cap;     // keys of a slice held in shared memory
+  int local_keys;  // tokens up to which a CTA selects alone
 };
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
@@ -85,7 +94,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   const float* w = P.w + head * P.w_stride;
   int* kept = P.kept + head * P.budget;
 
-  const bool local = L <= kLocalKeys;
+  const bool local = L <= P.local_keys;
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + P.list_off);  // the kept, of a local selection
   if (L > count) {
     // ---------------- selection ----------------
@@ -354,7 +363,8 @@ tm_status launch_evict(EvictParams P, cudaStream_t stream) {
   const View& V = P.V;
   static std::atomic<unsigned long long> done{0};
   if (!smem_attr_once(done, reinterpret_cast<const void*>(evict_kernel<FMT>), kStage + 2 * kLocalKeys)) return TM_ERR_CUDA;
-  // CTAs per cluster: as many as the pages or the keys can use, while all clusters fit the GPU at once.
+  // CTAs per cluster: as many as the pages or the keys can use, while two CTAs per SM hold all clusters
+  // (32 x 8 heads of 4001 tokens: clusters of one 59 us, of two 66, of four 81 at the time).
   const long long T = 1ll << V.t_shift, heads = (long long)V.B * V.Hkv;
   const long long units = 2 * ((P.budget + T - 1) / T), room = 2ll * num_sms(current_device());
   const int page = (int)T << P.d_shift;
@@ -362,8 +372,10 @@ tm_status launch_evict(EvictParams P, cudaStream_t stream) {
   int C = 1;
   while (C < kMaxCluster && heads * 2 * C <= room && (units > C * 8 || V.max_len > C * 4096ll)) C *= 2;
   if (units < P.move_warps * C) P.move_warps = (int)((units + C - 1) / C);
-  const long long slice = (V.max_len + C - 1) / C + kEvictThreads, alone = V.max_len < kLocalKeys ? V.max_len : kLocalKeys;
-  const long long most = V.max_len <= kLocalKeys || slice < alone ? alone : slice;
+  P.local_keys = C == 1 ? kLocalKeys : kLocalKeys / 2;
+  const long long slice = (V.max_len + C - 1) / C + kEvictThreads;
+  const long long alone = V.max_len < P.local_keys ? V.max_len : P.local_keys;
+  const long long most = V.max_len <= P.local_keys || slice < alone ? alone : slice;
   P.key_cap = (int)(most < kKeyCap ? most : kKeyCap);
   const size_t stage = (size_t)P.move_warps * page, keys = (size_t)P.key_cap * 4;
   cudaLaunchConfig_t cfg = {};
