@@ -356,3 +356,45 @@ def test_prompt_with_holes_and_negative_scale():
     run_attention(c, [150, 90], 8, "fp16", "prompt/holes", scale=-0.1)
     run_attention(c, [2, 2], 8, "fp16", "draft/holes", scale=-0.1)
     assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,new", [(40, 1, 1), (64, 1, 1), (100, 1, 1), (13, 1, 4), (24, 2, 2), (22, 2, 3), (6, 6, 33)])
+def test_rows_per_head(Hq, Hkv, new, weights):
+    """From 33 to over 64 rows of one KV head: each kernel, with and without the tokens' weights."""
+    c = Cache(f"kvb/rows/{Hq}/{new}", [300, 90], Hkv, 64, 32, "int8")
+    run_attention(c, [new, new], Hq, "bf16", f"rows/{Hq}", weights=weights)
+    assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("new", [2, 70])
+def test_bounds_of_the_host_hold(new):
+    """A sequence longer than max_len is read up to it; rows past max_q are not computed; lengths and row
+    starts out of range stay inside the buffers."""
+    c = Cache("kvb/bounds", [400, 200], 2, 128, 16, "e4m3")
+    blocks, q_start = c.to_device(binding), starts([new, new])
+    Q = rounded(normal("kvb/bounds/q", 2 * new, 4, 128), "fp16")[0].cuda()
+    batch = binding.KVBatch(device(c.table), device(c.kv_len), device(q_start), max_q=new, max_len=144)
+    out = binding.kvb_attention(blocks, batch, Q)
+    (k, ks), (v, vs) = c.pools
+    exact = Q.double().cpu().numpy()
+    # rows past token 144 all see the first 144 tokens
+    for b in range(2):
+        if c.kv_len[b] - new < 144:
+            continue
+        for i in range(new):
+            r = q_start[b] + i
+            one = ref.attention(exact[r:r + 1], k, v, ks, vs, c.table[b:b + 1], np.array([144]), np.array([0, 1]), "e4m3")
+            bo, _, _ = bounds(*one, 128, "fp16")
+            assert np.all(np.abs(out[r].double().cpu().numpy() - one[0][0]) <= bo[0])
+    # wrong numbers on the device: clamped, never followed
+    bad_len = torch.tensor([10 ** 9, -5], dtype=torch.int32, device="cuda")
+    bad_start = torch.tensor([5, 10 ** 9, -3], dtype=torch.int32, device="cuda")
+    batch = binding.KVBatch(device(c.table), bad_len, bad_start, max_q=new)
+    room = c.table.shape[1] * 16
+    w = torch.zeros(2, 2, room, device="cuda")
+    binding.kvb_attention(blocks, batch, Q, w_in=w, w_out=w)
+    binding.kvb_append(blocks, batch, Q[:, :2], Q[:, 2:], w=w)
+    binding.kvb_evict(blocks, batch, w, 40)
+    torch.cuda.synchronize()
+    assert binding.device_error() == 0

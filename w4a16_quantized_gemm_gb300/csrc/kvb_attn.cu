@@ -23,6 +23,12 @@
 // four k-steps take word by word (the queries are read in the same order), and
 // the V fragment's column n holds dimension 16 n + i of n-tile i (D = 128; 8 n + i
 // for 64).  sigma and the swizzle make all shared loads conflict-free.
+//
+// Measured: 32 x up to 4096 tokens, int8, 32 query and 8 KV heads, weights: 64 us for 217 MB of codes (first
+// launch 50, 0.62 of the HBM copy rate); 2 x 131072 tokens, e4m3, 64 query heads: 90 us for 453 MB (first
+// launch 80, 0.83).  Bound by the conversion: 3.8 warp instructions per byte of codes at 12 warps an SM (by
+// registers and shared memory), half of the ALU pipe.  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a
+// step with 12 or 16 warps: 65 to 88 and 96 to 119.
 #include "kvb_attn.h"
 
 namespace w4 {
@@ -76,7 +82,8 @@ __device__ __forceinline__ void mma_top(float& d0, float& d1, uint32_t a0, uint3
       : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-template <int FMT, int D, int RT>
+// KEEP: the scores are kept for the tokens' weights.
+template <int FMT, int D, int RT, bool KEEP>
 __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
   using SH = FewShape<D, RT>;
@@ -338,18 +345,37 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               if (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e]) sc[rt][a][2 * e + x] = -INFINITY;
-    if (P.scores)
+    // The scores for the weights.  With more than 8 rows a swap makes a lane's two tokens neighbours, so that four
+    // lanes write a whole sector (16 x 5 drafts: 65 us, without 68); with 8 its registers cost more (32 x 4096
+    // tokens: 66, without 64).
+    if constexpr (KEEP && RT == 0) {
+      if (last[0][0] >= 0) {
+        float* row = srow + tok0;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[0][a][x];
+      }
+    } else if constexpr (KEEP) {
 #pragma unroll
       for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (last[rt][e] >= 0) {
-            float* row = srow + (size_t)(rt * 16 + 8 * e) * P.score_stride + tok0;
+        for (int e = 0; e < E; ++e) {
+          float* row = srow + (size_t)(rt * 16 + 8 * e) * P.score_stride + tok0 + 2 * t;
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) row[8 * a + sg[x]] = sc[rt][a][2 * e + x];
+          for (int a = 0; a < 4; ++a) {
+            float x = sc[rt][a][2 * e], y = sc[rt][a][2 * e + 1];
+            if constexpr (D == 128) {
+              y = __shfl_xor_sync(0xffffffffu, y, 2);
+            } else {
+              const float z = __shfl_xor_sync(0xffffffffu, t & 1 ? x : y, 1);
+              x = t & 1 ? y : x;
+              y = z;
+            }
+            if (last[rt][e] >= 0) *reinterpret_cast<float2*>(row + 8 * a) = make_float2(x, y);
           }
+        }
+    }
     // ---- softmax
     uint32_t pa[TILES][2][2 * E];  // per 16-token group: A fragment
     const float inv[2] = {ex2(-lv[0]), ex2(-lv[1])};
@@ -666,14 +692,22 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
     if (j + k < P.w_stride) P.w_out[head + j + k] = (P.w_in ? P.w_in[head + j + k] : 0.f) + sum[k];
 }
 
-template <int FMT, int D, int RT>
+template <int FMT, int D, int RT, bool KEEP>
 tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int groups, cudaStream_t s) {
   using SH = FewShape<D, RT>;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(attn_kernel<FMT, D, RT>), SH::SMEM)) return TM_ERR_CUDA;
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(attn_kernel<FMT, D, RT, KEEP>), SH::SMEM)) return TM_ERR_CUDA;
   const dim3 grid((unsigned)P.chunks, (unsigned)(P.V.Hkv * groups), (unsigned)P.V.B);
-  attn_kernel<FMT, D, RT><<<grid, 32 * kFewWarps, SH::SMEM, s>>>(tmK, tmV, P);
+  attn_kernel<FMT, D, RT, KEEP><<<grid, 32 * kFewWarps, SH::SMEM, s>>>(tmK, tmV, P);
   return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+template <int FMT, int D, bool KEEP>
+tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int rt, int groups,
+                      cudaStream_t s) {
+  if (rt == 0) return launch_attn<FMT, D, 0, KEEP>(tmK, tmV, P, groups, s);
+  if (rt == 1) return launch_attn<FMT, D, 1, KEEP>(tmK, tmV, P, groups, s);
+  return launch_attn<FMT, D, 2, KEEP>(tmK, tmV, P, groups, s);
 }
 
 // A 16-token box of a pool [cells][T][D]; inner rows of D bytes, swizzled over their width.
@@ -704,19 +738,22 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   const int G = Hq / V.Hkv;
   const long long rows = (long long)V.max_q * G;
   const long long sms = num_sms(current_device());
-  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= kFewRows ? 2 : -1;
+  // 64 rows (16 sequences x 2000 tokens, 8 heads a group): this kernel 51.5 us, with weights 99.6; the tcgen05
+  // kernel 47.6, with its second pass for the weights 124.  At 32 rows this one takes 39.
+  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (weights ? kFewRows : kFewRows / 2) ? 2 : -1;
   p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
   const long long ctas = (long long)V.B * V.Hkv * p.groups;
   long long chunk, least, unit;
   if (p.rt >= 0) {
-    // Slices for two waves of CTAs, none shorter than two steps per warp.
+    // Slices for two waves of CTAs, none shorter than two steps per warp (2 x 131072 tokens: two waves
+    // 94 us, four 98, eight 101 at the time: starting a CTA costs about 3 us).
     const long long slots = sms * (p.rt < 2 ? 3 : 2);
     unit = kTile;
     least = 2 * kTile;
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
   } else {
-    // Slices only where the rows alone leave SMs idle.
+    // Slices only where the rows alone leave SMs idle (300 tokens over 30000: 182 us; unsliced 574).
     unit = 128;
     least = 512;
     chunk = ctas >= sms ? V.max_len : ((long long)V.max_len * ctas + 2 * sms - 1) / (2 * sms);
@@ -800,14 +837,15 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
   } else {
     CUtensorMap tmK, tmV;
     if (!pool_map(&tmK, cache->k, V, D) || !pool_map(&tmV, cache->v, V, D)) return TM_ERR_CUDA;
-    st = p.rt == 0   ? launch_attn<FMT, D, 0>(tmK, tmV, P, p.groups, s)
-         : p.rt == 1 ? launch_attn<FMT, D, 1>(tmK, tmV, P, p.groups, s)
-                     : launch_attn<FMT, D, 2>(tmK, tmV, P, p.groups, s);
+    st = p.scores ? launch_attn<FMT, D, true>(tmK, tmV, P, p.rt, p.groups, s)
+                  : launch_attn<FMT, D, false>(tmK, tmV, P, p.rt, p.groups, s);
   }
   if (st != TM_OK) return st;
   *launches = 1;
   // The second launch: the joins of several slices, and the weights from kept scores.
-  P.wpr = P.chunks >= 16 ? 8 : P.chunks >= 8 ? 4 : 1;
+  // Eight warps a row where few rows have many slices (128 rows of 57: 91 us in all, with one warp 114), one
+  // otherwise (4096 rows of 8: 39 us, with eight 45).
+  P.wpr = P.chunks >= 8 && (long long)V.rows * P.Hq <= 8 * num_sms(current_device()) ? 8 : 1;
   const long long per = 8 / P.wpr;
   const long long joins = P.chunks > 1 ? ((long long)V.max_q * P.Hq + per - 1) / per : 0;
   const long long sums = p.scores ? (P.w_stride + kWeightTokens - 1) / kWeightTokens * V.Hkv : 0;
