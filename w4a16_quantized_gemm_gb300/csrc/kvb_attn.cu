@@ -24,7 +24,7 @@
 // the V fragment's column n holds dimension 16 n + i of n-tile i (D = 128; 8 n + i
 // for 64).  sigma and the swizzle make all shared loads conflict-free.
 //
-// Measured: 32 x up to 4096 tokens, int8, 32 query and 8 KV heads, weights: 64 us for 217 MB of codes (first
+// Measured: 32 x up to 4096 tokens, int8, 32 query and 8 KV heads, weights: 62 us for 217 MB of codes (first
 // launch 50, 0.62 of the HBM copy rate); 2 x 131072 tokens, e4m3, 64 query heads: 90 us for 453 MB (first
 // launch 80, 0.83).  Bound by the conversion: 3.8 warp instructions per byte of codes at 12 warps an SM (by
 // registers and shared memory), half of the ALU pipe.  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
             for (int x = 0; x < 2; ++x)
               if (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e]) sc[rt][a][2 * e + x] = -INFINITY;
     // The scores for the weights.  With more than 8 rows a swap makes a lane's two tokens neighbours, so that four
-    // lanes write a whole sector (16 x 5 drafts: 65 us, without 68); with 8 its registers cost more (32 x 4096
+    // lanes write a whole sector (16 x 5 drafts: 65 us, without 68 then); with 8 its registers cost more (32 x 4096
     // tokens: 66, without 64).
     if constexpr (KEEP && RT == 0) {
       if (last[0][0] >= 0) {
@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
   constexpr int E = D / 32;
   __shared__ float acc_s[8][D], l_s[8];
   __shared__ float lse_s[kFewRows];
+  __shared__ int see_s[kFewRows];  // the last token that a row sees
   const View& V = P.V;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Span s = span(V, b);  // written before the first launch began
@@ -654,7 +655,10 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
         l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
         m = mn;
       }
-      if ((tid & 7) == 0 && row < rows) lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
+      if ((tid & 7) == 0 && row < rows) {
+        lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
+        see_s[row] = min(s.old + row / P.G, s.len - 1);
+      }
     }
   }
   __syncthreads();
@@ -665,26 +669,27 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
   if (j >= P.w_stride) return;
   float sum[4] = {};
   if (j < s.len) {
-    const int r0 = max(j + 3 - s.old, 0) * P.G;  // rows from here on see all four
+    const int r0 = max(j - s.old, 0) * P.G;  // rows from here on see the first of them,
+    const int r4 = j + 3 < s.len ? min(max(j + 3 - s.old, 0) * P.G, rows) : rows;  // and from here on all four
     const float* sc = P.scores + ((size_t)h * V.rows + s.row0) * P.G * P.score_stride + j;
-    if (j + 3 < s.len) {
-      for (int row = max(j - s.old, 0) * P.G; row < min(r0, rows); ++row) {
-        const int seen = s.old + row / P.G - j;  // the last of the four that the row sees
-        for (int k = 0; k <= seen && k < 4; ++k) sum[k] += ex2(sc[row * P.score_stride + k] - lse_s[row]);
-      }
 #pragma unroll 8
-      for (int row = r0; row < rows; ++row) {
-        const float4 x = *reinterpret_cast<const float4*>(sc + row * P.score_stride);
-        const float y = lse_s[row];
-        sum[0] += ex2(x.x - y);
-        sum[1] += ex2(x.y - y);
-        sum[2] += ex2(x.z - y);
-        sum[3] += ex2(x.w - y);
-      }
-    } else {
-      for (int k = 0; k < s.len - j; ++k)
-        for (int row = max(j + k - s.old, 0) * P.G; row < rows; ++row)
-          sum[k] += ex2(sc[row * P.score_stride + k] - lse_s[row]);
+    for (int row = r0; row < r4; ++row) {
+      const float4 x = *reinterpret_cast<const float4*>(sc + row * P.score_stride);
+      const float y = lse_s[row];
+      const int see = see_s[row] - j;
+      sum[0] += see >= 0 ? ex2(x.x - y) : 0.f;
+      sum[1] += see >= 1 ? ex2(x.y - y) : 0.f;
+      sum[2] += see >= 2 ? ex2(x.z - y) : 0.f;
+      sum[3] += see >= 3 ? ex2(x.w - y) : 0.f;
+    }
+#pragma unroll 8
+    for (int row = r4; row < rows; ++row) {
+      const float4 x = *reinterpret_cast<const float4*>(sc + row * P.score_stride);
+      const float y = lse_s[row];
+      sum[0] += ex2(x.x - y);
+      sum[1] += ex2(x.y - y);
+      sum[2] += ex2(x.z - y);
+      sum[3] += ex2(x.w - y);
     }
   }
 #pragma unroll
