@@ -6,7 +6,7 @@
 namespace w4 {
 namespace kvb {
 
-constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows
+constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows (without weights: half)
 
 struct AttnParams {
   View V;

@@ -9,7 +9,7 @@
 // the sum needs no exchange but the cluster's at the end and has a fixed order;
 // a compensated sum joins the row tiles (a long prompt adds tens of thousands of terms).
 //   warps 0-3, 4-7: epilogue of the first and the second token tile;
-//   warps 8-11: query rows by 16-byte asynchronous copies, three tiles ahead, and their lse;
+//   warps 8-11: query rows by 16-byte asynchronous copies into a ring of three, and their lse;
 //   warp 12: the products: one token tile's scores while the other's are summed.
 //
 // Measured: three prompts of up to 1499 tokens, 64 query and 8 KV heads: 62 us, tensor pipe 27 %, XU
