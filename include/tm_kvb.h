@@ -102,6 +102,7 @@ tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_bat
  *           [B][Hkv][w_stride]: w_out = w_in + the sum of p over the step's
  *           rows and the KV head's query heads.  w_in NULL counts as 0, and
  *           w_out may be w_in.  Summed in a fixed order.  w_stride >= max_len.
+ *           Written where the step has no rows, too.
  *   workspace: device, at least tm_kvb_attention_workspace bytes, 16-byte
  *           aligned (may be NULL where that is 0); calls that can overlap on the GPU need
  *           one each

@@ -1,0 +1,28 @@
+"""Paged 8-bit KV cache: the edges of its calls that need no GPU (made-up device
+addresses: nothing is read through them)."""
+import pytest
+
+from tests.test_kvb_host import A, ALIGN, INVALID, OK, UNSUP, batch, cache
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from w4a16_quantized_gemm_gb300 import binding, build
+    build.build()
+    return binding.load()
+
+
+def attention(lib, c, b, Q=A, qs=1024, Hq=8, out=A, wi=None, wo=None, ws=0, work=None, size=0):
+    return lib.tm_kvb_attention(c, b, Q, qs, Hq, 0, 0.0, out, None, wi, wo, ws, work, size, None)
+
+
+@pytest.mark.parametrize("none", [dict(q_start=A, rows=0), dict(q_start=A, max_q=0)])
+def test_weights_of_a_step_without_rows_are_checked(lib, none):
+    """w_out is written in such a step too, so its size and alignment count."""
+    b = batch(**none)
+    assert attention(lib, cache(), b, Q=None, out=None, wo=A, ws=255) == INVALID  # 256 tokens may be there
+    assert attention(lib, cache(), b, Q=None, out=None, wo=A + 2, ws=256) == ALIGN
+    assert attention(lib, cache(), b, Q=None, out=None, wi=A + 2, wo=A, ws=256) == ALIGN
+    assert attention(lib, cache(), b, Q=None, out=None, wo=A, ws=65536 * 128) == UNSUP
+    assert attention(lib, cache(), b, Q=None, out=None, wi=A, wo=A, ws=256) == OK  # in place: nothing to do
+    assert attention(lib, cache(), b, Q=None, out=None) == OK

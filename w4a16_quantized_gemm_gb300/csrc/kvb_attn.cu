@@ -887,12 +887,20 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   const View& V = P.V;
   if (dtype != TM_KVB_F16 && dtype != TM_KVB_BF16) return TM_ERR_INVALID_ARG;
   if (w_in && !w_out) return TM_ERR_INVALID_ARG;
-  if (V.B == 0 || V.rows == 0 || V.max_q == 0) return TM_OK;
-  if (!Q || !out || q_stride < (long long)Hq * cache->D) return TM_ERR_INVALID_ARG;
+  if (V.B == 0) return TM_OK;
   if (w_out && w_stride < V.max_len) return TM_ERR_INVALID_ARG;
   if (w_out && w_stride > 65535ll * 128) return TM_ERR_UNSUPPORTED;  // the grid's limit
-  if (!aligned(Q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(w_in, 4) ||
-      !aligned(w_out, 4) || !aligned(workspace, 16))
+  if (!aligned(w_in, 4) || !aligned(w_out, 4)) return TM_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (V.rows == 0 || V.max_q == 0) {  // no row draws weight: w_out = w_in
+    if (!w_out || w_out == w_in) return TM_OK;
+    const size_t bytes = (size_t)V.B * V.Hkv * w_stride * 4;
+    const cudaError_t e = w_in ? cudaMemcpyAsync(w_out, w_in, bytes, cudaMemcpyDeviceToDevice, s)
+                               : cudaMemsetAsync(w_out, 0, bytes, s);
+    return e == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+  }
+  if (!Q || !out || q_stride < (long long)Hq * cache->D) return TM_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
     return TM_ERR_ALIGNMENT;
   const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr);
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return TM_ERR_INVALID_ARG;
@@ -917,7 +925,6 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
     P.scores = reinterpret_cast<float*>(ws + p.score);
     P.score_stride = ((long long)V.max_len + kTile - 1) / kTile * kTile;
   }
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int launches = 0;
   if (cache->format == TM_KVB_INT8)
     st = cache->D == 64 ? run<TM_KVB_INT8, 64>(P, p, cache, s, &launches)
