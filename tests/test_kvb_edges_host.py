@@ -1,6 +1,9 @@
 """Paged 8-bit KV cache: the edges of its calls that need no GPU (made-up device
 addresses: nothing is read through them)."""
+import contextlib
+
 import pytest
+import torch
 
 from tests.test_kvb_host import A, ALIGN, INVALID, OK, UNSUP, batch, cache
 
@@ -26,3 +29,34 @@ def test_weights_of_a_step_without_rows_are_checked(lib, none):
     assert attention(lib, cache(), b, Q=None, out=None, wo=A, ws=65536 * 128) == UNSUP
     assert attention(lib, cache(), b, Q=None, out=None, wi=A, wo=A, ws=256) == OK  # in place: nothing to do
     assert attention(lib, cache(), b, Q=None, out=None) == OK
+
+
+def test_memory_made_for_a_call_is_its_streams(monkeypatch):
+    """binding._empty allocates with the given stream current, and records the caller's own."""
+    from w4a16_quantized_gemm_gb300 import binding
+    log = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        log.append(("enter", s))
+        yield
+        log.append(("leave", s))
+
+    class Made:
+        device = "dev"
+
+        def record_stream(self, s):
+            log.append(("record", s))
+
+    def empty(*a, **k):
+        log.append("empty")
+        return Made()
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: ("current", d))
+    monkeypatch.setattr(torch, "empty", empty)
+    assert isinstance(binding._empty(3, torch.uint8, "dev", "side"), Made)
+    assert log == [("enter", "side"), "empty", ("leave", "side"), ("record", ("current", "dev"))]
+    log.clear()
+    binding._empty(3, torch.uint8, "dev", None)
+    assert log == ["empty"]

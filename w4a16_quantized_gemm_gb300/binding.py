@@ -187,6 +187,18 @@ def _dev(t: torch.Tensor, dtype, name: str):
     return t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Device memory for a call on ``stream`` (None: the current one).  It is that stream's own: a block that
+    the current stream gave back may still be in use by work that is pending there, which ``stream`` does not
+    wait for.  The caller may use the tensor on its current stream as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 class PackedWeights:
     """Owns a ``tm_packed`` handle (device memory on the device of ``q``)."""
 
@@ -834,14 +846,9 @@ def _kvb_weights(t: Optional[torch.Tensor], B: int, Hkv: int, name: str):
     return _dev(t, torch.float32, name), shape[2]
 
 
-def _kvb_stream(cache, stream, *made):
-    """The call's stream; what the call allocated is kept for it."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(cache.index)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _kvb_stream(cache, stream):
+    """Handle of the call's stream."""
+    return torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else stream.cuda_stream
 
 
 def kvb_append(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.Tensor, w: Optional[torch.Tensor] = None,
@@ -885,9 +892,8 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
     workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
     qp, qs, dtype, shape = _kvb_rows(Q, None, cache.D, "Q")
     rows, Hq = shape[0], shape[1]
-    made_out = made_ws = None
     if out is None:
-        out = made_out = torch.empty(shape, dtype=Q.dtype, device=Q.device)
+        out = _empty(shape, Q.dtype, Q.device, stream)
     elif out.shape != shape:
         raise ValueError("out must have the shape of Q")
     lp = None
@@ -902,11 +908,11 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
     if workspace is None:
         size = kvb_attention_workspace(cache, batch, Hq, rows, wo is not None)
         if size:
-            workspace = made_ws = torch.empty(size, dtype=torch.uint8, device=Q.device)
+            workspace = _empty(size, torch.uint8, Q.device, stream)
     sp, size = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
     st = (_lib or load()).tm_kvb_attention(cache._ref, batch._rows(rows), qp, qs, Hq, dtype,
                                            0.0 if scale is None else scale, _dev(out, Q.dtype, "out"), lp, wi, wo, no,
-                                           sp, size, _kvb_stream(cache, stream, made_out, made_ws))
+                                           sp, size, _kvb_stream(cache, stream))
     if st:
         raise TMError(st, "tm_kvb_attention")
     return out
@@ -924,15 +930,12 @@ def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, fir
     left as it is."""
     wp, wn = _kvb_weights(w, batch.B, cache.Hkv, "w")
     op, on = (wp, wn) if w_out is None else _kvb_weights(w_out, batch.B, cache.Hkv, "w_out")
-    made = []
     if kept is None:
-        kept = torch.empty((batch.B, cache.Hkv, max(budget, 0)), dtype=torch.int32, device=w.device)
-        made.append(kept)
+        kept = _empty((batch.B, cache.Hkv, max(budget, 0)), torch.int32, w.device, stream)
     elif kept.shape != (batch.B, cache.Hkv, budget):
         raise ValueError("kept must be int32 [B][Hkv][budget]")
     if new_len is None:
-        new_len = torch.empty(batch.B, dtype=torch.int32, device=w.device)
-        made.append(new_len)
+        new_len = _empty(batch.B, torch.int32, w.device, stream)
     elif new_len.shape != (batch.B,):
         raise ValueError("new_len must be int32 [B]")
     dst = batch.table if dst_table is None else dst_table
@@ -940,6 +943,6 @@ def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, fir
         raise ValueError("dst_table must be int32 [B][n]")
     st = load().tm_kvb_evict(cache._ref, batch._ref, _dev(dst, torch.int32, "dst_table"), dst.shape[1], wp, wn, op, on,
                              budget, first, recent, _dev(kept, torch.int32, "kept"),
-                             _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache, stream, *made))
+                             _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache, stream))
     _check(st, "tm_kvb_evict")
     return kept, new_len
