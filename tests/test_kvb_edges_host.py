@@ -1,10 +1,14 @@
 """Paged 8-bit KV cache: the edges of its calls that need no GPU (made-up device
 addresses: nothing is read through them)."""
 import contextlib
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
+from tests.conftest import ROOT
 from tests.test_kvb_host import A, ALIGN, INVALID, OK, UNSUP, batch, cache
 
 
@@ -60,3 +64,16 @@ def test_memory_made_for_a_call_is_its_streams(monkeypatch):
     log.clear()
     binding._empty(3, torch.uint8, "dev", None)
     assert log == ["empty"]
+
+
+def test_a_warp_that_gives_up_waits_for_its_copies(tmp_path):
+    """The few-row kernel's ring: a warp that leaves its loop drains each copy in flight on that copy's own phase."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    exe = str(tmp_path / "ring")
+    subprocess.run([gxx, "-std=c++17", "-Wall", "-Werror", "-I", os.path.join(ROOT, "w4a16_quantized_gemm_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "kvb_ring_check.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    assert [int(n) for n in r.stdout.split()] == [sum(k + 1 for k in range(5 * S + 2)) for S in (2, 3, 4)]

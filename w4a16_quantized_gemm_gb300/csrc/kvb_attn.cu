@@ -30,6 +30,7 @@
 // registers and shared memory), half of the ALU pipe.  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a
 // step with 12 or 16 warps: 65 to 88 and 96 to 119.
 #include "kvb_attn.h"
+#include "kvb_ring.h"
 
 namespace w4 {
 namespace kvb {
@@ -80,6 +81,17 @@ __device__ __forceinline__ void mma_top(float& d0, float& d1, uint32_t a0, uint3
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};\n"
       : "+f"(d0), "+f"(d1), "=f"(x), "=f"(y)
       : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// A warp that gives up at step i of `steps`: none of its copies may land in memory that the join is about to
+// use.  (Inlined, it costs the loop registers: 1 % of the full batch's time.)
+template <int S>
+__device__ __noinline__ void drain_copies(uint32_t bars, int i, int steps) {
+  const unsigned long long t0 = globaltimer();
+  ring_drain<S>(i, steps, [&](int stage, uint32_t parity) {
+    while (!mbar_try_wait(bars + 8 * stage, parity) && globaltimer() - t0 < kWaitLimitNs) {
+    }
+  });
 }
 
 // KEEP: the scores are kept for the tokens' weights.
@@ -144,11 +156,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     const int cell = __shfl_sync(0xffffffffu, ahead ? nxt.cell : cur.cell, from);
     const int slot = __shfl_sync(0xffffffffu, ahead ? nxt.slot : cur.slot, from);
     const uint32_t there = __popc(__ballot_sync(0xffffffffu, cell >= 0 && lane < 2));
-    const uint32_t bar = bars + 8 * (i % S);
+    const uint32_t bar = bars + 8 * ring_stage<S>(i);
     if (lane == 0) mbar_expect_tx(bar, there * 2 * SH::BOX);
     __syncwarp();
     if (lane < 4 && cell >= 0)
-      tma_load_3d(ring + (i % S) * SH::STAGE + lane * SH::BOX, lane < 2 ? &tmK : &tmV, 0, slot, cell, bar);
+      tma_load_3d(ring + ring_stage<S>(i) * SH::STAGE + lane * SH::BOX, lane < 2 ? &tmK : &tmV, 0, slot, cell, bar);
   };
 #pragma unroll
   for (int i = 0; i < S; ++i) issue(i, 0);
@@ -248,10 +260,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
       cur = nxt;
       nxt = load_meta(batch + 1);
     }
-    const bool alive = mbar_wait(bars + 8 * (i % S), (uint32_t)(i / S) & 1u, abort_flag, &s_err_kvbd);
-    if (!__all_sync(0xffffffffu, alive)) break;
+    const bool alive = mbar_wait(bars + 8 * ring_stage<S>(i), ring_parity<S>(i), abort_flag, &s_err_kvbd);
+    if (!__all_sync(0xffffffffu, alive)) {
+      drain_copies<S>(bars, i, mine);
+      break;
+    }
     // plain shared loads, so that the compiler may bring them forward
-    const uint8_t* kt = smem + (ring - base) + (i % S) * SH::STAGE;
+    const uint8_t* kt = smem + (ring - base) + ring_stage<S>(i) * SH::STAGE;
     const uint8_t* vt = kt + 2 * SH::BOX;
     const int tok0 = j0 + (i * kFewWarps + warp) * kStep;
     float ks[2], lv[2];
@@ -462,13 +477,6 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     }
     __syncwarp();  // the stage is read: it may be filled again
     issue(i + S, batch);
-  }
-  if (*abort_flag) {
-    // A wait gave up: no copy may land in memory that the join is about to use.
-    const unsigned long long t0 = globaltimer();
-    for (int i = 0; i < S && i < mine; ++i)
-      while (!mbar_try_wait(bars + 8 * i, 0) && globaltimer() - t0 < kWaitLimitNs) {
-      }
   }
   __syncthreads();
 
