@@ -1,6 +1,7 @@
 """Paged 8-bit KV cache: the edges of its calls that need no GPU (made-up device
 addresses: nothing is read through them)."""
 import contextlib
+import ctypes
 import os
 import shutil
 import subprocess
@@ -77,3 +78,18 @@ def test_a_warp_that_gives_up_waits_for_its_copies(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
     assert [int(n) for n in r.stdout.split()] == [sum(k + 1 for k in range(5 * S + 2)) for S in (2, 3, 4)]
+
+
+def test_calls_with_other_rows_share_no_struct():
+    """One batch in two threads, a workspace query beside a launch: each call sees its own number of rows."""
+    from w4a16_quantized_gemm_gb300 import binding
+    b = binding.KVBatch.__new__(binding.KVBatch)  # without device tensors
+    b.q_start, b.B, b._c = object(), 3, batch(q_start=A)
+    b._ref = ctypes.byref(b._c)
+    refs = {n: b._rows(n) for n in (7, 3, 12, 7)}
+    assert {n: r._obj.rows for n, r in refs.items()} == {7: 7, 3: 3, 12: 12}
+    assert all(r._obj.q_start == A and r._obj.table_stride == 4 for r in refs.values())
+    b.q_start = None
+    assert b._rows(3)._obj.rows == 3
+    with pytest.raises(ValueError):
+        b._rows(4)

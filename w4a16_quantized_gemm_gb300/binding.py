@@ -820,8 +820,11 @@ class KVBatch:
     def _rows(self, rows: int):
         if self.q_start is None and rows != self.B:
             raise ValueError("without q_start there is one row per sequence")
-        self._c.rows = rows
-        return self._ref
+        if rows == self._c.rows:
+            return self._ref
+        c = KVBBatchStruct.from_buffer_copy(self._c)  # the call's own: another thread may call with other rows
+        c.rows = rows
+        return ctypes.byref(c)
 
 
 def _kvb_rows(t: torch.Tensor, heads, D: int, name: str):
