@@ -93,3 +93,12 @@ def test_calls_with_other_rows_share_no_struct():
     assert b._rows(3)._obj.rows == 3
     with pytest.raises(ValueError):
         b._rows(4)
+
+
+def test_grids_that_no_launch_takes_are_refused(lib):
+    """33 to 64 rows a head with weights: two groups of 32 rows, 80000 along the grid's y for 40000 heads."""
+    n, size = ctypes.c_size_t(7), lambda c, b, Hq, w: lib.tm_kvb_attention_workspace(c, b, Hq, w, ctypes.byref(n))
+    c, b, Hq = cache(Hkv=40000), batch(q_start=A, max_q=40, rows=120), 40000
+    assert size(c, b, Hq, 1) == UNSUP and size(c, b, Hq, 0) == OK
+    big = dict(qs=Hq * 128, Hq=Hq, wo=A, ws=256, work=A, size=1 << 62)
+    assert attention(lib, c, b, **big) == UNSUP

@@ -802,6 +802,10 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   return p;
 }
 
+// Whether the first launch fits its grid, a KV head per group of rows along y.  (The others do by the limits of
+// check and check_heads.)
+static bool plan_fits(const View& V, const Plan& p) { return p.rt < 0 || (long long)V.Hkv * p.groups <= 65535; }
+
 }  // namespace kvb
 
 cudaError_t kvb_attn_error_bits(uint32_t* bits, bool clear) {
@@ -837,7 +841,11 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
   tm_status st = check(cache, batch, false, &V);
   if (st == TM_OK) st = check_heads(V, batch, Hq);
   if (st != TM_OK) return st;
-  *bytes = V.B == 0 || V.rows == 0 || V.max_q == 0 ? 0 : make_plan(V, cache->D, Hq, weights != 0).bytes;
+  *bytes = 0;
+  if (V.B == 0 || V.rows == 0 || V.max_q == 0) return TM_OK;
+  const Plan p = make_plan(V, cache->D, Hq, weights != 0);
+  if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
+  *bytes = p.bytes;
   return TM_OK;
 }
 
@@ -862,7 +870,6 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
   const long long per = 8 / P.wpr;
   const long long joins = P.chunks > 1 ? ((long long)V.max_q * P.Hq + per - 1) / per : 0;
   const long long sums = p.scores ? (P.w_stride + kWeightTokens - 1) / kWeightTokens * V.Hkv : 0;
-  if (joins + sums > 0x7fffffffll) return TM_ERR_UNSUPPORTED;
   if (joins + sums > 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(joins + sums), (unsigned)V.B, 1);
@@ -911,6 +918,7 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   if (!aligned(Q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
     return TM_ERR_ALIGNMENT;
   const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr);
+  if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return TM_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   P.Q = static_cast<const uint16_t*>(Q);
