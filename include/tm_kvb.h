@@ -95,7 +95,7 @@ tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_bat
  * lse = -inf.  Any Hq that Hkv divides.
  *   Q     : device, dtype [rows][Hq][D], token stride q_stride in elements (a
  *           multiple of 8, >= Hq * D), 16-byte aligned
- *   scale : of the scores; 0 = 1 / sqrt(D)
+ *   scale : of the scores, finite; 0 = 1 / sqrt(D)
  *   out   : device, dtype [rows][Hq][D], contiguous, 16-byte aligned
  *   lse   : NULL, or device fp32 [rows][Hq]
  *   w_out : NULL, or the weight that each token drew, device fp32

@@ -20,8 +20,8 @@ def lib():
     return binding.load()
 
 
-def attention(lib, c, b, Q=A, qs=1024, Hq=8, out=A, wi=None, wo=None, ws=0, work=None, size=0):
-    return lib.tm_kvb_attention(c, b, Q, qs, Hq, 0, 0.0, out, None, wi, wo, ws, work, size, None)
+def attention(lib, c, b, Q=A, qs=1024, Hq=8, out=A, wi=None, wo=None, ws=0, work=None, size=0, scale=0.0):
+    return lib.tm_kvb_attention(c, b, Q, qs, Hq, 0, scale, out, None, wi, wo, ws, work, size, None)
 
 
 @pytest.mark.parametrize("none", [dict(q_start=A, rows=0), dict(q_start=A, max_q=0)])
@@ -102,3 +102,15 @@ def test_grids_that_no_launch_takes_are_refused(lib):
     assert size(c, b, Hq, 1) == UNSUP and size(c, b, Hq, 0) == OK
     big = dict(qs=Hq * 128, Hq=Hq, wo=A, ws=256, work=A, size=1 << 62)
     assert attention(lib, c, b, **big) == UNSUP
+
+
+def test_scales_of_the_scores(lib):
+    """NaN and infinities are refused, and so is what would quietly become 0, the default."""
+    from w4a16_quantized_gemm_gb300 import binding
+    none = batch(q_start=A, rows=0)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        assert attention(lib, cache(), none, scale=bad) == INVALID
+    assert attention(lib, cache(), none, scale=-0.5) == OK and attention(lib, cache(), none) == OK
+    for tiny in (1e-60, -1e-60):
+        with pytest.raises(ValueError, match="scale"):
+            binding.kvb_attention(None, None, None, scale=tiny)

@@ -889,10 +889,13 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
     be strided), over the cache (tm_kvb_attention); append the step's keys and
     values first.  Returns out [rows][Hq][D].
 
+    scale: of the scores, finite; None or 0: 1 / sqrt(D)
     lse:   fp32 [rows][Hq], receives the logarithm of each row's softmax sum
     w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
            token drew in this call; may be w_in
     workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
+    if scale and ctypes.c_float(scale).value == 0.0:
+        raise ValueError("scale rounds to 0 in fp32, which stands for 1 / sqrt(D)")
     qp, qs, dtype, shape = _kvb_rows(Q, None, cache.D, "Q")
     rows, Hq = shape[0], shape[1]
     if out is None:

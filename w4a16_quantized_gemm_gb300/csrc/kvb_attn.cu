@@ -29,6 +29,9 @@
 // launch 80, 0.83).  Bound by the conversion: 3.8 warp instructions per byte of codes at 12 warps an SM (by
 // registers and shared memory), half of the ALU pipe.  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a
 // step with 12 or 16 warps: 65 to 88 and 96 to 119.
+#include <cfloat>
+#include <cmath>
+
 #include "kvb_attn.h"
 #include "kvb_ring.h"
 
@@ -902,6 +905,7 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   const View& V = P.V;
   if (dtype != TM_KVB_F16 && dtype != TM_KVB_BF16) return TM_ERR_INVALID_ARG;
   if (w_in && !w_out) return TM_ERR_INVALID_ARG;
+  if (!(fabsf(scale) <= FLT_MAX)) return TM_ERR_INVALID_ARG;  // NaN too
   if (V.B == 0) return TM_OK;
   if (w_out && w_stride < V.max_len) return TM_ERR_INVALID_ARG;
   if (w_out && w_stride > 65535ll * 128) return TM_ERR_UNSUPPORTED;  // the grid's limit
