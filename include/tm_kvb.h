@@ -4,10 +4,15 @@
  *
  * A page (block) holds T tokens of one sequence for every KV head:
  *   codes  k, v   [pages][Hkv][T][D], one byte each: int8 (-127..127) or e4m3
- *   scales ks, vs [pages][Hkv], fp32;  value = code * scale
+ *   scales ks, vs [pages][Hkv], fp32, 2^-30 or more, as the append and the
+ *          eviction write them;  value = code * scale.  (A page of zero codes may
+ *          have scale 0.  A smaller value scale is read as 2^-30; what a negative
+ *          one gives is not defined.)
  * Token j of a sequence lives in slot j % T of page table[j / T].  The cache
  * of tm_w4a16.h (tm_kv_*) is dense, with a scale and a zero per token and head;
- * this one is for caches that grow, shrink and share pages.
+ * this one is for caches that grow, shrink and share pages.  Several sequences
+ * may name a page that a call only reads; see the append and the eviction for
+ * the pages that they write.
  *
  * Conventions are those of tm_w4a16.h: device pointers of the current device,
  * nothing throws, no call allocates or synchronises, every call is
@@ -54,7 +59,8 @@ typedef struct {
   int table_stride;   /* entries per row of the table */
   int max_q;          /* host bound of the new tokens of a sequence: rows past it are not computed */
   int max_len;        /* host bound of kv_len, used for planning and the workspace; longer sequences are
-                         read up to it.  0: table_stride * T */
+                         read up to it.  0: table_stride * T.  The attention cuts all sequences into slices
+                         of one size by it, so that a bound far above the lengths leaves SMs idle */
   long long rows;     /* rows of Q, K and V (q_start is clamped to 0 .. rows); B where q_start is NULL */
 } tm_kvb_batch;
 
@@ -106,9 +112,12 @@ tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_bat
  *   workspace: device, at least tm_kvb_attention_workspace bytes, 16-byte
  *           aligned (may be NULL where that is 0); calls that can overlap on the GPU need
  *           one each
- * The queries are exact in the products (bf16 rows carry a power of two), the
- * scores, the softmax statistics and all sums are fp32; p is rounded once to
- * fp16 for its product with the integer or e4m3 codes.
+ * fp16 queries are exact in the products.  bf16 rows carry a power of two into
+ * fp16: elements of at least 2^-31 of the row's largest are exact, smaller ones
+ * are off by at most 2^-39 of it.  The scores, the softmax statistics and all
+ * sums are fp32; p is rounded once to fp16 for its product with the codes (the
+ * type that holds both formats' codes exactly), and the sum that divides takes
+ * it unrounded.
  */
 tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q, long long q_stride,
                            int Hq, int dtype, float scale, void* out, float* lse, const float* w_in, float* w_out,
@@ -124,8 +133,10 @@ tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
  *   codes Q((c * s_old) / s); its slots past the last token become 0.
  *   A page whose tokens all keep their slots keeps its codes and its scale.
  *   dst_table: device int32 [B][dst_stride], dst_stride >= ceil(budget / T).
- *            May be the batch's own table (the eviction then runs in place);
- *            otherwise no destination page may be one that the call reads.
+ *            May be the batch's own table (the eviction then runs in place): each page
+ *            that it names then belongs to one sequence of the call.  A table with pages
+ *            that sequences share goes into fresh ones; apart from a page that keeps its
+ *            place, no destination page may be one that the call reads, or be named twice.
  *   w      : device fp32 [B][Hkv][w_stride], w_stride >= max_len
  *   w_out  : device fp32 [B][Hkv][w_out_stride], w_out_stride >= budget: the
  *            kept tokens' weights, 0 up to `budget` where fewer are kept.  May be w

@@ -167,6 +167,37 @@ def test_value_scales_decades_apart_in_one_call(fmt, new):
     assert 0 < small < 1e-2 * np.abs(want[0]).max() and tol[-1].max() < 0.1 * small
 
 
+# ---- pages that sequences share, pages that nothing was written to ----
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_shared_pages_are_read_and_moved_into_fresh_ones(fmt):
+    """Three sequences with one prefix: attention over it, and an eviction that leaves it as it was."""
+    T, budget = 32, 100
+    c = Cache(f"kvb/shared/{fmt}", [300, 170, 129], 2, 128, T, fmt, spare=3 * 4)
+    c.table[1:, :4] = c.table[0, :4]
+    for new in (1, 40):
+        run_attention(c, [new] * 3, 8, "fp16", f"shared/{new}")
+    before = [(codes[c.table[0]].copy(), s[c.table[0]].copy()) for codes, s in c.pools]
+    run_evict(c, budget, 40, 10, "shared")
+    assert all(np.array_equal(codes[c.table[0]], b) and np.array_equal(s[c.table[0]], d)
+               for (codes, s), (b, d) in zip(c.pools, before))
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("new", [1, 3, 50])
+def test_pages_that_nothing_was_written_to(fmt, new):
+    """Zero codes under scale 0: values of 0, equal scores."""
+    blocks = binding.KVBlocks.empty(6, 2, 32, 64, fmt)
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(1, 6)
+    batch = binding.KVBatch(table, device(np.array([180], np.int32)), device(starts([new])), max_q=new)
+    Q = torch.randn(new, 4, 64, device="cuda").half()
+    lse = torch.empty(new, 4, device="cuda")
+    out = binding.kvb_attention(blocks, batch, Q, lse=lse)
+    seen = torch.arange(180 - new + 1, 181, device="cuda").double().log()[:, None].expand(new, 4)
+    assert torch.equal(out, torch.zeros_like(out))
+    assert ((lse.double() - seen).abs() <= 2.0 ** -20 * (1 + seen)).all()  # a log2 and a product in fp32
+
+
 # ---- nothing outside the buffers, whatever the numbers on the device say ----
 
 class Guards:

@@ -796,7 +796,8 @@ class KVBatch:
     q_start: int32 [B + 1], where each sequence's rows begin in Q, K and V;
              None: one row each
     max_q, max_len: bounds of a sequence's rows and tokens that the host knows
-             (max_len 0: the room of the table)
+             (max_len 0: the room of the table; the work is planned by it, so that
+             a tight one is faster)
 
     The tensors are kept and read on the device at each call: a program advances
     kv_len, and fills in table entries, in place."""
@@ -931,7 +932,8 @@ def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, fir
     """Cut every sequence to ``budget`` tokens per KV head (tm_kvb_evict): the first
     ``first``, the last ``recent`` and the heaviest of the rest by w, fp32
     [B][Hkv][tokens].  dst_table int32 [B][n]: the pages that take them (None: in
-    place).  w_out: their weights, fp32 [B][Hkv][>= budget] (None: into w).
+    place: no page may then belong to two sequences of the batch; move sequences that
+    share pages into fresh ones).  w_out: their weights, fp32 [B][Hkv][>= budget] (None: into w).
     Returns (kept int32 [B][Hkv][budget], new_len int32 [B]); batch.kv_len is
     left as it is."""
     wp, wn = _kvb_weights(w, batch.B, cache.Hkv, "w")
