@@ -26,9 +26,11 @@
 //
 // Measured: 32 x up to 4096 tokens, int8, 32 query and 8 KV heads, weights: 62 us for 217 MB of codes (first
 // launch 50, 0.62 of the HBM copy rate); 2 x 131072 tokens, e4m3, 64 query heads: 90 us for 453 MB (first
-// launch 80, 0.83).  Bound by the conversion: 3.8 warp instructions per byte of codes at 12 warps an SM (by
-// registers and shared memory), half of the ALU pipe.  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a
-// step with 12 or 16 warps: 65 to 88 and 96 to 119.
+// launch 80, 0.83).  No unit is full there (issue slots 52 and 45 %, ALU pipe 49 %): what counts is the latency
+// of dependent instructions, 3.8 of a thread per byte of codes, at 12 warps an SM (by registers and shared
+// memory).  16 rows in place of 8: 65.4 and 94.4 us; 16 tokens a step with 12 or 16 warps: 65 to 88 and 96 to 119.
+// 13 x up to 1531 tokens, e4m3, 12 heads of 64 not shared, weights: 17 us for 23 MB, a launch of about 12 (624 CTAs,
+// 37 % of the issue slots, waiting for memory) and one of 8 (15 %, chains of loads and barriers).
 #include <cfloat>
 #include <cmath>
 
@@ -146,7 +148,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     m.cell = page >= 0 ? page * V.Hkv + h : -1;
     m.slot = j & ((1 << V.t_shift) - 1);
     m.ks = page >= 0 ? V.ks[m.cell] : 1.f;
-    // 2^lv stands for vs (to 2^-21 of it); its own inverse takes it out of l again.
+    // 2^lv stands for vs; its own inverse takes it out of l again, so that lv's rounding stays in the output: 2 ulp
+    // of lv, 2^-18.5 of vs at the smallest scales (|lv| of 16 or more), 2^-19.5 at scales above 2^-16.
     m.lv = page >= 0 ? __log2f(fmaxf(V.vs[m.cell], kScaleFloor)) : 0.f;
     return m;
   };
@@ -169,7 +172,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
   for (int i = 0; i < S; ++i) issue(i, 0);
 
   // ---- the queries, once, in the k order of the codes; bf16 rows are scaled by a
-  // power of two into fp16's range (exact down to 2^-39 of the row's maximum)
+  // power of two into fp16's range: exact for elements of 2^-31 of the row's maximum or more, off by at most
+  // 2^-39 of it for smaller ones
   uint32_t qa[RT == 2 ? 1 : KS][RT == 0 ? 2 : 4];
   float mul[TILES][E];
   int last[TILES][E];  // last visible token (-1: no row)
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
           for (int a = 0; a < 2; ++a) {
             const float p0 = ex2(sc[rt][2 * g + a][2 * e] + off), p1 = ex2(sc[rt][2 * g + a][2 * e + 1] + off);
             sum += p0 + p1;
-            pa[rt][g][E * a + e] = pack_half2(p0, p1);
+            pa[rt][g][E * a + e] = pack_half2(p0, p1);  // the codes' type in the product; l keeps all bits
           }
           l[rt][e] = fmaf(sum, inv[g], l[rt][e]);
         }

@@ -17,8 +17,9 @@
 //
 // Measured: 8 heads, 2304 -> 2048 tokens 18.6 us (a chain of latencies: key loads 1 us, four
 // rounds of histogram and scan 5 us, gather 4 us, requantising 4 us on 64 SMs); 32 x 8 heads, up
-// to 4001 -> 1000 tokens, e4m3, 50 us, 2.7 TB/s of what has to move (issue slots 62 %: arithmetic on
-// codes); 2 x 8 heads, 131072 -> 4096, 48 us (16 k keys per CTA through shared-memory histograms).
+// to 4001 -> 1000 tokens, e4m3, 51 us, 2.7 TB/s of what has to move (issue slots 62 %, DRAM 0.39 of the copy rate:
+// neither is full; arithmetic on codes and the latencies of the selection in turn); 2 x 8 heads, 131072 -> 4096,
+// 49 us (16 k keys per CTA through shared-memory histograms, barriers).  In place the same take 17, 56 and 48 us.
 #include "kvb_common.cuh"
 
 namespace w4 {

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
                                                    cg2, off2));
               const float p0 = ex2(e.x), p1 = ex2(e.y);
               sum = add_f32x2(sum, f32x2(p0, p1));
-              p[8 * k + c / 2] = pack_half2(p0, p1);
+              p[8 * k + c / 2] = pack_half2(p0, p1);  // the codes' type in the product; l keeps all bits
             }
             const float2 part = f32x2_get(sum);
             l = fmaf(part.x + part.y, mt.z, l);
