@@ -46,6 +46,8 @@ class Stack:
     def __init__(self, layers=2, hidden=1024, Hq=16, Hkv=4, D=64, B=4, budget=512, slack=128, T=64, fmt=torch.int8,
                  seed=0):
         gen = torch.Generator().manual_seed(seed)
+        if budget < 1 or slack < 1:
+            raise ValueError("budget and slack must be at least 1")
         self.B, self.budget, self.capacity = B, budget, budget + slack
         self.layers = [Layer(hidden, Hq, Hkv, D, B, self.capacity, T, fmt, gen) for _ in range(layers)]
         pages = -(-self.capacity // T)
@@ -53,7 +55,7 @@ class Stack:
         self.kv_len = torch.zeros(B, dtype=torch.int32, device="cuda")
         self.held = [0] * B  # the same on the host, for the bounds
         self.evictions, self.graph = 0, None
-        self.first, self.recent = 4, min(64, budget // 2)
+        self.first, self.recent = min(4, budget // 2), min(64, budget // 2)
 
     def norm(self, x):
         x = x.float()

@@ -274,3 +274,19 @@ def test_numbers_out_of_range_stay_inside_every_buffer(new, lens, begins):
                           for t, p in zip((blocks.k, blocks.v), pools))
     assert all(torch.equal(t, before) for t, before in inputs)
     assert new_len.tolist() == [min(max(n, 0), room, 40) for n in lens]
+
+
+@pytest.mark.parametrize("budget", [1, 2, 6])
+def test_example_with_a_small_budget(budget):
+    """The example's kept ends fit every budget."""
+    from tests.test_gpu_kvb_example import _module
+    m = _module()
+    stack = m.Stack(layers=1, B=2, budget=budget, slack=3)
+    gen = torch.Generator("cuda").manual_seed(7)
+    x = stack.prompt(torch.randn(2, 20, 1024, generator=gen, device="cuda").half())
+    for _ in range(5):
+        y = stack.decode(stack.norm(x[:, -1]))
+    torch.cuda.synchronize()
+    assert torch.isfinite(y).all() and stack.evictions > 2 and stack.kv_len.tolist() == stack.held
+    with pytest.raises(ValueError):
+        m.Stack(slack=0)
