@@ -199,6 +199,14 @@ def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.T
     return t
 
 
+def _contiguous(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """t, or its copy made on the call's stream, in that stream's memory."""
+    if stream is None or t.is_contiguous():
+        return t.contiguous()
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
 class PackedWeights:
     """Owns a ``tm_packed`` handle (device memory on the device of ``q``)."""
 
@@ -281,10 +289,10 @@ def gemm(X: torch.Tensor, w: PackedWeights, out: Optional[torch.Tensor] = None, 
         return _gemm_host(X, w, out, config, stream)
     M = X.shape[0]
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.float16, device=X.device)
+        out = _empty((M, w.N), torch.float16, X.device, stream)
     elif out.shape != (M, w.N) or out.dtype != torch.float16 or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA fp16 [M][N] tensor")
-    X = X.contiguous()
+    X = _contiguous(X, stream)
     s = stream if stream is not None else torch.cuda.current_stream(X.device)
     c = _cfg(config)
     lib = load()
@@ -306,10 +314,10 @@ def gemm_silu_mul(X: torch.Tensor, w: PackedWeights, out: Optional[torch.Tensor]
         raise ValueError("X must be a CUDA fp16 [M][K] tensor")
     M = X.shape[0]
     if out is None:
-        out = torch.empty((M, w.N // 2), dtype=torch.float16, device=X.device)
+        out = _empty((M, w.N // 2), torch.float16, X.device, stream)
     elif out.shape != (M, w.N // 2) or out.dtype != torch.float16 or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA fp16 [M][N/2] tensor")
-    X = X.contiguous()
+    X = _contiguous(X, stream)
     s = stream if stream is not None else torch.cuda.current_stream(X.device)
     c = _cfg(config)
     _check(load().tm_w4a16_gemm_silu_mul(X.data_ptr(), w.handle, out.data_ptr(), M,
@@ -362,10 +370,10 @@ def gemm_grouped(problems, config=None, stream: Optional[torch.cuda.Stream] = No
             raise ValueError("every X must have the same number of rows")
         cols = w.N // 2 if silu else w.N
         if out is None:
-            out = torch.empty((M, cols), dtype=torch.float16, device=X.device)
+            out = _empty((M, cols), torch.float16, X.device, stream)
         elif out.shape != (M, cols) or out.dtype != torch.float16 or not out.is_cuda or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous CUDA fp16 [{M}][{cols}] tensor")
-        items.append((X.contiguous(), w, out, bool(silu)))
+        items.append((_contiguous(X, stream), w, out, bool(silu)))
     if not items:
         raise ValueError("at least one problem")
     s = stream if stream is not None else torch.cuda.current_stream(items[0][0].device)
@@ -385,9 +393,9 @@ def _host_fp16(t: torch.Tensor, shape, name: str):
         raise ValueError(f"{name} must be a contiguous host fp16 tensor of shape {tuple(shape)}")
 
 
-def _staging(t: Optional[torch.Tensor], numel: int, device, name: str) -> torch.Tensor:
+def _staging(t: Optional[torch.Tensor], numel: int, device, name: str, stream) -> torch.Tensor:
     if t is None:
-        return torch.empty(numel, dtype=torch.float16, device=device)
+        return _empty(numel, torch.float16, device, stream)
     if not t.is_cuda or t.dtype != torch.float16 or not t.is_contiguous() or t.numel() < numel:
         raise ValueError(f"{name} must be a contiguous CUDA fp16 buffer of at least {numel} elements")
     return t
@@ -408,8 +416,8 @@ def gemm_host(X: torch.Tensor, w: PackedWeights, out: Optional[torch.Tensor] = N
     if out is None:
         out = torch.empty((M, w.N), dtype=torch.float16, pin_memory=True)
     _host_fp16(out, (M, w.N), "out")
-    X_dev = _staging(X_dev, M * w.K, w.device, "X_dev")
-    Y_dev = _staging(Y_dev, M * w.N, w.device, "Y_dev")
+    X_dev = _staging(X_dev, M * w.K, w.device, "X_dev", stream)
+    Y_dev = _staging(Y_dev, M * w.N, w.device, "Y_dev", stream)
     s = stream if stream is not None else torch.cuda.current_stream(w.device)
     c = _cfg(config)
     _check(load().tm_w4a16_gemm_host(X.data_ptr(), w.handle, out.data_ptr(), M, X_dev.data_ptr(), Y_dev.data_ptr(),
@@ -493,11 +501,11 @@ def quantize_rtn(W: torch.Tensor, g: int, stream: Optional[torch.cuda.Stream] = 
     if W.dim() != 2 or W.dtype != torch.float16:
         raise ValueError("W must be fp16 [K][N]")
     K, N = W.shape
-    Wd = W.contiguous()
+    Wd = _contiguous(W, stream)
     _dev(Wd, torch.float16, "W")
-    q = torch.empty((K, N), dtype=torch.uint8, device=Wd.device)
-    z = torch.empty((K // g if g > 0 else 0, N), dtype=torch.uint8, device=Wd.device)
-    s = torch.empty((K // g if g > 0 else 0, N), dtype=torch.float16, device=Wd.device)
+    q = _empty((K, N), torch.uint8, Wd.device, stream)
+    z = _empty((K // g if g > 0 else 0, N), torch.uint8, Wd.device, stream)
+    s = _empty((K // g if g > 0 else 0, N), torch.float16, Wd.device, stream)
     st = stream if stream is not None else torch.cuda.current_stream(Wd.device)
     with torch.cuda.device(Wd.device):
         _check(load().tm_quantize_rtn(Wd.data_ptr(), K, N, g, q.data_ptr(), z.data_ptr(), s.data_ptr(),
@@ -510,13 +518,13 @@ def kv_quantize(X: torch.Tensor, bits: int, stream: Optional[torch.cuda.Stream] 
     returns (codes uint8 [..., D or D/2], s fp16 [...], z uint8 [...])."""
     if X.dtype != torch.float16 or not X.is_cuda or X.dim() < 1:
         raise ValueError("X must be a CUDA fp16 tensor [..., D]")
-    X = X.contiguous()
+    X = _contiguous(X, stream)
     D = X.shape[-1]
     lead = tuple(X.shape[:-1])
     rows = X.numel() // D if D else 0
-    codes = torch.empty(lead + (D if bits == 8 else D // 2,), dtype=torch.uint8, device=X.device)
-    s = torch.empty(lead, dtype=torch.float16, device=X.device)
-    z = torch.empty(lead, dtype=torch.uint8, device=X.device)
+    codes = _empty(lead + (D if bits == 8 else D // 2,), torch.uint8, X.device, stream)
+    s = _empty(lead, torch.float16, X.device, stream)
+    z = _empty(lead, torch.uint8, X.device, stream)
     st = stream if stream is not None else torch.cuda.current_stream(X.device)
     _check(load().tm_kv_quantize(X.data_ptr(), rows, D, bits, codes.data_ptr(), s.data_ptr(), z.data_ptr(),
                                  ctypes.c_void_p(st.cuda_stream)), "tm_kv_quantize")
@@ -529,8 +537,8 @@ def kv_pack_v(codes: torch.Tensor, bits: int, stream: Optional[torch.cuda.Stream
     if codes.dim() != 4 or codes.dtype != torch.uint8 or codes.shape[3] != 128 * bits // 8:
         raise ValueError("codes must be uint8 [B][Hkv][L][128*bits/8]")
     B, Hkv, L, _ = codes.shape
-    codes = codes.contiguous()
-    tiles = torch.empty(B * Hkv * L * 128 * bits // 8, dtype=torch.uint8, device=codes.device)
+    codes = _contiguous(codes, stream)
+    tiles = _empty(B * Hkv * L * 128 * bits // 8, torch.uint8, codes.device, stream)
     st = stream if stream is not None else torch.cuda.current_stream(codes.device)
     _check(load().tm_kv_pack_v(codes.data_ptr(), B, L, Hkv, bits, tiles.data_ptr(), ctypes.c_void_p(st.cuda_stream)),
            "tm_kv_pack_v")
@@ -577,7 +585,7 @@ def kv_decode_attention(Q: torch.Tensor, k: tuple, v: tuple, lengths: torch.Tens
     if tuple(ks.shape) != (B, Hkv, L) or tuple(vs.shape) != (B, Hkv, L):
         raise ValueError("scales and zeros must be [B][Hkv][L] like the key codes")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float16, device=Q.device)
+        out = _empty((B, Hq, D), torch.float16, Q.device, stream)
     ts = [Q, kc, ks, kz, vc, vs, vz, lengths]
     if any((not t.is_cuda) or (not t.is_contiguous()) for t in ts) or lengths.dtype != torch.int32:
         raise ValueError("all inputs must be contiguous CUDA tensors; lengths int32")
@@ -614,8 +622,8 @@ def w8a8_quantize_act(X: torch.Tensor, out: Optional[tuple] = None, stream: Opti
         raise ValueError("X must be fp16 [M][K]")
     M, K = X.shape
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
-        sx = torch.empty((M,), dtype=torch.float32, device=X.device)
+        xq = _empty((M, K), torch.int8, X.device, stream)
+        sx = _empty((M,), torch.float32, X.device, stream)
     else:
         xq, sx = out
         if tuple(xq.shape) != (M, K) or tuple(sx.shape) != (M,):
@@ -634,8 +642,8 @@ def w8a8_quantize_act_f16(X: torch.Tensor, out: Optional[tuple] = None, stream: 
         raise ValueError("X must be fp16 [M][K]")
     M, K = X.shape
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.float16, device=X.device)
-        sx = torch.empty((M,), dtype=torch.float32, device=X.device)
+        xq = _empty((M, K), torch.float16, X.device, stream)
+        sx = _empty((M,), torch.float32, X.device, stream)
     else:
         xq, sx = out
         if tuple(xq.shape) != (M, K) or tuple(sx.shape) != (M,):
@@ -654,8 +662,8 @@ def w8_quantize_weight(W: torch.Tensor, stream: Optional[torch.cuda.Stream] = No
     if W.dim() != 2 or W.dtype != torch.float16:
         raise ValueError("W must be fp16 [K][N]")
     K, N = W.shape
-    q = torch.empty((K, N), dtype=torch.int8, device=W.device)
-    sw = torch.empty((N,), dtype=torch.float32, device=W.device)
+    q = _empty((K, N), torch.int8, W.device, stream)
+    sw = _empty((N,), torch.float32, W.device, stream)
     st = stream if stream is not None else torch.cuda.current_stream(W.device)
     _check(load().tm_w8_quantize_weight(_dev(W, torch.float16, "W"), K, N, q.data_ptr(), sw.data_ptr(),
                                         ctypes.c_void_p(st.cuda_stream)), "tm_w8_quantize_weight")
@@ -717,7 +725,7 @@ def w8a8_gemm(xq: torch.Tensor, sx: torch.Tensor, w: W8Packed, out: Optional[tor
     if tuple(sx.shape) != (M,):
         raise ValueError("sx must be fp32 [M]")
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.float16, device=xq.device)
+        out = _empty((M, w.N), torch.float16, xq.device, stream)
     if tuple(out.shape) != (M, w.N):
         raise ValueError("out must be fp16 [M][N]")
     st = stream if stream is not None else torch.cuda.current_stream(xq.device)
@@ -737,7 +745,7 @@ def w8a8_gemm_f16(xq16: torch.Tensor, sx: torch.Tensor, w: W8Packed, out: Option
     if tuple(sx.shape) != (M,):
         raise ValueError("sx must be fp32 [M]")
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.float16, device=xq16.device)
+        out = _empty((M, w.N), torch.float16, xq16.device, stream)
     if tuple(out.shape) != (M, w.N):
         raise ValueError("out must be fp16 [M][N]")
     st = stream if stream is not None else torch.cuda.current_stream(xq16.device)
