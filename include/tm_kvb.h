@@ -1,6 +1,7 @@
 /*
  * tm_kvb.h -- C ABI of the paged 8-bit KV cache with one scale per block of
- * tokens and head (GB300, sm_103a): append, attention, eviction.
+ * tokens and head (GB300, sm_103a): append (with position rotation), attention
+ * (causal, or of a tree of drafts), accepted drafts, eviction.
  *
  * A page (block) holds T tokens of one sequence for every KV head:
  *   codes  k, v   [pages][Hkv][T][D], one byte each: int8 (-127..127) or e4m3
@@ -87,7 +88,35 @@ typedef struct {
 tm_status tm_kvb_append(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Kn, long long k_stride,
                         const void* Vn, long long v_stride, int dtype, float* w, long long w_stride, void* stream);
 
-/* Bytes of device workspace that tm_kvb_attention needs for these shapes
+/* Rotation by position. */
+typedef struct {
+  const float* table; /* device fp32 [positions][dims], 16-byte aligned: a position's dims / 2 cosines, then its sines */
+  int positions;      /* >= 1 */
+  int dims;           /* leading dimensions of a head that rotate: a multiple of 16, 16 .. D */
+  int interleaved;    /* pairs (i, i + dims / 2), or, where not 0, neighbours (2 i, 2 i + 1); i: the pair's angle */
+  const int* pos;     /* device int32 [rows]: each row's position; NULL: its slot.  Clamped to 0 .. positions - 1 */
+} tm_kvb_rope;
+
+/*
+ * tm_kvb_append with the keys rotated on the way, and the queries beside them:
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin
+ * for every pair (x1, x2) of the rotating dimensions, in binary32 with each
+ * product and each sum rounded.  Rotated keys are quantised as the append does
+ * from binary32 (NaN that the rotation gives counts as 0, an infinity as the
+ * largest finite binary32), values as they are; rotated queries
+ * are rounded once to their type (no value is replaced).
+ *   Q, q_out : device, dtype [rows][Hq][D], token strides q_stride, qo_stride in elements
+ *           (multiples of 8, >= Hq * D), 16-byte aligned; Hkv divides Hq.  q_out may be Q
+ *           (with its stride), else it overlaps no input.  Rows of no sequence, and past max_q of one, are left
+ *           as they are.  NULL, NULL: keys and values alone (Hq and the strides are then not read)
+ * The rest as in tm_kvb_append.  One launch.
+ */
+tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Kn, long long k_stride,
+                             const void* Vn, long long v_stride, const void* Q, long long q_stride, int Hq,
+                             void* q_out, long long qo_stride, const tm_kvb_rope* rope, int dtype, float* w,
+                             long long w_stride, void* stream);
+
+/* Bytes of device workspace that tm_kvb_attention and tm_kvb_attention_tree need for these shapes
  * (only the host fields of cache and batch are read); weights != 0: with w_out. */
 tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq, int weights,
                                      size_t* bytes);
@@ -122,6 +151,45 @@ tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_bat
 tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q, long long q_stride,
                            int Hq, int dtype, float scale, void* out, float* lse, const float* w_in, float* w_out,
                            long long w_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tm_kvb_attention for new tokens that are a tree (or any graph) of drafts: row
+ * i of a sequence with n new tokens sees the kv_len - n tokens before them, and
+ * of the new ones those that its mask names,
+ *   j < kv_len - n, or bit (k % 32) of tree[row][k / 32] set, k = j - (kv_len - n)
+ * -- a node's ancestors and itself, where the rows are a tree's nodes.  Any mask is
+ * valid; a row that sees nothing gives out = 0 and lse = -inf.
+ *   tree  : device, 32-bit words [rows][tree_stride], 4-byte aligned,
+ *           tree_stride >= ceil(max_q / 32), which is how many words of a row are read: new
+ *           tokens past them are not seen, and bits past the new tokens say nothing
+ * The rest as in tm_kvb_attention, its workspace too.
+ */
+tm_status tm_kvb_attention_tree(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
+                                long long q_stride, int Hq, int dtype, float scale, const uint32_t* tree,
+                                long long tree_stride, void* out, float* lse, const float* w_in, float* w_out,
+                                long long w_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Keep a path through the new tokens of each sequence: new token path[b][i], i <
+ * count[b], moves to slot old + i, old = kv_len[b] - n.  A path is strictly ascending
+ * (a tree's nodes come after their parents); it ends at its first entry that is
+ * not above the one before it, or no new token (0 .. n - 1).
+ * A token that stays in its page keeps its codes.  One that comes from another
+ * page is a new value x = c * s_src of the page, by the rule of tm_kvb_append: the page's scale grows
+ * to what these need, and becomes that where the page keeps no token (of before, or of the path).
+ * Slots from old + count on keep what they hold.  A hole's tokens move as zeros,
+ * and what falls into a hole is dropped.
+ *   path   : device int32 [B][path_stride]
+ *   count  : device int32 [B] (clamped to 0 .. path_stride)
+ *   w      : NULL, or the token weights fp32 [B][Hkv][w_stride]: they move along, those of the
+ *            new tokens that are not kept become 0
+ *   new_len: device int32 [B]: old + count; kv_len where the sequence has no new token, or more of them than
+ *            tokens (such a sequence is left as it is).  Not kv_len itself
+ * A page of a sequence's new tokens belongs to that sequence alone.  Of the batch, max_q, max_len and (with q_start)
+ * rows are not read.  One launch.
+ */
+tm_status tm_kvb_accept(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const int* path, int path_stride,
+                        const int* count, float* w, long long w_stride, int* new_len, void* stream);
 
 /*
  * Cut every sequence to `budget` tokens per KV head: the first `first`, the

@@ -52,6 +52,21 @@ def finite(x: np.ndarray, top: float) -> np.ndarray:
     return np.clip(np.nan_to_num(x.astype(np.float32), nan=0.0), -np.float32(top), np.float32(top))
 
 
+def rotate(x, table, pos, interleaved=False):
+    """x [rows][heads][D] (binary32) with the pairs of its first dims dimensions turned by table [positions][dims]
+    (cosines, then sines) at pos [rows], clamped; binary32, each product and sum rounded."""
+    y = np.array(x, dtype=np.float32)
+    half = table.shape[1] // 2
+    cs = table[np.clip(pos, 0, table.shape[0] - 1)][:, None]
+    c, s = cs[..., :half], cs[..., half:]
+    first = slice(0, 2 * half, 2) if interleaved else slice(0, half)
+    second = slice(1, 2 * half, 2) if interleaved else slice(half, 2 * half)
+    a, b = y[..., first].copy(), y[..., second].copy()
+    with np.errstate(over="ignore", invalid="ignore"):
+        y[..., first], y[..., second] = a * c - b * s, b * c + a * s
+    return y
+
+
 def append(codes, scales, table, kv_len, q_start, x, fmt, top=65504.0):
     """New rows x [rows][Hkv][D] into codes [pages][Hkv][T][D] and scales [pages][Hkv], in place."""
     pages, Hkv, T, _ = codes.shape
@@ -60,7 +75,7 @@ def append(codes, scales, table, kv_len, q_start, x, fmt, top=65504.0):
         n, length = int(q_start[b + 1] - q_start[b]), int(kv_len[b])
         old = length - n
         for blk in range(max(old, 0) // T, -(-length // T) if n else 0):
-            page = table[b, blk]
+            page = table[b, blk] if blk < table.shape[1] else -1
             if not 0 <= page < pages:
                 continue
             lo, hi = max(old, blk * T, 0), min(length, (blk + 1) * T)
@@ -89,9 +104,10 @@ def tokens(codes, scales, row, length, h, fmt):
     return x, there
 
 
-def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None):
+def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None, tree=None):
     """Q [rows][Hq][D] (binary64 values) -> out, lse [rows][Hq], w [B][Hkv][max len], and for
-    error bounds sum p |v| [rows][Hq][D] and max_j scale sum |q k| [rows][Hq]."""
+    error bounds sum p |v| [rows][Hq][D] and max_j scale sum |q k| [rows][Hq].
+    tree: mask words [rows][words] over the sequence's new tokens, in place of the causal rule."""
     rows, Hq, D = Q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -105,7 +121,13 @@ def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None):
             kh, there = tokens(k, ks, table[b], length, h, fmt)
             vh, _ = tokens(v, vs, table[b], length, h, fmt)
             for i in range(n):
-                seen = there & (np.arange(length) <= length - n + i)
+                if tree is None:
+                    seen = there & (np.arange(length) <= length - n + i)
+                else:
+                    words = [int(x) & 0xffffffff for x in tree[q_start[b] + i]]
+                    mask = sum(x << (32 * k) for k, x in enumerate(words))
+                    seen = there & np.array([j < length - n or mask >> (j - length + n) & 1 == 1 for j in range(length)],
+                                            dtype=bool)
                 if not seen.any():
                     continue
                 for g in range(G):
@@ -165,3 +187,62 @@ def evict(pools, table, dst_table, kv_len, w, budget, first, recent, fmt):
                     now = max(np.float32(np.abs(x).max() * STEP[fmt]), FLOOR)
                     codes[to, h], scales[to, h] = encode(x / now, fmt), now
     return kept, new_len, w_out
+
+
+def accept(pools, table, kv_len, q_start, path, count, w, fmt):
+    """Accepted paths: pools [(codes, scales)] and w (or None) changed in place, token by token.  Returns new_len."""
+    pages, Hkv, T, D = pools[0][0].shape
+    new_len = np.zeros(table.shape[0], dtype=np.int32)
+    for b in range(table.shape[0]):
+        n, length = int(q_start[b + 1] - q_start[b]), max(int(kv_len[b]), 0)
+        old = length - n
+        new_len[b] = length
+        if n == 0 or old < 0:
+            continue
+        kept = []
+        for at in path[b][:max(int(count[b]), 0)]:
+            if not 0 <= at < n or (kept and at <= kept[-1]):
+                break
+            kept.append(int(at))
+        new_len[b] = old + len(kept)
+        page_of = lambda slot: table[b, slot // T] if slot // T < table.shape[1] else -1  # noqa: E731
+        for h in range(Hkv):
+            if w is not None:
+                row = w[b, h]
+                moved = [row[old + at] if old + at < len(row) else 0.0 for at in kept] + [0.0] * (n - len(kept))
+                for i, x in enumerate(moved):
+                    if old + i < len(row):
+                        row[old + i] = x
+            for codes, scales in pools:
+                before, scale_before = codes.copy(), scales.copy()
+                for blk in range(old // T, -(-(old + len(kept)) // T)):
+                    page = page_of(blk * T)
+                    if not 0 <= page < pages:
+                        continue
+                    stay, away = {}, {}
+                    for i, at in enumerate(kept):
+                        if (old + i) // T != blk:
+                            continue
+                        if (old + at) // T == blk:
+                            stay[(old + i) % T] = before[page, h, (old + at) % T]
+                        else:
+                            p = page_of(old + at)
+                            there = 0 <= p < pages
+                            x = decode(before[p, h, (old + at) % T], fmt).astype(np.float32) * scale_before[p, h] if there \
+                                else np.zeros(D, np.float32)
+                            away[(old + i) % T] = x
+                    for t, c in stay.items():
+                        codes[page, h, t] = c
+                    if not away:
+                        continue
+                    s = max(np.float32(max(np.abs(x).max() for x in away.values()) * STEP[fmt]), FLOOR)
+                    held = list(range(max(0, old - blk * T))) + list(stay)
+                    if held:
+                        was = scale_before[page, h]
+                        if s > was:
+                            codes[page, h, held] = encode(decode(codes[page, h, held], fmt).astype(np.float32) * was / s, fmt)
+                        s = max(s, was)
+                    scales[page, h] = s
+                    for t, x in away.items():
+                        codes[page, h, t] = encode(x / s, fmt)
+    return new_len

@@ -1,5 +1,5 @@
-"""Thin ctypes binding of ``include/tm_w4a16.h``, ``include/tm_w8a8.h`` and
-``include/tm_kvb.h`` (argument marshalling only).
+"""Thin ctypes binding of ``include/tm_w4a16.h``, ``include/tm_w8a8.h``,
+``include/tm_kvb.h`` and ``include/tm_lora.h`` (argument marshalling only).
 
 Every step of the computation runs in the CUDA library; PyTorch provides
 device memory and streams.  If the library is missing this module raises --
@@ -28,7 +28,8 @@ EXPORTS = ("tm_status_str", "tm_packed_bytes", "tm_pack_weights", "tm_unpack_wei
            "tm_w8_quantize_weight", "tm_kv_append", "tm_w4a16_gemm_host", "tm_w4a16_gemm_host_batch",
            "tm_w8a8_quantize_act_f16", "tm_w8a8_gemm_f16", "tm_w4a16_gemm_host_static",
            "tm_w4a16_gemm_grouped", "tm_gemm_plan_grouped", "tm_kvb_append", "tm_kvb_attention",
-           "tm_kvb_attention_workspace", "tm_kvb_evict")
+           "tm_kvb_attention_workspace", "tm_kvb_evict", "tm_kvb_append_rope", "tm_kvb_attention_tree",
+           "tm_kvb_accept", "tm_lora_add")
 
 GROUP_MAX = 4  # TM_GROUP_MAX
 
@@ -51,6 +52,18 @@ class KVBBatchStruct(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
                 ("B", ctypes.c_int), ("table_stride", ctypes.c_int), ("max_q", ctypes.c_int),
                 ("max_len", ctypes.c_int), ("rows", ctypes.c_longlong)]
+
+
+class KVBRopeStruct(ctypes.Structure):
+    """``tm_kvb_rope``."""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int), ("dims", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("pos", ctypes.c_void_p)]
+
+
+class LoraAdaptersStruct(ctypes.Structure):
+    """``tm_lora_adapters``."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("n", ctypes.c_int),
+                ("K", ctypes.c_int), ("N", ctypes.c_int), ("R", ctypes.c_int)]
 
 
 class GemmConfig(ctypes.Structure):
@@ -158,6 +171,15 @@ def load(path: Optional[str] = None):
     lib.tm_kvb_attention.argtypes = [pc, pb, vp, ll, ci, ci, ctypes.c_float, vp, vp, vp, vp, ll, vp, csz, vp]
     lib.tm_kvb_evict.restype = ci
     lib.tm_kvb_evict.argtypes = [pc, pb, vp, ci, vp, ll, vp, ll, ci, ci, ci, vp, vp, vp]
+    lib.tm_kvb_append_rope.restype = ci
+    lib.tm_kvb_append_rope.argtypes = [pc, pb, vp, ll, vp, ll, vp, ll, ci, vp, ll, ctypes.POINTER(KVBRopeStruct), ci, vp,
+                                       ll, vp]
+    lib.tm_kvb_attention_tree.restype = ci
+    lib.tm_kvb_attention_tree.argtypes = [pc, pb, vp, ll, ci, ci, ctypes.c_float, vp, ll, vp, vp, vp, vp, ll, vp, csz, vp]
+    lib.tm_kvb_accept.restype = ci
+    lib.tm_kvb_accept.argtypes = [pc, pb, vp, ci, vp, vp, ll, vp, vp]
+    lib.tm_lora_add.restype = ci
+    lib.tm_lora_add.argtypes = [ctypes.POINTER(LoraAdaptersStruct), vp, ll, vp, ll, vp, ll, ll, vp, vp, ci, vp]
     _lib = lib
     return lib
 
@@ -889,20 +911,9 @@ def kvb_attention_workspace(cache: KVBlocks, batch: KVBatch, Hq: int, rows: int,
     return n.value
 
 
-def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optional[torch.Tensor] = None,
-                  lse: Optional[torch.Tensor] = None, w_in: Optional[torch.Tensor] = None,
-                  w_out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                  workspace: Optional[torch.Tensor] = None,
-                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """Causal attention of the step's queries, fp16 or bf16 [rows][Hq][D] (rows may
-    be strided), over the cache (tm_kvb_attention); append the step's keys and
-    values first.  Returns out [rows][Hq][D].
-
-    scale: of the scores, finite; None or 0: 1 / sqrt(D)
-    lse:   fp32 [rows][Hq], receives the logarithm of each row's softmax sum
-    w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
-           token drew in this call; may be w_in
-    workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
+def _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream):
+    """Arguments that kvb_attention and kvb_attention_tree share, before and after the tree's, out, and the workspace
+    (the caller holds it until its launches are made)."""
     if scale and ctypes.c_float(scale).value == 0.0:
         raise ValueError("scale rounds to 0 in fp32, which stands for 1 / sqrt(D)")
     qp, qs, dtype, shape = _kvb_rows(Q, None, cache.D, "Q")
@@ -925,12 +936,144 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
         if size:
             workspace = _empty(size, torch.uint8, Q.device, stream)
     sp, size = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    st = (_lib or load()).tm_kvb_attention(cache._ref, batch._rows(rows), qp, qs, Hq, dtype,
-                                           0.0 if scale is None else scale, _dev(out, Q.dtype, "out"), lp, wi, wo, no,
-                                           sp, size, _kvb_stream(cache, stream))
+    return ((cache._ref, batch._rows(rows), qp, qs, Hq, dtype, 0.0 if scale is None else scale),
+            (_dev(out, Q.dtype, "out"), lp, wi, wo, no, sp, size, _kvb_stream(cache, stream)), out, workspace)
+
+
+def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, w_in: Optional[torch.Tensor] = None,
+                  w_out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of the step's queries, fp16 or bf16 [rows][Hq][D] (rows may
+    be strided), over the cache (tm_kvb_attention); append the step's keys and
+    values first.  Returns out [rows][Hq][D].
+
+    scale: of the scores, finite; None or 0: 1 / sqrt(D)
+    lse:   fp32 [rows][Hq], receives the logarithm of each row's softmax sum
+    w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
+           token drew in this call; may be w_in
+    workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
+    head, tail, out, held = _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream)
+    st = (_lib or load()).tm_kvb_attention(*head, *tail)
     if st:
         raise TMError(st, "tm_kvb_attention")
     return out
+
+
+def kvb_attention_tree(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, tree: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       w_in: Optional[torch.Tensor] = None, w_out: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of a tree of drafted tokens (tm_kvb_attention_tree): each row sees the tokens before its
+    sequence's new ones, and of the new ones those that its mask names.
+
+    tree: int32 [rows][>= ceil(max_q / 32)], rows may be strided: bit k % 32 of word k / 32 stands for the
+          sequence's new token k (``tree_masks`` builds them from parents)
+
+    The rest as in kvb_attention, the workspace too."""
+    if (tree.dim() != 2 or tree.shape[0] != Q.shape[0] or tree.dtype is not torch.int32 or not tree.is_cuda
+            or 32 * tree.shape[1] < batch.max_q or (tree.stride(1) != 1 and tree.shape[1] > 1)):
+        raise ValueError("tree must be CUDA int32 [rows][ceil(max_q / 32)], its words contiguous")
+    head, tail, out, held = _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream)
+    stride = tree.stride(0) if tree.shape[0] > 1 else tree.shape[1]
+    st = (_lib or load()).tm_kvb_attention_tree(*head, tree.data_ptr(), stride, *tail)
+    if st:
+        raise TMError(st, "tm_kvb_attention_tree")
+    return out
+
+
+def tree_masks(parents) -> torch.Tensor:
+    """Masks for kvb_attention_tree from each sequence's parents: a list per sequence with every node's parent, an
+    earlier node of it, or -1.  Returns int32 [rows][words] on the host, the sequences' nodes one after another."""
+    words = max([(len(p) + 31) // 32 for p in parents] + [1])
+    rows = []
+    for p in parents:
+        sees = []
+        for i, up in enumerate(p):
+            if not -1 <= up < i:
+                raise ValueError("a node's parent is an earlier node, or -1")
+            sees.append((sees[up] if up >= 0 else 0) | 1 << i)
+        rows += [[(m >> 32 * k) & 0xffffffff for k in range(words)] for m in sees]
+    t = torch.tensor(rows, dtype=torch.int64).reshape(len(rows), words)
+    return torch.where(t >= 2 ** 31, t - 2 ** 32, t).to(torch.int32)
+
+
+class Rope:
+    """Rotation by position (tm_kvb_rope): table fp32 [positions][dims] with a position's dims / 2
+    cosines, then its sines; pairs (i, i + dims / 2), or neighbours where interleaved."""
+
+    def __init__(self, table: torch.Tensor, interleaved: bool = False):
+        if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] % 16 or table.shape[1] < 16:
+            raise ValueError("table must be fp32 [positions][dims], dims a multiple of 16")
+        self.table, self.interleaved = table, bool(interleaved)
+        self.positions, self.dims = table.shape
+        self._p = _dev(table, torch.float32, "table")
+
+
+def kvb_append_rope(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.Tensor, rope: Rope,
+                    Q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                    pos: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """kvb_append with the keys rotated by their positions, and the queries beside them (tm_kvb_append_rope).
+
+    Q:     fp16 or bf16 [rows][Hq][D] (rows may be strided); None: keys and values alone
+    q_out: receives the rotated queries, like Q; may be Q (None: allocated).  Returned
+    pos:   int32 [rows], each row's position; None: its slot in the cache"""
+    Hkv, D = cache.Hkv, cache.D
+    kp, ks, dtype, shape = _kvb_rows(K, Hkv, D, "K")
+    vp, vs, vdtype, vshape = _kvb_rows(V, Hkv, D, "V")
+    if vshape != shape or vdtype != dtype:
+        raise ValueError("V must have the shape and dtype of K")
+    rows = shape[0]
+    qp, qs, Hq, op, os_ = None, 0, 0, None, 0
+    if Q is not None:
+        qp, qs, qdtype, qshape = _kvb_rows(Q, None, D, "Q")
+        if qshape[0] != rows or qdtype != dtype:
+            raise ValueError("Q must have the rows and dtype of K")
+        Hq = qshape[1]
+        if q_out is None:
+            q_out = _empty(qshape, Q.dtype, Q.device, stream)
+        op, os_, odtype, oshape = _kvb_rows(q_out, Hq, D, "q_out")
+        if oshape != qshape or odtype != dtype:
+            raise ValueError("q_out must have the shape and dtype of Q")
+    elif q_out is not None:
+        raise ValueError("q_out comes with Q")
+    pp = None
+    if pos is not None:
+        if pos.shape != (rows,):
+            raise ValueError("pos must be int32 [rows]")
+        pp = _dev(pos, torch.int32, "pos")
+    wp, wn = _kvb_weights(w, batch.B, Hkv, "w")
+    r = KVBRopeStruct(rope._p, rope.positions, rope.dims, rope.interleaved, pp)
+    st = (_lib or load()).tm_kvb_append_rope(cache._ref, batch._rows(rows), kp, ks, vp, vs, qp, qs, Hq, op, os_,
+                                             ctypes.byref(r), dtype, wp, wn, _kvb_stream(cache, stream))
+    if st:
+        raise TMError(st, "tm_kvb_append_rope")
+    return q_out
+
+
+def kvb_accept(cache: KVBlocks, batch: KVBatch, path: torch.Tensor, count: torch.Tensor,
+               w: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Keep a path through the new tokens of each sequence (tm_kvb_accept): path int32 [B][n], ascending indices of
+    the sequence's new tokens, of which the first count[b] (int32 [B]) hold.  w: token weights fp32
+    [B][Hkv][tokens], moved along.  Returns new_len int32 [B]; batch.kv_len is left as it is."""
+    B = batch.B
+    if path.dim() != 2 or path.shape[0] != B or count.shape != (B,):
+        raise ValueError("path must be int32 [B][n] and count int32 [B]")
+    if new_len is None:
+        new_len = _empty(B, torch.int32, path.device, stream)
+    elif new_len.shape != (B,):
+        raise ValueError("new_len must be int32 [B]")
+    wp, wn = _kvb_weights(w, B, cache.Hkv, "w")
+    st = (_lib or load()).tm_kvb_accept(cache._ref, batch._ref, _dev(path, torch.int32, "path"), path.shape[1],
+                                        _dev(count, torch.int32, "count"), wp, wn, _dev(new_len, torch.int32, "new_len"),
+                                        _kvb_stream(cache, stream))
+    if st:
+        raise TMError(st, "tm_kvb_accept")
+    return new_len
 
 
 def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, first: int = 0, recent: int = 0,
@@ -962,3 +1105,66 @@ def kvb_evict(cache: KVBlocks, batch: KVBatch, w: torch.Tensor, budget: int, fir
                              _dev(new_len, torch.int32, "new_len"), _kvb_stream(cache, stream))
     _check(st, "tm_kvb_evict")
     return kept, new_len
+
+
+# ---- low-rank adapters beside a shared projection (include/tm_lora.h) ----
+
+class Adapters:
+    """The low-rank adapters of one projection: A fp16 [n][R][K], B fp16 [n][N][R], contiguous on one device; scale
+    fp32 [n] (None: 1).  R is a multiple of 8, 8 .. 128: pad lower ranks with zeros."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+            raise ValueError("A must be fp16 [n][R][K] and B fp16 [n][N][R]")
+        if scale is not None and scale.shape != A.shape[:1]:
+            raise ValueError("scale must be fp32 [n]")
+        n, R, K = A.shape
+        N = B.shape[1]
+        if R % 8 or not 8 <= R <= 128 or K % 8 or N % 8 or K < 8 or N < 8:
+            raise ValueError("R must be a multiple of 8 up to 128, K and N multiples of 8")
+        if A.device != B.device or (scale is not None and scale.device != A.device):
+            raise ValueError("A, B and scale must be on one device")
+        self.A, self.B, self.scale = A, B, scale
+        self.n, self.R, self.K, self.N, self.device, self.index = n, R, K, N, A.device, A.device.index
+        self._c = LoraAdaptersStruct(_dev(A, torch.float16, "A"), _dev(B, torch.float16, "B"),
+                                     None if scale is None else _dev(scale, torch.float32, "scale"), n, K, N, R)
+        self._ref = ctypes.byref(self._c)
+
+
+def _lora_rows(t: torch.Tensor, cols: int, name: str):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != cols or t.dtype is not torch.float16 or not t.is_cuda or stride[1] != 1:
+        raise ValueError(f"{name} must be a CUDA fp16 tensor [rows][{cols}] (its rows may have a stride)")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else cols
+
+
+def lora_add(Y: torch.Tensor, X: torch.Tensor, adapters: Adapters, ids: torch.Tensor,
+             q_start: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out = Y + scale[a] (X . A[a]^T) . B[a]^T with a the adapter of each row's sequence (tm_lora_add): Y fp16
+    [rows][N], a projection's output, X fp16 [rows][K], its input (rows may be strided).
+
+    ids:     int32 [B], each sequence's adapter; outside 0 .. n-1: none
+    q_start: int32 [B + 1], where each sequence's rows begin; None: one row each
+    out:     fp16 [rows][N]; None: Y itself.  Rows of no sequence are left as they are"""
+    yp, ys = _lora_rows(Y, adapters.N, "Y")
+    xp, xs = _lora_rows(X, adapters.K, "X")
+    rows = X.shape[0]
+    if Y.shape[0] != rows:
+        raise ValueError("Y must have the rows of X")
+    op, os_ = yp, ys
+    if out is None:
+        out = Y
+    else:
+        op, os_ = _lora_rows(out, adapters.N, "out")
+        if out.shape[0] != rows:
+            raise ValueError("out must have the rows of X")
+    B = ids.shape[0] if ids.dim() == 1 else -1
+    if B < 0 or (q_start is None and B != rows) or (q_start is not None and q_start.shape != (B + 1,)):
+        raise ValueError("ids must be int32 [B], q_start int32 [B + 1] (None: one row each)")
+    st = (_lib or load()).tm_lora_add(adapters._ref, xp, xs, yp, ys, op, os_, rows, _dev(ids, torch.int32, "ids"),
+                                      None if q_start is None else _dev(q_start, torch.int32, "q_start"), B,
+                                      _kvb_stream(adapters, stream))
+    if st:
+        raise TMError(st, "tm_lora_add")
+    return out

@@ -99,8 +99,8 @@ __device__ __noinline__ void drain_copies(uint32_t bars, int i, int steps) {
   });
 }
 
-// KEEP: the scores are kept for the tokens' weights.
-template <int FMT, int D, int RT, bool KEEP>
+// KEEP: the scores are kept for the tokens' weights.  TREE: the new tokens are seen by the rows' masks.
+template <int FMT, int D, int RT, bool KEEP, bool TREE>
 __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
     attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
   using SH = FewShape<D, RT>;
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
   // Tokens [j0, j1) that some row of the group sees; all rows see those up to `all`.
   const int last_i = (min(row_base + SH::ROWS, rows) - 1) / P.G;
   const int j0 = chunk * P.chunk;
-  const int j1 = min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
-  const int all = min(s.old + row_base / P.G, j1 - 1);
+  const int j1 = TREE ? min(s.len, j0 + P.chunk) : min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
+  const int all = min(TREE ? s.old - 1 : s.old + row_base / P.G, j1 - 1);
   if (j0 >= j1 && chunk > 0) return;  // slice 0 still writes what an empty row gives
   const int steps = j1 > j0 ? (j1 - j0 + kStep - 1) / kStep : 0;
   const int mine = steps > warp ? (steps - warp + kFewWarps - 1) / kFewWarps : 0;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
   uint32_t qa[RT == 2 ? 1 : KS][RT == 0 ? 2 : 4];
   float mul[TILES][E];
   int last[TILES][E];  // last visible token (-1: no row)
+  [[maybe_unused]] const uint32_t* mask[TILES][E];
   size_t hr[TILES][E];
 #pragma unroll
   for (int rt = 0; rt < TILES; ++rt)
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
       const bool ok = row < rows;
       const int i = ok ? row / P.G : 0;
       const int hq = h * P.G + (ok ? row - i * P.G : 0);
-      last[rt][e] = ok ? min(s.old + i, s.len - 1) : -1;
+      last[rt][e] = ok ? (TREE ? s.len - 1 : min(s.old + i, s.len - 1)) : -1;
+      if constexpr (TREE) mask[rt][e] = P.tree + (s.row0 + i) * P.tree_stride;
       hr[rt][e] = (size_t)(s.row0 + i) * P.Hq + hq;
       const uint16_t* q = P.Q + (s.row0 + i) * P.q_stride + (long long)hq * D;
       uint32_t raw[KS][2];
@@ -361,12 +363,16 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
 #pragma unroll
       for (int rt = 0; rt < TILES; ++rt)
 #pragma unroll
-        for (int e = 0; e < E; ++e)
+        for (int e = 0; e < E; ++e) {
+          uint32_t see = 0xffffffffu;
+          if (TREE && tok0 + kStep > s.old) see = last[rt][e] >= 0 ? tree_bits(P, mask[rt][e], tok0 - s.old) : 0u;
 #pragma unroll
           for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              if (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e]) sc[rt][a][2 * e + x] = -INFINITY;
+              if (!there[a >> 1] || tok0 + 8 * a + sg[x] > last[rt][e] || (TREE && !((see >> (8 * a + sg[x])) & 1u)))
+                sc[rt][a][2 * e + x] = -INFINITY;
+        }
     // The scores for the weights.  With more than 8 rows a swap makes a lane's two tokens neighbours, so that four
     // lanes write a whole sector (16 x 5 drafts: 65 us, without 68 then); with 8 its registers cost more (32 x 4096
     // tokens: 66, without 64).
@@ -577,11 +583,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, FewShape<D, RT>::CTAS)
 }
 
 // Slices that the CTAs of row (query i, head g of the group) wrote: up to the
-// last token that the rows they share see, and slice 0.
+// last token that the rows they share see (of a tree: to the end), and slice 0.
+template <bool TREE>
 __device__ __forceinline__ int slices_of(const AttnParams& P, const Span& s, int i, int g) {
   const int per = P.rows_per_cta;
   const int last_i = (min(((i * P.G + g) / per + 1) * per, s.n * P.G) - 1) / P.G;
-  const int end = min(s.len, s.old + last_i + 1);
+  const int end = TREE ? s.len : min(s.len, s.old + last_i + 1);
   return end > 0 ? (end + P.chunk - 1) / P.chunk : 1;
 }
 
@@ -591,7 +598,7 @@ __device__ __forceinline__ int slices_of(const AttnParams& P, const Span& s, int
 constexpr int kFinishThreads = 256;
 constexpr int kWeightTokens = 4 * kFinishThreads;
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams P, int joins) {
   constexpr int E = D / 32;
   __shared__ float acc_s[8][D], l_s[8];
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
     const int i = at / P.Hq;
     const bool ok = i < s.n;
     const size_t hr = (size_t)(s.row0 + (ok ? i : 0)) * P.Hq + (at - i * P.Hq);
-    const int n = ok ? slices_of(P, s, i, (at - i * P.Hq) % P.G) : 0;
+    const int n = ok ? slices_of<TREE>(P, s, i, (at - i * P.Hq) % P.G) : 0;
     const float2* ml = P.part_ml + hr * P.chunks;
     float m = kNone;
     for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
       float m = kNone, l = 0.f;
       if (row < rows) {
         const int i = row / P.G, g = row - i * P.G;
-        const int n = slices_of(P, s, i, g);
+        const int n = slices_of<TREE>(P, s, i, g);
         const float2* ml = P.part_ml + ((size_t)(s.row0 + i) * P.Hq + h * P.G + g) * P.chunks;
         for (int c = tid & 7; c < n; c += 8) {
           const float2 v = ml[c];
@@ -672,20 +679,20 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
       }
       if ((tid & 7) == 0 && row < rows) {
         lse_s[row] = l == 0.f ? INFINITY : log2f(l) + m;  // nothing seen: no weight
-        see_s[row] = min(s.old + row / P.G, s.len - 1);
+        see_s[row] = TREE ? s.len - 1 : min(s.old + row / P.G, s.len - 1);
       }
     }
   }
   __syncthreads();
-  // Four tokens per thread.  The rows' CTAs wrote every score up to the row's last visible token;
-  // what the row does not see before that (holes) is -inf.
+  // Four tokens per thread.  The rows' CTAs wrote every score up to the row's last visible token (of a tree: of
+  // every token); what the row does not see before that (holes, other branches) is -inf.
   const size_t head = ((size_t)b * V.Hkv + h) * P.w_stride;
   const int j = part * kWeightTokens + 4 * tid;
   if (j >= P.w_stride) return;
   float sum[4] = {};
   if (j < s.len) {
-    const int r0 = max(j - s.old, 0) * P.G;  // rows from here on see the first of them,
-    const int r4 = j + 3 < s.len ? min(max(j + 3 - s.old, 0) * P.G, rows) : rows;  // and from here on all four
+    const int r0 = TREE ? 0 : max(j - s.old, 0) * P.G;  // rows from here on see the first of them,
+    const int r4 = j + 3 < s.len ? TREE ? 0 : min(max(j + 3 - s.old, 0) * P.G, rows) : rows;  // from here on all four
     const float* sc = P.scores + ((size_t)h * V.rows + s.row0) * P.G * P.score_stride + j;
 #pragma unroll 8
     for (int row = r0; row < r4; ++row) {
@@ -712,22 +719,22 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const AttnParams
     if (j + k < P.w_stride) P.w_out[head + j + k] = (P.w_in ? P.w_in[head + j + k] : 0.f) + sum[k];
 }
 
-template <int FMT, int D, int RT, bool KEEP>
+template <int FMT, int D, int RT, bool KEEP, bool TREE>
 tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int groups, cudaStream_t s) {
   using SH = FewShape<D, RT>;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(attn_kernel<FMT, D, RT, KEEP>), SH::SMEM)) return TM_ERR_CUDA;
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(attn_kernel<FMT, D, RT, KEEP, TREE>), SH::SMEM)) return TM_ERR_CUDA;
   const dim3 grid((unsigned)P.chunks, (unsigned)(P.V.Hkv * groups), (unsigned)P.V.B);
-  attn_kernel<FMT, D, RT, KEEP><<<grid, 32 * kFewWarps, SH::SMEM, s>>>(tmK, tmV, P);
+  attn_kernel<FMT, D, RT, KEEP, TREE><<<grid, 32 * kFewWarps, SH::SMEM, s>>>(tmK, tmV, P);
   return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
 }
 
-template <int FMT, int D, bool KEEP>
+template <int FMT, int D, bool KEEP, bool TREE>
 tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int rt, int groups,
                       cudaStream_t s) {
-  if (rt == 0) return launch_attn<FMT, D, 0, KEEP>(tmK, tmV, P, groups, s);
-  if (rt == 1) return launch_attn<FMT, D, 1, KEEP>(tmK, tmV, P, groups, s);
-  return launch_attn<FMT, D, 2, KEEP>(tmK, tmV, P, groups, s);
+  if (rt == 0) return launch_attn<FMT, D, 0, KEEP, TREE>(tmK, tmV, P, groups, s);
+  if (rt == 1) return launch_attn<FMT, D, 1, KEEP, TREE>(tmK, tmV, P, groups, s);
+  return launch_attn<FMT, D, 2, KEEP, TREE>(tmK, tmV, P, groups, s);
 }
 
 // A 16-token box of a pool [cells][T][D]; inner rows of D bytes, swizzled over their width.
@@ -856,7 +863,7 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
   return TM_OK;
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool TREE>
 static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cudaStream_t s, int* launches) {
   const View& V = P.V;
   tm_status st;
@@ -865,8 +872,8 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
   } else {
     CUtensorMap tmK, tmV;
     if (!pool_map(&tmK, cache->k, V, D) || !pool_map(&tmV, cache->v, V, D)) return TM_ERR_CUDA;
-    st = p.scores ? launch_attn<FMT, D, true>(tmK, tmV, P, p.rt, p.groups, s)
-                  : launch_attn<FMT, D, false>(tmK, tmV, P, p.rt, p.groups, s);
+    st = p.scores ? launch_attn<FMT, D, true, TREE>(tmK, tmV, P, p.rt, p.groups, s)
+                  : launch_attn<FMT, D, false, TREE>(tmK, tmV, P, p.rt, p.groups, s);
   }
   if (st != TM_OK) return st;
   *launches = 1;
@@ -887,7 +894,7 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, finish_kernel<D>, P, (int)joins) != cudaSuccess) return TM_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, finish_kernel<D, TREE>, P, (int)joins) != cudaSuccess) return TM_ERR_CUDA;
     ++*launches;
   }
   if (P.w_out && !p.scores) {
@@ -898,10 +905,11 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
   return TM_OK;
 }
 
-extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
-                                      long long q_stride, int Hq, int dtype, float scale, void* out, float* lse,
-                                      const float* w_in, float* w_out, long long w_stride, void* workspace,
-                                      size_t workspace_bytes, void* stream) {
+template <bool TREE>
+static tm_status attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q, long long q_stride,
+                           int Hq, int dtype, float scale, const uint32_t* tree, long long tree_stride, void* out,
+                           float* lse, const float* w_in, float* w_out, long long w_stride, void* workspace,
+                           size_t workspace_bytes, void* stream) {
   AttnParams P = {};
   tm_status st = check(cache, batch, true, &P.V);
   if (st == TM_OK) st = check_heads(P.V, batch, Hq);
@@ -925,6 +933,13 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   if (!Q || !out || q_stride < (long long)Hq * cache->D) return TM_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
     return TM_ERR_ALIGNMENT;
+  if (TREE) {
+    P.tree = tree;
+    P.tree_stride = tree_stride;
+    P.tree_words = (V.max_q - 1) / 32 + 1;
+    if (!tree || tree_stride < P.tree_words) return TM_ERR_INVALID_ARG;
+    if (!aligned(tree, 4)) return TM_ERR_ALIGNMENT;
+  }
   const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr);
   if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return TM_ERR_INVALID_ARG;
@@ -951,11 +966,28 @@ extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_ba
   }
   int launches = 0;
   if (cache->format == TM_KVB_INT8)
-    st = cache->D == 64 ? run<TM_KVB_INT8, 64>(P, p, cache, s, &launches)
-                        : run<TM_KVB_INT8, 128>(P, p, cache, s, &launches);
+    st = cache->D == 64 ? run<TM_KVB_INT8, 64, TREE>(P, p, cache, s, &launches)
+                        : run<TM_KVB_INT8, 128, TREE>(P, p, cache, s, &launches);
   else
-    st = cache->D == 64 ? run<TM_KVB_E4M3, 64>(P, p, cache, s, &launches)
-                        : run<TM_KVB_E4M3, 128>(P, p, cache, s, &launches);
+    st = cache->D == 64 ? run<TM_KVB_E4M3, 64, TREE>(P, p, cache, s, &launches)
+                        : run<TM_KVB_E4M3, 128, TREE>(P, p, cache, s, &launches);
   if (st == TM_OK) set_launch_count(launches);
   return st;
+}
+
+extern "C" tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
+                                      long long q_stride, int Hq, int dtype, float scale, void* out, float* lse,
+                                      const float* w_in, float* w_out, long long w_stride, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  return attention<false>(cache, batch, Q, q_stride, Hq, dtype, scale, nullptr, 0, out, lse, w_in, w_out, w_stride,
+                          workspace, workspace_bytes, stream);
+}
+
+extern "C" tm_status tm_kvb_attention_tree(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
+                                           long long q_stride, int Hq, int dtype, float scale, const uint32_t* tree,
+                                           long long tree_stride, void* out, float* lse, const float* w_in,
+                                           float* w_out, long long w_stride, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+  return attention<true>(cache, batch, Q, q_stride, Hq, dtype, scale, tree, tree_stride, out, lse, w_in, w_out,
+                         w_stride, workspace, workspace_bytes, stream);
 }

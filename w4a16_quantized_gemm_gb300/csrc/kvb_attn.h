@@ -27,6 +27,10 @@ struct AttnParams {
   float2* part_ml;    // [rows][Hq][chunks]: m, l
   float* scores;      // [Hkv][rows x G][score_stride], base-2 logarithms of the unnormalised weights
   long long score_stride;
+  // A tree's masks, [rows][tree_stride] words of which the first tree_words count; NULL: causal.
+  const uint32_t* tree;
+  long long tree_stride;
+  int tree_words;
 };
 
 // The tcgen05 kernel (kvb_prefill.cu): `pairs` pairs of 128-row tiles per
@@ -37,6 +41,13 @@ tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs,
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream);
 
 #if defined(__CUDACC__)
+// What a tree's row sees of 32 tokens: bit x stands for new token `first` + x (below 0: a token before the tree).
+__device__ __forceinline__ uint32_t tree_bits(const AttnParams& P, const uint32_t* mask, int first) {
+  const int at = first >> 5;  // rounds down
+  auto word = [&](int k) { return k < 0 ? 0xffffffffu : k < P.tree_words ? mask[k] : 0u; };
+  return __funnelshift_r(word(at), word(at + 1), first & 31);
+}
+
 // mbar_wait with a spin before the timer comes in.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
 #pragma unroll 1

@@ -83,7 +83,7 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   return v;
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool TREE>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParams P) {
   using SH = PreShape<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
   if (row_base >= rows) return;
   const int last_i = (min(row_base + 2 * kPreTile, rows) - 1) / P.G;
   const int j0 = chunk * P.chunk;
-  const int j1 = min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
+  const int j1 = TREE ? min(s.len, j0 + P.chunk) : min(min(s.len, j0 + P.chunk), s.old + last_i + 1);
   if (j0 >= j1 && chunk > 0) return;  // slice 0 still writes what an empty row gives
   const int N = j1 > j0 ? (j1 - j0 + kPreTile - 1) / kPreTile : 0;
   const int M = rows - row_base > kPreTile ? 2 : 1;  // row tiles
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     const bool ok = row < rows;
     const int qi = ok ? row / P.G : 0;
     const size_t hr = (size_t)(s.row0 + qi) * P.Hq + h * P.G + (ok ? row - qi * P.G : 0);
-    const int last = ok ? min(s.old + qi, s.len - 1) : -1;  // last visible token
+    const int last = ok ? (TREE ? s.len - 1 : min(s.old + qi, s.len - 1)) : -1;  // last visible token
     float mul = fabsf(P.scale_log2);
     if (i < M) {
       // The row's queries into shared memory, as fp16; bf16 rows times a power of two.  A negative
@@ -292,6 +292,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > rel || ((holes >> (c >> 4)) & 1u)) v[c >> 5][c & 31] = 0xff800000u;
+        }
+        if (TREE && j0 + (n + 1) * kPreTile > s.old) {  // a tile with new tokens
+          const uint32_t* mask = P.tree + (s.row0 + qi) * P.tree_stride;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = ok ? tree_bits(P, mask, j0 + n * kPreTile + 32 * c - s.old) : 0u;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((see >> x) & 1u)) v[c][x] = 0xff800000u;
+          }
         }
         float tm = -INFINITY;
 #pragma unroll
@@ -519,14 +529,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool TREE>
 static tm_status launch(const AttnParams& P, int pairs, cudaStream_t stream) {
   using SH = PreShape<D>;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(prefill_kernel<FMT, D>), SH::SMEM)) return TM_ERR_CUDA;
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(prefill_kernel<FMT, D, TREE>), SH::SMEM)) return TM_ERR_CUDA;
   const dim3 grid((unsigned)(P.V.B * P.V.Hkv), (unsigned)(pairs * P.chunks));
-  prefill_kernel<FMT, D><<<grid, kPreThreads, SH::SMEM, stream>>>(P);
+  prefill_kernel<FMT, D, TREE><<<grid, kPreThreads, SH::SMEM, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
+template <int FMT, int D>
+static tm_status launch(const AttnParams& P, int pairs, cudaStream_t stream) {
+  return P.tree ? launch<FMT, D, true>(P, pairs, stream) : launch<FMT, D, false>(P, pairs, stream);
 }
 
 tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs, cudaStream_t stream) {

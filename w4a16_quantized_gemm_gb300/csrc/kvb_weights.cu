@@ -40,7 +40,8 @@ struct WtShape {
   static constexpr uint32_t SMEM = BARS + 128 + 1024;
 };
 
-template <int FMT, int D, bool BF16>
+// TREE: every row sees the tokens before the new ones, and of these those that its mask names.
+template <int FMT, int D, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams P) {
   using SH = WtShape<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   const int tok0 = blockIdx.y * kWtTokens;
   const Span s = span(V, b);
   const int rows = s.n * P.G;
-  const int first = max(tok0 - s.old, 0);  // the first query that sees a token of the tile
+  const int first = TREE ? 0 : max(tok0 - s.old, 0);  // the first query that sees a token of the tile
   const int r0 = first < s.n ? first * P.G : rows;
   const int tiles = tok0 < s.len && r0 < rows ? (rows - r0 + kWtTile - 1) / kWtTile : 0;
   const int N = (tiles - share + P.split - 1) / P.split;  // tiles share, share + split, ... are this CTA's
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   // Whether some row of tile n sees the second token tile at all; once it does, later ones do.
   auto second = [&](int n) {
     const int last_i = (min(first_row(n) + kWtTile, rows) - 1) / P.G;
-    return tok0 + kWtTile < s.len && s.old + last_i >= tok0 + kWtTile;
+    return tok0 + kWtTile < s.len && (TREE || s.old + last_i >= tok0 + kWtTile);
   };
 
   const uint32_t bars = base + SH::BARS;
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       }
       ++seen;
       tc_fence_after();
-      const bool whole = s.old + first_row(n) / P.G >= tok0 + kWtTile * half + kWtTile - 1;  // every row sees every token
+      // whether every row sees every token
+      const bool whole = s.old + (TREE ? -1 : first_row(n) / P.G) >= tok0 + kWtTile * half + kWtTile - 1;
       uint64_t part[4] = {};
 #pragma unroll 1
       for (int x0 = 0; x0 < 128; x0 += 64) {  // 64 rows at a time: 128 scores would not fit the registers
@@ -181,7 +183,20 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
             const int2 see = *reinterpret_cast<const int2*>(last + 4 * k);
             const float p0 = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x));
             const float p1 = ex2(fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y));
-            part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(j <= see.x ? p0 : 0.f, j <= see.y ? p1 : 0.f));
+            bool see0, see1;
+            if constexpr (TREE) {
+              const int node = j - s.old;  // its word is the same one for most of the warp: a broadcast
+              auto sees = [&](int row) {
+                return node < 0 || (row >= 0 && (node >> 5) < P.tree_words &&
+                                    ((P.tree[row * P.tree_stride + (node >> 5)] >> (node & 31)) & 1u));
+              };
+              see0 = sees(see.x);
+              see1 = sees(see.y);
+            } else {
+              see0 = j <= see.x;
+              see1 = j <= see.y;
+            }
+            part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(see0 ? p0 : 0.f, see1 ? p1 : 0.f));
           }
         }
       }
@@ -215,7 +230,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
       if (n < N) {
         const int slot = n % kWtSlots;
         const float x = lrow < rows ? P.lse[(size_t)(s.row0 + li) * P.Hq + h * G + lg] : -INFINITY;
-        const int last = lrow < rows ? min(s.old + li, s.len - 1) : -1;
+        // the row's last visible token (of a tree: its mask's row); none: -1
+        const int last = lrow < rows ? (TREE ? s.row0 + li : min(s.old + li, s.len - 1)) : -1;
         alive = alive && wait_bar(q_empty(slot), ((uint32_t)(n / kWtSlots) & 1u) ^ 1u, abort_flag, &s_err_kvbw);
         if (alive) {
           const uint32_t dst = base + slot * SH::TILE + (c >> 3) * SH::PANEL;
@@ -331,11 +347,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
-template <int FMT, int D, bool BF16>
+template <int FMT, int D, bool BF16, bool TREE>
 static tm_status launch(const AttnParams& P, cudaStream_t stream) {
   using SH = WtShape<D>;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(weights_kernel<FMT, D, BF16>), SH::SMEM)) return TM_ERR_CUDA;
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(weights_kernel<FMT, D, BF16, TREE>), SH::SMEM)) return TM_ERR_CUDA;
   AttnParams Q = P;
   Q.split = kWtSplit;
   cudaLaunchConfig_t cfg = {};
@@ -350,12 +366,13 @@ static tm_status launch(const AttnParams& P, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_kernel<FMT, D, BF16>, Q) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, weights_kernel<FMT, D, BF16, TREE>, Q) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
 }
 
 template <int FMT, int D>
 static tm_status launch(const AttnParams& P, cudaStream_t stream) {
-  return P.bf16 ? launch<FMT, D, true>(P, stream) : launch<FMT, D, false>(P, stream);
+  if (P.tree) return P.bf16 ? launch<FMT, D, true, true>(P, stream) : launch<FMT, D, false, true>(P, stream);
+  return P.bf16 ? launch<FMT, D, true, false>(P, stream) : launch<FMT, D, false, false>(P, stream);
 }
 
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream) {
