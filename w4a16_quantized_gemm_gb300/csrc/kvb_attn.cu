@@ -760,7 +760,7 @@ struct Plan {
   size_t part, part_ml, lse, score, bytes;  // offsets, total
 };
 
-static Plan make_plan(const View& V, int D, int Hq, bool weights) {
+static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
   Plan p = {};
   const int G = Hq / V.Hkv;
   const long long rows = (long long)V.max_q * G;
@@ -768,7 +768,10 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
   // 64 rows (16 sequences x 2000 tokens, 8 heads a group): this kernel 51.5 us, with weights 99.6; the tcgen05
   // kernel 47.6, with its second pass for the weights 124.  At 32 rows this one takes 39.
   p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (weights ? kFewRows : kFewRows / 2) ? 2 : -1;
-  p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : 256;
+  // Trees: up to 128 rows have a tcgen05 kernel of their own (16 sequences of 4096 tokens, 8 KV heads: 32 rows 53 us
+  // in the kernel for few rows and 55 in that one, 128 rows 52).
+  const bool narrow = tree && p.rt < 0 && rows <= 128;
+  p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : narrow ? 128 : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
   const long long ctas = (long long)V.B * V.Hkv * p.groups;
   long long chunk, least, unit;
@@ -779,6 +782,21 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights) {
     unit = kTile;
     least = 2 * kTile;
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
+  } else if (tree) {
+    // The slices for which waves of CTAs x (tiles of a slice + what starting a CTA costs, about six) is the least;
+    // the joining launch costs about four.
+    unit = 128;
+    least = 512;
+    const long long tiles = (V.max_len + 127) / 128;
+    long long best = 1, cost = -1;
+    for (long long c = 1; c == 1 || (c <= 64 && tiles / c >= 4); ++c) {
+      const long long t = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 6) + (c > 1 ? 4 : 0);
+      if (cost < 0 || t < cost) {
+        best = c;
+        cost = t;
+      }
+    }
+    chunk = (V.max_len + best - 1) / best;
   } else {
     // Slices only where the rows alone leave SMs idle (300 tokens over 30000: 182 us; unsliced 574).
     unit = 128;
@@ -857,9 +875,9 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
   if (st != TM_OK) return st;
   *bytes = 0;
   if (V.B == 0 || V.rows == 0 || V.max_q == 0) return TM_OK;
-  const Plan p = make_plan(V, cache->D, Hq, weights != 0);
+  const Plan p = make_plan(V, cache->D, Hq, weights != 0, false), t = make_plan(V, cache->D, Hq, weights != 0, true);
   if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
-  *bytes = p.bytes;
+  *bytes = p.bytes > t.bytes ? p.bytes : t.bytes;
   return TM_OK;
 }
 
@@ -868,7 +886,7 @@ static tm_status run(AttnParams P, const Plan& p, const tm_kvb_cache* cache, cud
   const View& V = P.V;
   tm_status st;
   if (p.rt < 0) {
-    st = launch_prefill_attn(P, FMT, D, p.groups, s);
+    st = p.rows_per_cta == 128 ? launch_tree_attn(P, FMT, D, s) : launch_prefill_attn(P, FMT, D, p.groups, s);
   } else {
     CUtensorMap tmK, tmV;
     if (!pool_map(&tmK, cache->k, V, D) || !pool_map(&tmV, cache->v, V, D)) return TM_ERR_CUDA;
@@ -940,7 +958,7 @@ static tm_status attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
     if (!tree || tree_stride < P.tree_words) return TM_ERR_INVALID_ARG;
     if (!aligned(tree, 4)) return TM_ERR_ALIGNMENT;
   }
-  const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr);
+  const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr, TREE);
   if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return TM_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -37,6 +37,9 @@ struct AttnParams {
 // (sequence, KV head); slices of P.chunk tokens, a multiple of 128.
 tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs, cudaStream_t stream);
 
+// The same for trees of up to 128 rows a KV head (kvb_tree.cu).
+tm_status launch_tree_attn(const AttnParams& P, int format, int D, cudaStream_t stream);
+
 // The weights that tokens drew from many rows, by their lse (kvb_weights.cu).
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream);
 
@@ -46,6 +49,18 @@ __device__ __forceinline__ uint32_t tree_bits(const AttnParams& P, const uint32_
   const int at = first >> 5;  // rounds down
   auto word = [&](int k) { return k < 0 ? 0xffffffffu : k < P.tree_words ? mask[k] : 0u; };
   return __funnelshift_r(word(at), word(at + 1), first & 31);
+}
+
+// What a tree's row sees of columns 32 c .. 32 c + 31 of a token tile: up to column `rel`, without holes (a bit per
+// 16 columns), and of the new tokens, of which the tile's first is number `fresh`, those in its mask.
+__device__ __forceinline__ uint32_t tree_columns(const AttnParams& P, const uint32_t* mask, int fresh, int rel,
+                                                 uint32_t holes, int c) {
+  const int x = rel - 32 * c;
+  uint32_t see = x >= 31 ? 0xffffffffu : x < 0 ? 0u : (2u << x) - 1u;
+  if ((holes >> (2 * c)) & 1u) see &= 0xffff0000u;
+  if ((holes >> (2 * c)) & 2u) see &= 0x0000ffffu;
+  if (fresh + 32 * c + 32 > 0 && x >= 0) see &= tree_bits(P, mask, fresh + 32 * c);
+  return see;
 }
 
 // mbar_wait with a spin before the timer comes in.
@@ -95,10 +110,116 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
       : "memory");
 }
 
+// MN-major operand: rows of K (tokens) of 128 bytes, 128-byte swizzle, 8-row
+// atoms 1024 bytes apart along K, 64-element panels `panel` bytes apart along N.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t panel) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+
+// 16 bytes, or zeros.
+__device__ __forceinline__ uint4 ldg_or_zero(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)ok));
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// Into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// One warp: pages and scales of the 16-token groups of N token tiles of 128 (from token j0 on, up to j1), a slot of
+// META [SLOTS][8] x {ks, log2 vs, 1 / vs, group of the pool} and one of HOLES (bits) for each.  A page's number, then its
+// scales: two loads that wait for each other, so that lane 8 i + g takes group g of tile i of four tiles at once, the
+// scales four tiles ahead and the numbers eight (tile by tile they cost 3.2 k cycles each, more than all the rest of
+// a tile of 128 rows).  The codes are requested into L2 on the way, four tiles ahead.
+template <int D, int SLOTS>
+__device__ __forceinline__ void publish_pages(const View& V, int b, int h, int j0, int j1, int N, uint32_t meta,
+                                              uint32_t holes_at, uint32_t full, uint32_t empty,
+                                              volatile int* abort_flag, uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const int* table = V.table + (size_t)b * V.table_stride;
+  auto token = [&](int n) { return j0 + n * 128 + 16 * lane; };  // the lane's of tiles n .. n + 3
+  auto entry = [&](int n) { return token(n) < j1 ? table[token(n) >> V.t_shift] : -1; };
+  struct Group {
+    float ks, vs;
+    uint32_t at;
+    bool hole;
+  };
+  auto scales = [&](int n, int page) {
+    const int j = token(n);
+    const bool there = (unsigned)page < (unsigned)V.pages && j < j1;
+    Group g = {1.f, 1.f, 0xffffffffu, j < j1 && !there};
+    if (there) {
+      const size_t cell = (size_t)page * V.Hkv + h;
+      g.at = (uint32_t)(((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) >> 4);
+      g.ks = V.ks[cell];
+      g.vs = V.vs[cell];
+    }
+    return g;
+  };
+  // A page at a time: each of these copies takes its thread about 60 cycles.
+  auto request = [&](int n, const Group& g) {
+    if (g.at != 0xffffffffu && (token(n) & ((1 << V.t_shift) - 1)) == 0) {
+      prefetch_l2(V.k + (size_t)g.at * (16 * D), D << V.t_shift);
+      prefetch_l2(V.v + (size_t)g.at * (16 * D), D << V.t_shift);
+    }
+  };
+  int page = entry(0);
+  Group next = scales(0, page);
+  page = entry(4);
+#pragma unroll 1
+  for (int n0 = 0; n0 < N; n0 += 4) {
+    const Group g = next;
+    next = scales(n0 + 4, page);  // past the end: nothing
+    page = entry(n0 + 8);
+    const float lv = __log2f(fmaxf(g.vs, kScaleFloor)), inv = ex2(-lv);
+    const uint32_t holes = __ballot_sync(0xffffffffu, g.hole);
+#pragma unroll 1
+    for (int n = n0; n < N && n < n0 + 4; ++n) {
+      const int slot = n % SLOTS;
+      const bool alive = wait_bar(empty + 8 * slot, ((uint32_t)(n / SLOTS) & 1u) ^ 1u, abort_flag, err);
+      if (!__all_sync(0xffffffffu, alive)) return;
+      if (lane >> 3 == n - n0)
+        sts128(meta + slot * 128 + (lane & 7) * 16, __float_as_uint(g.ks), __float_as_uint(lv), __float_as_uint(inv), g.at);
+      if (lane == 0)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(holes_at + 4 * slot), "r"((holes >> (8 * (n - n0))) & 0xffu) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * slot);
+      if (lane >> 3 == n - n0) request(n0 + 4, next);
+      __syncwarp();
+    }
+  }
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// tcgen05.wait::ld for a load into r: what reads r stays behind the wait.
+__device__ __forceinline__ void tc_wait_ld_of(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // Tensor memory: 32 lanes x 32 consecutive 32-bit columns, thread i to lane (base lane + i).
@@ -111,6 +232,15 @@ __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t 
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 #endif

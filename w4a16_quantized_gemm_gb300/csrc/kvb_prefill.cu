@@ -58,31 +58,6 @@ struct PreShape {
   static constexpr uint32_t SMEM = BARS + 256 + 1024;
 };
 
-// MN-major operand: rows of K (tokens) of 128 bytes, 128-byte swizzle, 8-row
-// atoms 1024 bytes apart along K, 64-element panels `panel` bytes apart along N.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t panel) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-         (uint64_t)1u << 46 | (uint64_t)2u << 61;
-}
-
-// 16 bytes, or zeros.
-__device__ __forceinline__ uint4 ldg_or_zero(const void* p, bool ok) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((int)ok));
-  return v;
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-
 template <int FMT, int D, bool TREE>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParams P) {
   using SH = PreShape<D>;
@@ -226,6 +201,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     const int qi = ok ? row / P.G : 0;
     const size_t hr = (size_t)(s.row0 + qi) * P.Hq + h * P.G + (ok ? row - qi * P.G : 0);
     const int last = ok ? (TREE ? s.len - 1 : min(s.old + qi, s.len - 1)) : -1;  // last visible token
+    [[maybe_unused]] const uint32_t* mask = TREE ? P.tree + (s.row0 + qi) * P.tree_stride : nullptr;
     float mul = fabsf(P.scale_log2);
     if (i < M) {
       // The row's queries into shared memory, as fp16; bf16 rows times a power of two.  A negative
@@ -288,19 +264,24 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
         tc_wait_ld();
         const int rel = last - (j0 + n * kPreTile);  // columns 0 .. rel are visible
         const uint32_t holes = lds32(base + SH::HOLES + 4 * slot);
-        if (!__all_sync(0xffffffffu, rel >= kPreTile - 1) || holes) {
+        if constexpr (!TREE) {
+          if (!__all_sync(0xffffffffu, rel >= kPreTile - 1) || holes) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > rel || ((holes >> (c >> 4)) & 1u)) v[c >> 5][c & 31] = 0xff800000u;
-        }
-        if (TREE && j0 + (n + 1) * kPreTile > s.old) {  // a tile with new tokens
-          const uint32_t* mask = P.tree + (s.row0 + qi) * P.tree_stride;
+            for (int c = 0; c < 128; ++c)
+              if (c > rel || ((holes >> (c >> 4)) & 1u)) v[c >> 5][c & 31] = 0xff800000u;
+          }
+        } else {
+          // Tiles with new tokens, the end or holes.  A bit a column: what these loops hold has to stay in the
+          // instruction cache (with comparisons a column, tiles without any of this took half as long again).
+          const int fresh = j0 + n * kPreTile - s.old;
+          if (fresh + kPreTile > 0 || !__all_sync(0xffffffffu, rel >= kPreTile - 1) || holes) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t see = ok ? tree_bits(P, mask, j0 + n * kPreTile + 32 * c - s.old) : 0u;
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = tree_columns(P, mask, fresh, rel, holes, c);
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((see >> x) & 1u)) v[c][x] = 0xff800000u;
+              for (int k = 0; k < 32; ++k)
+                if (!((see >> k) & 1u)) v[c][k] = 0xff800000u;
+            }
           }
         }
         float tm = -INFINITY;
@@ -491,34 +472,39 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
       convert(std::integral_constant<int, D == 128 ? 4 : 2>{}, 96 + (warp - 14) * kWarpRows, 2 * kWarpRows);
     } else if (warp == 13) {
       // ---------------- pages and scales ----------------
-      for (int n = 0; n < N; ++n) {
-        const int slot = n % kPreMeta;
-        const bool alive =
-            wait_bar(meta_empty(slot), ((uint32_t)(n / kPreMeta) & 1u) ^ 1u, abort_flag, &s_err_kvb);
-        if (!__all_sync(0xffffffffu, alive)) break;
-        const int j = j0 + n * kPreTile + 16 * lane;
-        bool hole = false;
-        if (lane < 8) {
-          const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
-          hole = j < j1 && page < 0;
-          float ks = 1.f, vs = 1.f;
-          uint32_t group = 0xffffffffu;
-          if (page >= 0) {
-            const size_t cell = (size_t)page * V.Hkv + h;
-            group = (uint32_t)(((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) >> 4);
-            ks = V.ks[cell];
-            vs = fmaxf(V.vs[cell], kScaleFloor);
+      if constexpr (TREE) {
+        publish_pages<D, kPreMeta>(V, b, h, j0, j1, N, base + SH::META, base + SH::HOLES, meta_full(0), meta_empty(0),
+                                   abort_flag, &s_err_kvb);
+      } else {
+        for (int n = 0; n < N; ++n) {
+          const int slot = n % kPreMeta;
+          const bool alive =
+              wait_bar(meta_empty(slot), ((uint32_t)(n / kPreMeta) & 1u) ^ 1u, abort_flag, &s_err_kvb);
+          if (!__all_sync(0xffffffffu, alive)) break;
+          const int j = j0 + n * kPreTile + 16 * lane;
+          bool hole = false;
+          if (lane < 8) {
+            const int page = j < j1 ? page_of(V, V.table, b, V.table_stride, j >> V.t_shift) : -1;
+            hole = j < j1 && page < 0;
+            float ks = 1.f, vs = 1.f;
+            uint32_t group = 0xffffffffu;
+            if (page >= 0) {
+              const size_t cell = (size_t)page * V.Hkv + h;
+              group = (uint32_t)(((cell << V.t_shift) + (j & ((1 << V.t_shift) - 1))) >> 4);
+              ks = V.ks[cell];
+              vs = fmaxf(V.vs[cell], kScaleFloor);
+            }
+            const float lv = __log2f(vs);
+            sts128(base + SH::META + slot * 128 + lane * 16, __float_as_uint(ks), __float_as_uint(lv),
+                   __float_as_uint(ex2(-lv)), group);
           }
-          const float lv = __log2f(vs);
-          sts128(base + SH::META + slot * 128 + lane * 16, __float_as_uint(ks), __float_as_uint(lv),
-                 __float_as_uint(ex2(-lv)), group);
+          const uint32_t holes = __ballot_sync(0xffffffffu, hole);
+          if (lane == 0)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::HOLES + 4 * slot), "r"(holes) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(meta_full(slot));
+          __syncwarp();
         }
-        const uint32_t holes = __ballot_sync(0xffffffffu, hole);
-        if (lane == 0)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + SH::HOLES + 4 * slot), "r"(holes) : "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(meta_full(slot));
-        __syncwarp();
       }
     }
   }
@@ -540,14 +526,14 @@ static tm_status launch(const AttnParams& P, int pairs, cudaStream_t stream) {
 }
 
 template <int FMT, int D>
-static tm_status launch(const AttnParams& P, int pairs, cudaStream_t stream) {
+static tm_status launch_any(const AttnParams& P, int pairs, cudaStream_t stream) {
   return P.tree ? launch<FMT, D, true>(P, pairs, stream) : launch<FMT, D, false>(P, pairs, stream);
 }
 
 tm_status launch_prefill_attn(const AttnParams& P, int format, int D, int pairs, cudaStream_t stream) {
   if (format == TM_KVB_INT8)
-    return D == 64 ? launch<TM_KVB_INT8, 64>(P, pairs, stream) : launch<TM_KVB_INT8, 128>(P, pairs, stream);
-  return D == 64 ? launch<TM_KVB_E4M3, 64>(P, pairs, stream) : launch<TM_KVB_E4M3, 128>(P, pairs, stream);
+    return D == 64 ? launch_any<TM_KVB_INT8, 64>(P, pairs, stream) : launch_any<TM_KVB_INT8, 128>(P, pairs, stream);
+  return D == 64 ? launch_any<TM_KVB_E4M3, 64>(P, pairs, stream) : launch_any<TM_KVB_E4M3, 128>(P, pairs, stream);
 }
 
 }  // namespace kvb
