@@ -1,13 +1,12 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out = Y + scale_a (X A_a^T) B_a^T,  a the adapter of the row's sequence.
 //
-// One launch: a cluster of eight CTAs takes a tile of 16 or 64 rows and the adapters that appear in it.
+// One launch: a cluster of eight CTAs takes rows that use an adapter.
 //   T = X A^T: each CTA a share of K, on mma.m16n8k16;
-//   the eight partial T meet in distributed shared memory: CTA c sums the tile's rows c, c + 8, ... and hands them,
-//     scaled by a power of two into fp16's range, to all eight;
+//   the eight partial T meet in distributed shared memory: CTA c sums rows c, c + 8, ... and hands them, scaled by a
+//     power of two into fp16's range, to all eight;
 //   out: each CTA a share of N.
-// No partial result goes through memory, rows that use another adapter are computed along and not stored, and an
-// adapter is read once per tile that uses it.
+// No partial result goes through memory.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -22,6 +21,7 @@ static __device__ uint32_t s_err_lora;
 
 constexpr int kThreads = 256;
 constexpr int kCluster = 8;
+constexpr int kDevices = 32;  // whose limits are kept
 
 struct Params {
   const __half* X;
@@ -40,17 +40,20 @@ struct Params {
 // NT: groups of 8 ranks.
 template <int NT>
 struct Shape {
-  static constexpr int ROWS = 16;
   static constexpr int KW = 8;             // warps that share K
   static constexpr int RP = 8 * NT;        // ranks, padded
   static constexpr int KS = (NT + 1) / 2;  // k-steps of the second product
-  static constexpr uint32_t PART = 0;      // [KW][ROWS][RP] fp32
-  static constexpr uint32_t SUM = PART + KW * ROWS * RP * 4;  // [ROWS][RP] fp32, this CTA's share of K
-  static constexpr uint32_t FRAG = SUM + ROWS * RP * 4;       // [KS][32] x 16 bytes: T as A fragments
-  static constexpr uint32_t MUL = FRAG + KS * 512;            // [ROWS] fp32
-  static constexpr uint32_t SMEM = MUL + ROWS * 4;
+  static constexpr uint32_t PART = 0;      // [KW][16][RP] fp32
+  static constexpr uint32_t SUM = PART + KW * 16 * RP * 4;  // [16][RP] fp32, this CTA's share of K
+  static constexpr uint32_t FRAG = SUM + 16 * RP * 4;       // [KS][32] x 16 bytes: T as A fragments
+  static constexpr uint32_t MUL = FRAG + KS * 512;            // [16] fp32
+  static constexpr uint32_t SMEM = MUL + 16 * 4;
 };
 
+// Into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ uint4 ldg16(const __half* p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
 }
@@ -105,17 +108,12 @@ __device__ __forceinline__ void find_rows(const Params& P, int row0, Rows<ROWS>&
   __syncthreads();
 }
 
-// Rows without an adapter: columns c0 .. c1 - 1 of Y as they are.
-template <int ROWS>
-__device__ __forceinline__ void copy_rows(const Params& P, int row0, const Rows<ROWS>& s, int c0, int c1) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < ROWS; r += kThreads / 32) {
-    if (s.id[r] != -1) continue;
-    const __half* src = P.Y + (row0 + r) * P.ys;
-    __half* dst = P.out + (row0 + r) * P.os;
-    for (int c = c0 + 8 * lane; c < min(c1, P.N); c += 256)
-      *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-  }
+// A row without an adapter, by one warp: columns c0 .. c1 - 1 of Y as they are.
+__device__ __forceinline__ void copy_row(const Params& P, long long row, int c0, int c1) {
+  const __half* src = P.Y + row * P.ys;
+  __half* dst = P.out + row * P.os;
+  for (int c = c0 + 8 * (int)(threadIdx.x & 31); c < min(c1, P.N); c += 256)
+    *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
 }
 
 // The eight partial T [ROWS][RP] (fp32, at `sum` of each CTA) meet: CTA c takes rows c, c + 8, ..., adds the CTAs'
@@ -172,32 +170,122 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t y, float a, float b, floa
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Tiles of 16 rows: a decode batch.  Operands go from global memory to the products' registers.  The sum over k may go
-// in any order, so that a lane's 16-byte chunk of a row holds the eight k of two products and both operands are read
-// in whole sectors.
+// Decode batches: up to 256 rows a tile, whose rows come together by adapter, 16 at a time (an item of work: an adapter
+// and 16 of its rows), so that an adapter is read once however its rows lie.
+constexpr int kSpan = 256;
+constexpr int kItems = kSpan;  // at most one per row
+constexpr int kSlots = 512;    // of the table of adapters, at most half full
+struct Items {
+  int seq[kSpan];               // as in Rows
+  int key[kSlots], start[kSlots];           // an adapter, its first item
+  uint32_t rows[kThreads / 32][kSlots / 4];  // a byte each: how many rows of a warp use it
+  int sums[kThreads / 32];
+  int total;                    // items
+  int adapter[kItems], size[kItems];
+  uint8_t pick[kItems * 16];    // the rows of each
+};
+// Returns the adapter of the thread's row: -1: none, -2: no sequence.
+__device__ __forceinline__ int find_items(const Params& P, int row0, Items& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int here = min(kSpan, P.rows - row0);
+  s.seq[tid] = P.q_start || tid >= here ? -1 : row0 + tid;
+  for (int i = tid; i < kSlots; i += kThreads) {
+    s.key[i] = -1;
+    for (int w = 0; w < kThreads / 32; w += 4) (&s.rows[0][0])[i * 2 + w / 4] = 0u;
+  }
+  __syncthreads();
+  if (P.q_start) {
+    for (int b = tid; b < P.seqs; b += kThreads) {
+      const int lo = max(min(max(P.q_start[b], 0), P.rows), row0);
+      const int hi = min(min(max(P.q_start[b + 1], 0), P.rows), row0 + here);
+      for (int r = lo; r < hi; ++r) atomicMax(&s.seq[r - row0], b);
+    }
+    __syncthreads();
+  }
+  const int b = s.seq[tid];
+  int a = b >= 0 ? P.ids[b] : -2;
+  if (b >= 0 && (unsigned)a >= (unsigned)P.n) a = -1;
+  // Where an adapter stands in the table goes by who comes first; a row's place among its adapter's rows by their order,
+  // so that all CTAs of a cluster agree.
+  const uint32_t same = __match_any_sync(0xffffffffu, a);
+  auto counts = [&](int w) { return reinterpret_cast<uint8_t*>(s.rows[w]); };
+  int slot = 0, place = 0, rows = 0;
+  if (a >= 0) {
+    for (slot = a % kSlots;; slot = (slot + 1) % kSlots) {
+      const int was = atomicCAS(&s.key[slot], -1, a);
+      if (was == -1 || was == a) break;
+    }
+    place = __popc(same & ((1u << lane) - 1u));
+    if (place == 0) counts(warp)[slot] = (uint8_t)__popc(same);
+  }
+  __syncthreads();
+  if (a >= 0)
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int n = counts(w)[slot];
+      rows += n;
+      if (w < warp) place += n;
+    }
+  const int mine = a >= 0 && place == 0 ? (rows + 15) / 16 : 0;
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) s.sums[warp] = sum;
+  __syncthreads();
+  int before = sum - mine;
+  for (int w = 0; w < warp; ++w) before += s.sums[w];
+  if (mine) s.start[slot] = before;
+  for (int j = 0; j < mine; ++j) {
+    s.adapter[before + j] = a;
+    s.size[before + j] = min(16, rows - 16 * j);
+  }
+  if (tid == kThreads - 1) s.total = before + mine;
+  __syncthreads();
+  if (a >= 0) s.pick[16 * (s.start[slot] + place / 16) + place % 16] = (uint8_t)tid;
+  __syncthreads();
+  return a;
+}
+
+// Operands go from global memory to the products' registers.  The sum over k may go in any order, so that a lane's 16-byte
+// chunk of a row holds the eight k of two products and both operands are read in whole sectors.
 template <int NT>
 __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Params P) {
   using SH = Shape<NT>;
-  constexpr int ROWS = SH::ROWS, RP = SH::RP, KS = SH::KS, KW = SH::KW;
+  constexpr int RP = SH::RP, KS = SH::KS, KW = SH::KW;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Rows<ROWS> rows;
+  __shared__ Items items;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   const int rank = (int)cluster_ctarank();
   const int cl = blockIdx.x / kCluster;
   const int tile = cl / P.splits, split = cl - tile * P.splits;
-  const int row0 = tile * ROWS;
+  const int row0 = tile * kSpan;
   const uint32_t base = smem_u32(smem);
-  find_rows(P, row0, rows);
-  const int count = rows.count;
+  const int own = find_items(P, row0, items);
+  const int count = items.total;
 
   // This CTA's columns, in blocks of 32.
   const int blocks = (P.N + 31) / 32, parts = kCluster * P.splits, part = split * kCluster + rank;
   const int n0 = (int)((long long)blocks * part / parts), n1 = (int)((long long)blocks * (part + 1) / parts);
-  if (blockIdx.y == 0 && P.out != P.Y) copy_rows(P, row0, rows, 32 * n0, 32 * n1);
+  if (P.out != P.Y)  // rows without an adapter, shared out over the tile's clusters
+    for (uint32_t left = __ballot_sync(0xffffffffu, own == -1 && tid % gridDim.y == blockIdx.y); left; left &= left - 1)
+      copy_row(P, row0 + 32 * warp + __ffs(left) - 1, 32 * n0, 32 * n1);
 
   for (int z = blockIdx.y; z < count; z += gridDim.y) {
-    const int a = rows.list[z];
-    const bool lo_ok = rows.id[gr] == a, hi_ok = rows.id[gr + 8] == a;
+    const int a = items.adapter[z], size = items.size[z];
+    const bool lo_ok = gr < size, hi_ok = gr + 8 < size;
+    const long long r_lo = row0 + (lo_ok ? items.pick[16 * z + gr] : 0), r_hi = row0 + (hi_ok ? items.pick[16 * z + gr + 8] : 0);
+    // Its columns of B, one run of memory, on their way to L2 while T is computed; and the next item's A, a share
+    // of it by each CTA.
+    if (tid == 0 && n1 > n0)
+      prefetch_l2(P.B + ((size_t)a * P.N + 32 * n0) * P.R, (uint32_t)(min(32 * n1, P.N) - 32 * n0) * P.R * 2);
+    if (tid == 32 && z + (int)gridDim.y < count) {
+      const long long units = (long long)P.R * P.K / 8, u0 = units * rank / kCluster, u1 = units * (rank + 1) / kCluster;
+      if (u1 > u0)
+        prefetch_l2(P.A + (size_t)items.adapter[z + gridDim.y] * P.R * P.K + 8 * u0, (uint32_t)(u1 - u0) * 16);
+    }
     // ---- T: this warp's chunks of 32 k
     {
       float acc[NT][4];
@@ -205,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-      const __half* xl = P.X + (row0 + gr) * P.xs + 8 * t;
-      const __half* xh = xl + 8 * P.xs;
+      const __half* xl = P.X + r_lo * P.xs + 8 * t;
+      const __half* xh = P.X + r_hi * P.xs + 8 * t;
       const __half* pa = P.A + ((size_t)a * P.R + gr) * P.K + 8 * t;
       const int chunks = (P.K + 31) / 32, stride = kCluster * KW;
       constexpr int AHEAD = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // chunks whose loads are in flight
@@ -234,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
           fetch(ch + (q + AHEAD) * stride, q);
         }
       }
-      float* dst = reinterpret_cast<float*>(smem + SH::PART) + (warp * ROWS + gr) * RP + 2 * t;
+      float* dst = reinterpret_cast<float*>(smem + SH::PART) + (warp * 16 + gr) * RP + 2 * t;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(acc[i][0], acc[i][1]);
@@ -245,15 +333,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
     {
       const float* src = reinterpret_cast<const float*>(smem + SH::PART);
       float* dst = reinterpret_cast<float*>(smem + SH::SUM);
-      for (int i = tid; i < ROWS * RP; i += kThreads) {
+      for (int i = tid; i < 16 * RP; i += kThreads) {
         float v = src[i];
 #pragma unroll
-        for (int k = 1; k < KW; ++k) v += src[k * ROWS * RP + i];
+        for (int k = 1; k < KW; ++k) v += src[k * 16 * RP + i];
         dst[i] = v;
       }
     }
     // a lane holds ranks 4 x .. 4 x + 3 of a k-step, as it reads B
-    exchange<ROWS, RP, KS>(P, a, rank, base + SH::SUM, base + SH::FRAG, base + SH::MUL, [](int c, int& x, int& word) {
+    exchange<16, RP, KS>(P, a, rank, base + SH::SUM, base + SH::FRAG, base + SH::MUL, [](int c, int& x, int& word) {
       x = c >> 2;
       word = 2 * ((c >> 1) & 1);
     });
@@ -272,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
       const int c0 = 32 * nb + 8 * t;
       const bool in = c0 < P.N;
       uint4 y[2] = {};
-      if (lo_ok && in) y[0] = *reinterpret_cast<const uint4*>(P.Y + (row0 + gr) * P.ys + c0);
-      if (hi_ok && in) y[1] = *reinterpret_cast<const uint4*>(P.Y + (row0 + gr + 8) * P.ys + c0);
+      if (lo_ok && in) y[0] = *reinterpret_cast<const uint4*>(P.Y + r_lo * P.ys + c0);
+      if (hi_ok && in) y[1] = *reinterpret_cast<const uint4*>(P.Y + r_hi * P.ys + c0);
       float acc[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -294,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = add_half2(yw[i], acc[i][2 * half], acc[i][2 * half + 1], f);
         if ((half ? hi_ok : lo_ok) && in)
-          *reinterpret_cast<uint4*>(P.out + (row0 + gr + 8 * half) * P.os + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(P.out + (half ? r_hi : r_lo) * P.os + c0) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -357,7 +445,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 32 ? 3 : RP == 64 ? 2 : 1)
   const int n0 = (int)((long long)blocks * part / parts), cols = (int)((long long)blocks * (part + 1) / parts) - n0;
   const int first = cols > 0 ? (int)((tile * 2654435761u >> 8) % (unsigned)cols) : 0;
   auto column = [&](int i) { return 64 * (n0 + (i + first < cols ? i + first : i + first - cols)); };
-  if (blockIdx.y == 0 && P.out != P.Y) copy_rows(P, row0, rows, 64 * n0, 64 * (n0 + cols));
+  if (blockIdx.y == 0 && P.out != P.Y)
+    for (int r = warp; r < ROWS; r += kThreads / 32)
+      if (rows.id[r] == -1) copy_row(P, row0 + r, 64 * n0, 64 * (n0 + cols));
 
   // Lines of 128 bytes, 16-byte chunk c of line r at c ^ (r % 8), as the copies lay them: what a warp reads at once (eight
   // lines, one chunk) covers all banks.
@@ -515,29 +605,56 @@ __global__ void __launch_bounds__(kThreads, RP <= 32 ? 3 : RP == 64 ? 2 : 1)
   }
 }
 
+static void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int smem, cudaStream_t s) {
+  *cfg = {};
+  cfg->blockDim = dim3(kThreads, 1, 1);
+  cfg->dynamicSmemBytes = (size_t)smem;
+  cfg->stream = s;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = kCluster;
+  at->val.clusterDim.y = 1;
+  at->val.clusterDim.z = 1;
+  cfg->attrs = at;
+  cfg->numAttrs = 1;
+}
+
+// A launch of `tiles` x `splits` x `slots` clusters.  Slots: adapters of a tile (or adapters and 16 of their rows) side by
+// side, as many as there may be but no more clusters than start at once, which the driver knows (GPCs are no
+// multiple of a cluster): a second wave costs as much as the first.  Splits: clusters that share a tile's columns
+// where it leaves SMs idle; each reads the rows and A again, so no more than make B's part the smaller.
 template <typename Kernel, typename... Args>
-static tm_status launch(Kernel kernel, int smem, dim3 grid, std::atomic<unsigned long long>& done, cudaStream_t s,
-                        const Args&... args) {
+static tm_status launch(Kernel kernel, int smem, long long tiles, long long slots, std::atomic<unsigned long long>& done,
+                        std::atomic<int>* room_at, Params P, cudaStream_t s, const Args&... args) {
   if (!smem_attr_once(done, reinterpret_cast<const void*>(kernel), smem)) return TM_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute at;
+  configure(&cfg, &at, smem, s);
+  const int device = current_device();
+  std::atomic<int>* cached = device >= 0 && device < kDevices ? room_at + device : nullptr;
+  int room = cached ? cached->load(std::memory_order_relaxed) : 0;
+  if (room <= 0) {
+    cfg.gridDim = dim3(kCluster, 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&room, kernel, &cfg) != cudaSuccess || room < 1) return TM_ERR_CUDA;
+    if (cached) cached->store(room, std::memory_order_relaxed);
+  }
+  if (slots * tiles > room) slots = room / tiles;
+  if (slots < 1) slots = 1;
+  long long splits = room / 2 / (tiles * slots);
+  const long long blocks = (P.N + 32 * kCluster - 1) / (32 * kCluster);
+  if (splits > blocks) splits = blocks;
+  if (splits > 1 + P.N / P.K) splits = 1 + P.N / P.K;
+  if (splits < 1) splits = 1;
+  if (tiles * splits * kCluster > 0x7fffffffll) return TM_ERR_UNSUPPORTED;
+  P.splits = (int)splits;
+  cfg.gridDim = dim3((unsigned)(tiles * splits * kCluster), (unsigned)slots, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, args..., P) == cudaSuccess ? TM_OK : TM_ERR_CUDA;
 }
 
 template <int NT>
-static tm_status launch_add(const Params& P, dim3 grid, cudaStream_t s) {
+static tm_status launch_add(const Params& P, long long tiles, long long slots, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch(add_kernel<NT>, Shape<NT>::SMEM, grid, done, s, P);
+  static std::atomic<int> room[kDevices];
+  return launch(add_kernel<NT>, Shape<NT>::SMEM, tiles, slots, done, room, P, s);
 }
 
 // fp16 [d2][d1][d0], rows `stride` elements apart; boxes of b1 rows x b0 elements (of at most 128 bytes, swizzled over them).
@@ -558,22 +675,23 @@ static bool tensor_map(CUtensorMap* map, const void* p, long long d0, long long 
 }
 
 template <int RP>
-static tm_status launch_wide(const Params& P, dim3 grid, cudaStream_t s) {
+static tm_status launch_wide(const Params& P, long long tiles, long long slots, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
+  static std::atomic<int> room[kDevices];
   Maps M;
   if (!tensor_map(&M.x, P.X, P.K, P.rows, 0, P.xs, 64, 64) || !tensor_map(&M.a, P.A, P.K, P.R, P.n, P.K, 64, RP) ||
       !tensor_map(&M.y, P.Y, P.N, P.rows, 0, P.ys, 64, 64) ||
       !tensor_map(&M.b, P.B, P.R, P.N, P.n, P.R, RP < 64 ? RP : 64, 64))
     return TM_ERR_CUDA;
-  return launch(add_wide_kernel<RP>, Wide<RP>::SMEM, grid, done, s, M, P);
+  return launch(add_wide_kernel<RP>, Wide<RP>::SMEM, tiles, slots, done, room, P, s, M);
 }
 
-static tm_status launch(const Params& P, bool wide, dim3 grid, cudaStream_t s) {
-  if (P.R <= 8 && !wide) return launch_add<1>(P, grid, s);
-  if (P.R <= 16) return wide ? launch_wide<16>(P, grid, s) : launch_add<2>(P, grid, s);
-  if (P.R <= 32) return wide ? launch_wide<32>(P, grid, s) : launch_add<4>(P, grid, s);
-  if (P.R <= 64) return wide ? launch_wide<64>(P, grid, s) : launch_add<8>(P, grid, s);
-  return wide ? launch_wide<128>(P, grid, s) : launch_add<16>(P, grid, s);
+static tm_status launch(const Params& P, bool wide, long long tiles, long long slots, cudaStream_t s) {
+  if (P.R <= 8 && !wide) return launch_add<1>(P, tiles, slots, s);
+  if (P.R <= 16) return wide ? launch_wide<16>(P, tiles, slots, s) : launch_add<2>(P, tiles, slots, s);
+  if (P.R <= 32) return wide ? launch_wide<32>(P, tiles, slots, s) : launch_add<4>(P, tiles, slots, s);
+  if (P.R <= 64) return wide ? launch_wide<64>(P, tiles, slots, s) : launch_add<8>(P, tiles, slots, s);
+  return wide ? launch_wide<128>(P, tiles, slots, s) : launch_add<16>(P, tiles, slots, s);
 }
 
 }  // namespace lora
@@ -614,27 +732,15 @@ extern "C" tm_status tm_lora_add(const tm_lora_adapters* ad, const void* X, long
   lora::Params P = {static_cast<const __half*>(X), static_cast<const __half*>(Y), static_cast<__half*>(out), x_stride,
                     y_stride, out_stride, static_cast<const __half*>(ad->A), static_cast<const __half*>(ad->B), ad->scale,
                     ids, q_start, (int)rows, B, ad->n, ad->K, ad->N, ad->R, 1};
-  // Rows come in runs of one adapter where sequences are long: tiles of 64 then read an adapter a quarter as often.
+  // Rows come in runs of one adapter where sequences are long.
   const bool wide = rows >= 16ll * B && ad->n > 0;
-  const int tile = wide ? 64 : 16;
-  const long long tiles = (rows + tile - 1) / tile;
-  const long long room = 2ll * num_sms(current_device()) / lora::kCluster;  // clusters that start at once
-  long long slots = ad->n < tile ? ad->n : tile;                            // adapters of a tile side by side
-  if (slots > rows) slots = rows;
+  const int tile = wide ? 64 : lora::kSpan;
+  const long long in_tile = rows < tile ? rows : tile;
+  long long slots = ad->n < in_tile ? ad->n : in_tile;
   if (slots > B) slots = B;
-  if (slots * tiles > room) slots = room / tiles;
-  if (slots < 1) slots = 1;
-  // Clusters that share a tile's columns: each reads the rows and A again, so no more than make B's part the smaller.
-  long long splits = room / 2 / (tiles * slots);
-  const long long blocks = (ad->N + 32 * lora::kCluster - 1) / (32 * lora::kCluster);
-  if (splits > blocks) splits = blocks;
-  if (splits > 1 + ad->N / ad->K) splits = 1 + ad->N / ad->K;
-  if (splits < 1) splits = 1;
-  P.splits = (int)splits;
-  if (tiles * splits * lora::kCluster > 0x7fffffffll) return TM_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(tiles * splits * lora::kCluster), (unsigned)slots, 1);
+  if (!wide) slots += in_tile / 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const tm_status st = lora::launch(P, wide, grid, s);
+  const tm_status st = lora::launch(P, wide, (rows + tile - 1) / tile, slots, s);
   if (st == TM_OK) set_launch_count(1);
   return st;
 }
