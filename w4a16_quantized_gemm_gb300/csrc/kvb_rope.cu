@@ -5,9 +5,8 @@
 // in binary32, each product and each sum rounded (no fused multiply-add: the codes are then the same wherever they
 // are computed).  Rotated keys are quantised from binary32, not from a 16-bit copy.
 //
-// One CTA per (page that new tokens fall into, KV head, role): role 0 takes the keys and the query heads of the
-// group, so that a cosine and a sine, once in registers, serve 1 + Hq / Hkv heads; role 1 the values, as in the
-// append without rotation.  A thread works on units of 16 dimensions: two vectors of 8 that hold both halves of their
+// One CTA per (page that new tokens fall into, KV head, role): keys, values as in the append without rotation, and the
+// query heads of the group.  A thread works on units of 16 dimensions: two vectors of 8 that hold both halves of their
 // pairs.  The rotated keys stay in registers (at most 64 a thread) across the maximum and the rounding.
 #include "kvb_append.cuh"
 
@@ -23,6 +22,7 @@ struct RopeParams {
   const float* table;
   const int* pos;
   int positions, dims;
+  int roles;  // CTAs of a page and KV head: keys, values, and queries where there are any
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, bool bf16, float* y) {
@@ -75,21 +75,75 @@ __device__ __forceinline__ uint32_t codes_of(const float* y, const Divisor& by) 
 
 // UNITS: units of 16 dimensions per thread, enough for the new tokens of one page and head.
 template <int FMT, bool BF16, int UNITS, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const RopeParams R) {
+__global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rope_kernel(const RopeParams R) {
   __shared__ uint32_t warp_max[kAppendThreads / 32];
   const AppendParams& P = R.A;
   const View& V = P.V;
-  const int b = blockIdx.z, h = blockIdx.y, role = blockIdx.x & 1, tid = threadIdx.x;
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int nth = (int)(blockIdx.x / R.roles), role = (int)blockIdx.x - nth * R.roles;
   const Span s = span(V, b);
   const int T = 1 << V.t_shift;
   // Pages by slot; queries of rows without one (more rows than tokens: negative slots) are rotated all the same.
-  const int blk = (s.old >> V.t_shift) + (int)(blockIdx.x >> 1);
+  const int blk = (s.old >> V.t_shift) + nth;
   const int begin = blk * T;
   const int lo = max(s.old, begin), hi = min(s.old + s.n, begin + T);
   if (lo >= hi) return;
+  const int D = 1 << P.d_shift, unit_shift = P.d_shift - 4;
+  const int total = (hi - lo) << unit_shift;
+  const int turning = R.dims >> 4;  // units of a token that rotate
+  // The first element of a unit's two vectors.
+  auto places = [&](int p, int& d0, int& d1) {
+    const bool halves = !INTER && p < turning;
+    d0 = halves ? 8 * p : 16 * p;
+    d1 = halves ? 8 * p + (R.dims >> 1) : 16 * p + 8;
+  };
+  auto angles = [&](long long row, int t, int p, float* c, float* sn) {
+    const int at = min(max(R.pos ? R.pos[row] : t, 0), R.positions - 1);
+    const float* cs = R.table + (size_t)at * R.dims + 8 * p;
+    load8(cs, c);
+    load8(cs + (R.dims >> 1), sn);
+  };
+
+  if (role == 2) {  // ---- queries: four heads of the group, so that angles serve them together
+    const int fours = (R.G + 3) >> 2;
+    for (int i = tid; i < total * fours; i += kAppendThreads) {
+      const int u = i / fours, g0 = 4 * (i - u * fours);
+      const int t = lo + (u >> unit_shift), p = u & ((1 << unit_shift) - 1);
+      const long long row = s.row0 + (long long)(t - s.old);
+      int d0, d1;
+      places(p, d0, d1);
+      const uint16_t* src = R.Q + row * R.q_stride + (long long)(h * R.G + g0) * D;
+      uint16_t* dst = R.q_out + row * R.qo_stride + (long long)(h * R.G + g0) * D;
+      uint4 a[4], z[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g0 + g < R.G) {
+          a[g] = *reinterpret_cast<const uint4*>(src + g * D + d0);
+          z[g] = *reinterpret_cast<const uint4*>(src + g * D + d1);
+        }
+      float c[8], sn[8];
+      if (p < turning) angles(row, t, p, c, sn);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g0 + g < R.G) {
+          if (p < turning) {
+            float q[16];
+            unpack8(a[g], BF16, q);
+            unpack8(z[g], BF16, q + 8);
+            turn16<INTER>(q, c, sn);
+            a[g] = pack8(q, BF16);
+            z[g] = pack8(q + 8, BF16);
+          }
+          *reinterpret_cast<uint4*>(dst + g * D + d0) = a[g];
+          *reinterpret_cast<uint4*>(dst + g * D + d1) = z[g];
+        }
+    }
+    return;
+  }
+
   const bool slots = blk >= 0 && blk < V.table_stride;
   const int page = slots ? page_of(V, V.table, b, V.table_stride, blk) : -1;
-  if (role == 1) {
+  if (role == 1) {  // ---- values
     if (P.w && slots)
       for (int t = lo + tid; t < hi && t < P.w_stride; t += kAppendThreads)
         P.w[((size_t)b * V.Hkv + h) * P.w_stride + t] = 0.f;
@@ -98,20 +152,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const RopeP
     return;
   }
 
-  const int D = 1 << P.d_shift, unit_shift = P.d_shift - 4;
-  const int total = (hi - lo) << unit_shift;
-  const int turning = R.dims >> 4;  // units of a token that rotate
+  // ---- keys
+  if (page < 0) return;  // a hole takes none
   const float top = BF16 ? 3.3895313892515355e38f : 65504.f;
   const uint16_t* keys = P.x[0] + (long long)h * D;
-  // The first element of a unit's two vectors.
-  auto places = [&](int p, int& d0, int& d1) {
-    const bool halves = !INTER && p < turning;
-    d0 = halves ? 8 * p : 16 * p;
-    d1 = halves ? 8 * p + (R.dims >> 1) : 16 * p + 8;
-  };
   float y[UNITS][16];
   // The rotated keys; clean: NaN and infinities replaced before and after.
-  auto fetch = [&](int i, auto clean, auto&& with_angles) {
+  auto fetch = [&](int i, auto clean) {
     const int u = tid + i * kAppendThreads;
 #pragma unroll
     for (int e = 0; e < 16; ++e) y[i][e] = 0.f;
@@ -120,64 +167,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const RopeP
     const long long row = s.row0 + (long long)(t - s.old);
     int d0, d1;
     places(p, d0, d1);
-    if (page >= 0) {
-      const uint16_t* src = keys + row * P.stride[0];
-      const uint4 a = *reinterpret_cast<const uint4*>(src + d0), c = *reinterpret_cast<const uint4*>(src + d1);
-      unpack8(a, BF16, y[i]);
-      unpack8(c, BF16, y[i] + 8);
-    }
+    const uint16_t* src = keys + row * P.stride[0];
+    const uint4 a = *reinterpret_cast<const uint4*>(src + d0), z = *reinterpret_cast<const uint4*>(src + d1);
+    unpack8(a, BF16, y[i]);
+    unpack8(z, BF16, y[i] + 8);
     if (decltype(clean)::value)
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[i][e] = finite(y[i][e], top);
-    float c[8], sn[8];
     if (p < turning) {
-      const int at = min(max(R.pos ? R.pos[row] : t, 0), R.positions - 1);
-      const float* cs = R.table + (size_t)at * R.dims + 8 * p;
-      load8(cs, c);
-      load8(cs + (R.dims >> 1), sn);
+      float c[8], sn[8];
+      angles(row, t, p, c, sn);
       turn16<INTER>(y[i], c, sn);
     }
     if (decltype(clean)::value)
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[i][e] = finite(y[i][e], 3.40282347e38f);
-    with_angles(row, p, d0, d1, c, sn);
   };
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
-    fetch(i, std::false_type{}, [&](long long row, int p, int d0, int d1, const float* c, const float* sn) {
-      // the same dimensions of the group's query heads
-      if (!R.Q) return;
-      const uint16_t* src = R.Q + row * R.q_stride + (long long)h * R.G * D;
-      uint16_t* dst = R.q_out + row * R.qo_stride + (long long)h * R.G * D;
-      for (int g0 = 0; g0 < R.G; g0 += 4) {
-        uint4 a[4], z[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (g0 + g < R.G) {
-            a[g] = *reinterpret_cast<const uint4*>(src + (g0 + g) * D + d0);
-            z[g] = *reinterpret_cast<const uint4*>(src + (g0 + g) * D + d1);
-          }
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (g0 + g < R.G) {
-            if (p < turning) {
-              float q[16];
-              unpack8(a[g], BF16, q);
-              unpack8(z[g], BF16, q + 8);
-              turn16<INTER>(q, c, sn);
-              a[g] = pack8(q, BF16);
-              z[g] = pack8(q + 8, BF16);
-            }
-            *reinterpret_cast<uint4*>(dst + (g0 + g) * D + d0) = a[g];
-            *reinterpret_cast<uint4*>(dst + (g0 + g) * D + d1) = z[g];
-          }
-      }
-    });
+    fetch(i, std::false_type{});
 #pragma unroll
     for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(y[i][e]) & 0x7fffffffu);
   }
-  if (page < 0) return;  // uniform: a hole takes no keys
   auto join = [&](uint32_t v) {  // over the CTA
     v = __reduce_max_sync(0xffffffffu, v);
     __syncthreads();
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const RopeP
     m = 0u;
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-      fetch(i, std::true_type{}, [](long long, int, int, int, const float*, const float*) {});
+      fetch(i, std::true_type{});
 #pragma unroll
       for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(y[i][e]) & 0x7fffffffu);
     }
@@ -290,7 +302,8 @@ extern "C" tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_
   P.pos = rope->pos;
   P.positions = rope->positions;
   P.dims = rope->dims;
-  const dim3 grid((unsigned)(2 * append_pages(V)), (unsigned)V.Hkv, (unsigned)V.B);
+  P.roles = Q ? 3 : 2;
+  const dim3 grid((unsigned)(P.roles * append_pages(V)), (unsigned)V.Hkv, (unsigned)V.B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int units = ((cache->T < V.max_q ? cache->T : V.max_q) * D / 16 + kAppendThreads - 1) / kAppendThreads;
   const bool bf16 = dtype == TM_KVB_BF16, inter = rope->interleaved != 0;
