@@ -90,17 +90,23 @@ def test_infinities_stay_in_their_rows():
     assert torch.equal(got[~bad], clean[~bad])
 
 
-def test_claims_that_overlap_and_run_out_of_range():
-    """Row starts that are no partition: nothing outside is touched, a row that several claim takes the last one's."""
-    p = Problem("lora/claims", [1] * 40, 64, 64, 16, 3, [0] * 40)
+@pytest.mark.parametrize("rows", [40, 400])
+def test_claims_that_overlap_and_run_out_of_range(rows):
+    """Row starts that are no partition (few rows a sequence, and many): nothing outside is touched, a row that several
+    claim takes the last one's."""
+    p = Problem(f"lora/claims/{rows}", [1] * rows, 64, 64, 16, 3, [0] * rows)
     ad = binding.Adapters(p.A.cuda(), p.B.cuda())
     X, Y = p.X[:, 8:].cuda(), p.Y[:, :64].contiguous().cuda()
+    u = rows // 4
     out = binding.lora_add(Y, X, ad, device(np.array([0, 1, 2, 1], np.int32)),
-                           q_start=device(np.array([-5, 20, 10, 30, 10 ** 9], np.int32)), out=torch.full_like(Y, 7.0))
-    whole = [binding.lora_add(Y, X, ad, torch.full((40,), a, dtype=torch.int32, device="cuda"), out=torch.empty_like(Y))
+                           q_start=device(np.array([-5, 2 * u, u, 3 * u, 10 ** 9], np.int32)),
+                           out=torch.full_like(Y, 7.0))
+    whole = [binding.lora_add(Y, X, ad, torch.full((4,), a, dtype=torch.int32, device="cuda"),
+                              q_start=device(np.arange(0, rows + 1, u).astype(np.int32)), out=torch.empty_like(Y))
              for a in range(3)]
-    # sequence 0: rows 0 .. 19; 1: none; 2: 10 .. 29; 3: 30 .. 39
-    assert torch.equal(out[:10], whole[0][:10]) and torch.equal(out[10:30], whole[2][10:30]) and torch.equal(out[30:], whole[1][30:])
+    # sequence 0: rows 0 .. 2 u - 1; 1: none; 2: u .. 3 u - 1; 3: 3 u ..
+    assert torch.equal(out[:u], whole[0][:u]) and torch.equal(out[u:3 * u], whole[2][u:3 * u])
+    assert torch.equal(out[3 * u:], whole[1][3 * u:])
 
 
 def test_no_adapters_at_all():

