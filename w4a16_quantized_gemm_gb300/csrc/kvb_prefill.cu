@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
     const bool ok = row < rows;
     const int qi = ok ? row / P.G : 0;
     const size_t hr = (size_t)(s.row0 + qi) * P.Hq + h * P.G + (ok ? row - qi * P.G : 0);
-    const int last = ok ? (TREE ? s.len - 1 : min(s.old + qi, s.len - 1)) : -1;  // last visible token
+    const int last = TREE ? s.len - 1 : ok ? min(s.old + qi, s.len - 1) : -1;  // last visible token
+    const bool busy = !TREE || __any_sync(0xffffffffu, ok);  // else the warp's rows are no one's: it keeps the tiles going
     [[maybe_unused]] const uint32_t* mask = TREE ? P.tree + (s.row0 + qi) * P.tree_stride : nullptr;
     float mul = fabsf(P.scale_log2);
     if (i < M) {
@@ -258,6 +259,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           alive = false;
           break;
         }
+        if (TREE && !busy) {
+          if (lane == 0) {
+            mbar_arrive(p_full(i, 0));
+            mbar_arrive(p_full(i, 1));
+            mbar_arrive(meta_empty(slot));
+          }
+          continue;
+        }
         tc_fence_after();
         const uint32_t meta = base + SH::META + slot * 128;
         uint32_t v[4][32];
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           // Tiles with new tokens, the end or holes.  A bit a column: what these loops hold has to stay in the
           // instruction cache (with comparisons a column, tiles without any of this took half as long again).
           const int fresh = j0 + n * kPreTile - s.old;
-          if (fresh + kPreTile > 0 || !__all_sync(0xffffffffu, rel >= kPreTile - 1) || holes) {
+          if (fresh + kPreTile > 0 || rel < kPreTile - 1 || holes) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t see = tree_columns(P, mask, fresh, rel, holes, c);
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
           a = max3(a, a2, fmaxf(val(14), val(15)));
           tm = fmaxf(tm, fmaf(a, fmaxf(mt.x * mul, 1e-35f), mt.y));
         }
-        if (__any_sync(0xffffffffu, tm > m + kPreSlack)) {
+        if (__any_sync(0xffffffffu, (!TREE || ok) && tm > m + kPreSlack)) {
           const float mn = fmaxf(m, tm), f = ex2(m - mn);
           m = mn;
           l *= f;

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
     const bool ok = r < rows;
     const int qi = ok ? r / P.G : 0;
     const size_t hr = (size_t)(s.row0 + qi) * P.Hq + h * P.G + (ok ? r - qi * P.G : 0);
-    const int last = ok ? s.len - 1 : -1;
+    const bool busy = __any_sync(0xffffffffu, ok);  // else the warp's rows are no one's: it keeps the tiles going
     const uint32_t* mask = P.tree + (s.row0 + qi) * P.tree_stride;
     float mul = fabsf(P.scale_log2);
     {
@@ -160,12 +160,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
         alive = false;
         break;
       }
+      if (!busy) {
+        if (lane == 0) {
+          mbar_arrive(p_full(i, 0));
+          mbar_arrive(p_full(i, 1));
+          mbar_arrive(meta_empty(slot));
+        }
+        continue;
+      }
       tc_fence_after();
       const uint32_t meta = base + SH::META + slot * 128;
-      const int rel = last - (j0 + n * kTreeTile);     // columns 0 .. rel are there
+      const int rel = s.len - 1 - (j0 + n * kTreeTile);  // columns 0 .. rel are there
       const int fresh = j0 + n * kTreeTile - s.old;    // the tile's first token, counted in new ones
       const uint32_t holes = lds32(base + SH::HOLES + 4 * slot);
-      const bool part = fresh + kTreeTile > 0 || !__all_sync(0xffffffffu, rel >= kTreeTile - 1) || holes;
+      const bool part = fresh + kTreeTile > 0 || rel < kTreeTile - 1 || holes;
       // Half a tile's scores at a time, once for the maximum and once for the weights (all of them would take
       // the registers of two warps), in loops that stay in the instruction cache.
       uint32_t v[2][32];
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
           tm = fmaxf(tm, fmaf(a, fmaxf(mt.x * mul, 1e-35f), mt.y));
         }
       }
-      if (__any_sync(0xffffffffu, tm > m + kTreeSlack)) {
+      if (__any_sync(0xffffffffu, ok && tm > m + kTreeSlack)) {
         const float mn = fmaxf(m, tm), f = ex2(m - mn);
         m = mn;
         l *= f;
