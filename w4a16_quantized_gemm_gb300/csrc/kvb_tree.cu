@@ -22,7 +22,7 @@ namespace kvb {
 
 static __device__ uint32_t s_err_kvbt;
 
-constexpr int kTreeThreads = 576;
+constexpr int kTreeThreads = 640;  // the last two warps lend their registers
 constexpr int kTreeTile = 128;  // tokens per tile, rows
 constexpr int kTreeSlots = 3;   // K tiles in flight, V tiles
 constexpr int kTreeMeta = 4;    // tiles whose scales are in flight
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
 
   if (warp < 8) {
     // ---------------- softmax: one row per thread ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const bool ok = r < rows;
@@ -174,29 +175,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
       const int fresh = j0 + n * kTreeTile - s.old;    // the tile's first token, counted in new ones
       const uint32_t holes = lds32(base + SH::HOLES + 4 * slot);
       const bool part = fresh + kTreeTile > 0 || rel < kTreeTile - 1 || holes;
-      // Half a tile's scores at a time, once for the maximum and once for the weights (all of them would take
-      // the registers of two warps), in loops that stay in the instruction cache.
       uint32_t v[2][32];
-      auto scores = [&](int half) {
-        tc_ld_32x32b_x32(ts + 64 * half, v[0]);
-        tc_ld_32x32b_x32(ts + 64 * half + 32, v[1]);
-        tc_wait_ld_of(v[0]);
-        tc_wait_ld_of(v[1]);
-        if (part)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t see = tree_columns(P, mask, fresh, rel, holes, 2 * half + c);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((see >> k) & 1u)) v[c][k] = 0xff800000u;
-          }
-      };
-      float tm = -INFINITY;
+      // What the row does not see, in tensor memory, in a loop of its own: the tiles without any of this stay in the
+      // instruction cache.
+      if (part) {
 #pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_ld_32x32b_x32(ts + 32 * c, v[0]);
+          const uint32_t see = tree_columns(P, mask, fresh, rel, holes, c);
+          tc_wait_ld_of(v[0]);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((see >> k) & 1u)) v[0][k] = 0xff800000u;
+          tc_st_32x32b_x32(ts + 32 * c, v[0]);
+        }
+        tc_wait_st();
+      }
+      // A quarter of the tile's scores is on its way while the one before is used: 0 .. 3 for the maximum, then 2 and 3,
+      // which are still there, and 0 and 1 again for the weights (all of them would take the registers of two warps).
+      float tm = -INFINITY;
+      tc_ld_32x32b_x32(ts, v[0]);
+#pragma unroll
       for (int half = 0; half < 2; ++half) {
-        scores(half);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          if (g == 0) {
+            tc_wait_ld_of(v[0]);
+            tc_ld_32x32b_x32(ts + 64 * half + 32, v[1]);
+          } else if (g == 2) {
+            tc_wait_ld_of(v[1]);
+            if (half == 0) tc_ld_32x32b_x32(ts + 64, v[0]);
+          }
           const float4 mt = lds_f4(meta + 64 * half + 16 * g);
           auto val = [&](int c) { return __uint_as_float(v[g >> 1][16 * (g & 1) + c]); };
           float a = max3(val(0), val(1), val(2)), a2 = max3(val(3), val(4), val(5));
@@ -225,12 +234,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
           }
         }
       }
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        scores(half);
+#pragma unroll
+      for (int half = 1; half >= 0; --half) {
         uint32_t p[16];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          if (g == 0 && half == 0) {
+            tc_wait_ld_of(v[0]);
+            tc_ld_32x32b_x32(ts + 32, v[1]);
+          } else if (g == 2) {
+            if (half == 1) {
+              tc_ld_32x32b_x32(ts, v[0]);
+            } else {
+              tc_wait_ld_of(v[1]);
+            }
+          }
           const float4 mt = lds_f4(meta + 64 * half + 16 * g);
           const float cg = fmaxf(mt.x * mul, 1e-35f), off = mt.y + kTreeBias - m;
           const uint64_t cg2 = f32x2(cg, cg), off2 = f32x2(off, off);
@@ -245,9 +263,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
           }
           const float2 part_sum = f32x2_get(sum);
           l = fmaf(part_sum.x + part_sum.y, mt.z, l);
-          if (g & 1) tc_st_32x32b_x16(ts + 32 * half + 8 * (g - 1), p);  // over scores that have been read
+          if (g & 1) tc_st_32x32b_x16(ts + 64 * half + 8 * (g - 1), p);  // over this half's scores
         }
-        // The first half goes to the tensor cores while the second is computed.
+        // One half goes to the tensor cores while the other is computed.
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -330,6 +348,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
     tc_fence_before();
   } else if (warp < 16) {
     // ---------------- codes -> fp16 tiles: warps 8-11 the keys', 12-15 the values' ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int kv = (warp - 8) >> 2;
     // A warp's pass takes 4 (D = 64: 8) rows, the next one those 16 (32) rows further on: the same row of another
     // 16-token group, so that of all addresses only the group changes.  Eight lanes write two rows of one
@@ -390,75 +409,81 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
         mbar_arrive(meta_empty(n % kTreeMeta));  // tile n's groups were read when it was fetched
       }
     }
-  } else if (warp == 16) {
-    // ---------------- products ----------------
-    // The whole warp walks the loop, so that descriptors and addresses stay uniform; one lane issues.
-    if (N > 0) {
-      constexpr uint32_t id_s = idesc_f16_f32(128, 128);
-      constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
-      constexpr uint64_t kTileDesc = SH::TILE >> 4, kPanelDesc = SH::PANEL >> 4;
-      const uint64_t dq = smem_desc_sw128(base), dk = smem_desc_sw128(base + SH::K_OFF);
-      const uint64_t dv = smem_desc_mn(base + SH::V_OFF, SH::PANEL);
-      const uint32_t lead = elect_one();
-      const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);  // known to be uniform
-      auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvbt)) != 0;
-      };
-      // Scores of tile n into those of half n % 2, whose weights of tile n - 2 have been used.
-      auto scores = [&](int n) {
-        const int i = n & 1, slot = n % kTreeSlots;
-        if (!wait_all(full(0, slot), (uint32_t)(n / kTreeSlots) & 1u)) return false;
-        tc_fence_after();
-        const uint64_t db = dk + (uint64_t)slot * kTileDesc;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (k >> 2) * kPanelDesc + (k & 3) * 2;
-          mma_ss_if(lead, tm0 + 128 * i, dq + off, db + off, id_s, k > 0);
-        }
-        commit_if(lead, s_full(i));
-        commit_if(lead, empty(0, slot));
-        return true;
-      };
-      bool alive = wait_all(q_full, 0);
-      // scores 0, 1, [output n, scores n + 2] ...
-#pragma unroll 1
-      for (int n = -2; n < N && alive; ++n) {
-        if (n >= 0) {
-          const int i = n & 1, turn = n >> 1, slot = n % kTreeSlots;
-          alive = wait_all(full(1, slot), (uint32_t)(n / kTreeSlots) & 1u);
-          const uint64_t db = dv + (uint64_t)slot * kTileDesc;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            alive = alive && wait_all(p_full(i, half), (uint32_t)turn & 1u);
-            if (!alive) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              mma_ts_if(lead, tm0 + 256 + D * i, tm0 + 128 * i + 8 * k, db + (uint64_t)((k * 16 * 128) >> 4), id_o,
-                        turn > 0 || k > 0);
-          }
-          if (!alive) break;
-          commit_if(lead, empty(1, slot));
-        }
-        if (n + 2 < N) alive = scores(n + 2);
-      }
-      commit_if(lead, o_full);
-      if (lead) {
-        // Nothing is left in flight when tensor memory is freed, on an abort either.
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(o_full, 0)) {
-          if (globaltimer() - t0 > kWaitLimitNs) {
-            atomicOr(&s_err_kvbt, kErrTimeout);
-            break;
-          }
-        }
-      }
-    }
-    __syncwarp();
   } else {
-    // ---------------- pages and scales ----------------
-    publish_pages<D, kTreeMeta>(V, b, h, j0, j1, N, base + SH::META, base + SH::HOLES, meta_full(0), meta_empty(0),
-                                abort_flag, &s_err_kvbt);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 16) {
+      // ---------------- products ----------------
+      // The whole warp walks the loop, so that descriptors and addresses stay uniform; one lane issues.
+      if (N > 0) {
+        constexpr uint32_t id_s = idesc_f16_f32(128, 128);
+        constexpr uint32_t id_o = idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
+        constexpr uint64_t kTileDesc = SH::TILE >> 4, kPanelDesc = SH::PANEL >> 4;
+        const uint64_t dq = smem_desc_sw128(base), dk = smem_desc_sw128(base + SH::K_OFF);
+        const uint64_t dv = smem_desc_mn(base + SH::V_OFF, SH::PANEL);
+        const uint32_t lead = elect_one();
+        const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);  // known to be uniform
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+          return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, &s_err_kvbt)) != 0;
+        };
+        auto keys = [&](int n) { return wait_all(full(0, n % kTreeSlots), (uint32_t)(n / kTreeSlots) & 1u); };
+        // Scores of tile n into those of half n % 2, whose weights of tile n - 2 have been used.
+        auto scores = [&](int n) {
+          const int i = n & 1, slot = n % kTreeSlots;
+          tc_fence_after();
+          const uint64_t db = dk + (uint64_t)slot * kTileDesc;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (k >> 2) * kPanelDesc + (k & 3) * 2;
+            mma_ss_if(lead, tm0 + 128 * i, dq + off, db + off, id_s, k > 0);
+          }
+          commit_if(lead, s_full(i));
+          commit_if(lead, empty(0, slot));
+        };
+        bool alive = wait_all(q_full, 0);
+        // scores 0, 1, [output n, scores n + 2] ...
+#pragma unroll 1
+        for (int n = -2; n < N && alive; ++n) {
+          if (n >= 0) {
+            const int i = n & 1, turn = n >> 1, slot = n % kTreeSlots;
+            alive = wait_all(full(1, slot), (uint32_t)(n / kTreeSlots) & 1u);
+            const uint64_t db = dv + (uint64_t)slot * kTileDesc;
+#pragma unroll
+            for (int half = 1; half >= 0; --half) {
+              alive = alive && wait_all(p_full(i, half), (uint32_t)turn & 1u);
+              // The next keys are looked for here, not between the weights and the scores that wait for their place.
+              if (half == 1 && n + 2 < N) alive = alive && keys(n + 2);
+              if (!alive) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts_if(lead, tm0 + 256 + D * i, tm0 + 128 * i + 64 * half + 8 * k,
+                          db + (uint64_t)(((4 * half + k) * 16 * 128) >> 4), id_o, turn > 0 || half == 0 || k > 0);
+            }
+            if (!alive) break;
+            commit_if(lead, empty(1, slot));
+          } else if (n + 2 < N) {
+            alive = keys(n + 2);
+          }
+          if (n + 2 < N && alive) scores(n + 2);
+        }
+        commit_if(lead, o_full);
+        if (lead) {
+          // Nothing is left in flight when tensor memory is freed, on an abort either.
+          const unsigned long long t0 = globaltimer();
+          while (!mbar_try_wait(o_full, 0)) {
+            if (globaltimer() - t0 > kWaitLimitNs) {
+              atomicOr(&s_err_kvbt, kErrTimeout);
+              break;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 17) {
+      // ---------------- pages and scales ----------------
+      publish_pages<D, kTreeMeta>(V, b, h, j0, j1, N, base + SH::META, base + SH::HOLES, meta_full(0), meta_empty(0),
+                                  abort_flag, &s_err_kvbt);
+    }
   }
   __syncthreads();
   if (warp == 16) {
