@@ -1,5 +1,6 @@
 // Attention of trees of drafts over the paged 8-bit KV cache, up to 128 rows (nodes x query heads of a KV head): on
-// tcgen05 like the kernel for prompts (kvb_prefill.cu, whose mathematics this is), but bound by what brings the codes in.
+// tcgen05 like the kernel for prompts (kvb_prefill.cu, whose mathematics this is), but bound by what brings the codes
+// in.
 //
 // A CTA takes one (sequence, KV head) and a slice of the tokens in tiles of 128, which its two halves take in turn,
 // each with a running softmax and an output of its own; they are joined at the end.  With one row tile every tile of
@@ -40,7 +41,8 @@ struct TreeShape {
   static constexpr uint32_t META = V_OFF + kTreeSlots * TILE;   // [kTreeMeta][8] x {ks, lv, 1 / vs, group}
   static constexpr uint32_t HOLES = META + kTreeMeta * 8 * 16;  // [kTreeMeta] bits of the 16-token groups
   static constexpr uint32_t BARS = HOLES + 16;
-  static constexpr uint32_t SMEM = BARS + 256 + 1024;
+  static constexpr uint32_t DOWN = BARS + 256;       // [128]: what the rows' queries were scaled by, inverted
+  static constexpr uint32_t SMEM = DOWN + 512 + 1024;
 };
 
 template <int FMT, int D>
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 224);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 228);
   if (tid == 0) {
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     mbar_init(o_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
@@ -108,44 +110,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
     const uint32_t* mask = P.tree + (s.row0 + qi) * P.tree_stride;
     float mul = fabsf(P.scale_log2);
     {
-      // The row's queries into shared memory, as fp16; bf16 rows times a power of two.  A negative
-      // scale is taken into their sign.
+      // Queries into shared memory, 16 bytes a thread, a row by neighbouring lanes: as fp16, bf16 rows times a power of
+      // two.  A negative scale is taken into their sign.
+      constexpr int LANES = D / 8, STEP = 256 / LANES, PASSES = kTreeTile / STEP;
       const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;
-      const uint16_t* q = P.Q + (s.row0 + qi) * P.q_stride + (long long)(h * P.G + (ok ? r - qi * P.G : 0)) * D;
-      float up = 1.f;
-      if (P.bf16) {
-        float m = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = ldg_or_zero(q + 8 * c, ok);
-          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+      const int c = tid % LANES, r0 = tid / LANES;
+      uint4 x[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = r0 + p * STEP;
+        const bool have = row < rows;
+        const int q = have ? row / P.G : 0;
+        const int head = h * P.G + (have ? row - q * P.G : 0);
+        x[p] = ldg_or_zero(P.Q + (s.row0 + q) * P.q_stride + (long long)head * D + 8 * c, have);
+      }
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = r0 + p * STEP;
+        uint32_t wd[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+        if (P.bf16) {
+          float2 f[4];
+          float top = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack(wd[k], true);
-            m = max3(m, fabsf(f.x), fabsf(f.y));
+            f[k] = unpack(wd[k], true);
+            top = max3(top, fabsf(f[k].x), fabsf(f[k].y));
           }
-        }
-        const int e2 = max((int)(__float_as_uint(m) >> 23) - 127, -100);
-        up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
-        mul *= __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
-      }
-      if (i == 0) {
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = ldg_or_zero(q + 8 * c, ok);
-          uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-          if (P.bf16)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = unpack(wd[k], true);
-              wd[k] = pack_half2(f.x * up, f.y * up);
-            }
-          sts128(base + (c >> 3) * SH::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4), wd[0] ^ flip, wd[1] ^ flip,
-                 wd[2] ^ flip, wd[3] ^ flip);
+          for (int k = 1; k < LANES; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+          const int e2 = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+          const float up = __uint_as_float((uint32_t)(127 + min(14 - e2, 126)) << 23);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) wd[k] = pack_half2(f[k].x * up, f[k].y * up);
+          if (c == 0)
+            reinterpret_cast<float*>(smem + SH::DOWN)[row] = __uint_as_float((uint32_t)(127 - min(14 - e2, 126)) << 23);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        sts128(base + (c >> 3) * SH::PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), wd[0] ^ flip, wd[1] ^ flip,
+               wd[2] ^ flip, wd[3] ^ flip);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      if (P.bf16) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        mul *= reinterpret_cast<const float*>(smem + SH::DOWN)[r];
       }
     }
 
@@ -191,8 +199,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
         }
         tc_wait_st();
       }
-      // A quarter of the tile's scores is on its way while the one before is used: 0 .. 3 for the maximum, then 2 and 3,
-      // which are still there, and 0 and 1 again for the weights (all of them would take the registers of two warps).
+      // A quarter of the tile's scores is on its way while the one before is used: 0 .. 3 for the maximum, then 2 and
+      // 3, which are still there, and 0 and 1 again for the weights (all of them would take the registers of two warps).
       float tm = -INFINITY;
       tc_ld_32x32b_x32(ts, v[0]);
 #pragma unroll
@@ -278,49 +286,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
       alive = __all_sync(0xffffffffu, alive);
       tc_fence_after();
     }
-    // ---- the second half's state to the first, through the tiles' memory (free: all products are done)
-    float* other = reinterpret_cast<float*>(smem + SH::K_OFF) + r;  // [D + 2][128]
-    float f1 = 1.f, f2 = 0.f;
-    if (i == 1 && alive && N > 1) {
-      other[D * kTreeTile] = m;
-      other[(D + 1) * kTreeTile] = l;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
+    // ---- the halves are joined through the tiles' memory (free: all products are done), each for half the columns
+    constexpr int COLS = D / 2;
+    float* state = reinterpret_cast<float*>(smem + SH::K_OFF) + r;            // [m, l of the first, of the second][128]
+    auto given = [&](int to_half) { return state + (4 + to_half * COLS) * kTreeTile; };  // [COLS][128]
+    auto output = [&](int c, uint32_t (&o)[32]) {
+      if (i < N) {
         tc_ld_32x32b_x32(to + c, o);
         tc_wait_ld_of(o);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) other[(c + k) * kTreeTile] = __uint_as_float(o[k]);
+        for (int k = 0; k < 32; ++k) o[k] = 0u;
+      }
+    };
+    if (alive) {
+      state[2 * i * kTreeTile] = m;
+      state[(2 * i + 1) * kTreeTile] = l;
+#pragma unroll 1
+      for (int c = 0; c < COLS; c += 32) {
+        uint32_t o[32];
+        output((1 - i) * COLS + c, o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) given(1 - i)[(c + k) * kTreeTile] = __uint_as_float(o[k]);
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (i == 0 && N > 1) {
-      const float m2 = other[D * kTreeTile], mn = fmaxf(m, m2);
-      f1 = ex2(m - mn);
-      f2 = ex2(m2 - mn);
-      l = l * f1 + other[(D + 1) * kTreeTile] * f2;
-      m = mn;
-    }
     // ---- the row's output, or its state for the joining launch
-    if (i == 0 && alive) {
-      const float inv = l > 0.f || l != l ? __fdividef(1.f, l) : 0.f;
+    if (alive) {
+      const float m0 = state[0], m1 = state[2 * kTreeTile], top = fmaxf(m0, m1), f0 = ex2(m0 - top), f1 = ex2(m1 - top);
+      const float sum = state[kTreeTile] * f0 + state[3 * kTreeTile] * f1;
+      const float inv = sum > 0.f || sum != sum ? __fdividef(1.f, sum) : 0.f;
+      const float mine = i ? f1 : f0, others = i ? f0 : f1;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < COLS; c += 32) {
         uint32_t o[32];
-        if (N > 0) {
-          tc_ld_32x32b_x32(to + c, o);
-          tc_wait_ld_of(o);
-          if (N > 1)
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              o[k] = __float_as_uint(__uint_as_float(o[k]) * f1 + other[(c + k) * kTreeTile] * f2);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
+        output(i * COLS + c, o);
         if (!ok) continue;
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = __float_as_uint(__uint_as_float(o[k]) * mine + given(i)[(c + k) * kTreeTile] * others);
         if (P.chunks == 1) {
-          uint16_t* out = P.out + hr * D + c;
+          uint16_t* out = P.out + hr * D + i * COLS + c;
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             uint32_t wd[4];
@@ -332,17 +338,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
             *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
           }
         } else {
-          float* dst = P.part + (hr * P.chunks + chunk) * D + c;
+          float* dst = P.part + (hr * P.chunks + chunk) * D + i * COLS + c;
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
             *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
-      if (ok) {
+      if (ok && i == 0) {
         if (P.chunks > 1)
-          P.part_ml[hr * P.chunks + chunk] = make_float2(m - kTreeBias, l);
+          P.part_ml[hr * P.chunks + chunk] = make_float2(top - kTreeBias, sum);
         else if (P.lse)
-          P.lse[hr] = l == 0.f ? -INFINITY : (log2f(l) + m - kTreeBias) * 0.693147180559945f;
+          P.lse[hr] = sum == 0.f ? -INFINITY : (log2f(sum) + top - kTreeBias) * 0.693147180559945f;
       }
     }
     tc_fence_before();
