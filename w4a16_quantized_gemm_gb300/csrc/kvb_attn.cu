@@ -733,8 +733,9 @@ template <int FMT, int D, bool KEEP, bool TREE>
 tm_status launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& P, int rt, int groups,
                       cudaStream_t s) {
   if (rt == 0) return launch_attn<FMT, D, 0, KEEP, TREE>(tmK, tmV, P, groups, s);
-  if (rt == 1) return launch_attn<FMT, D, 1, KEEP, TREE>(tmK, tmV, P, groups, s);
-  return launch_attn<FMT, D, 2, KEEP, TREE>(tmK, tmV, P, groups, s);
+  if constexpr (KEEP || !TREE)  // trees without weights go to tcgen05 from 17 rows on
+    if (rt == 2) return launch_attn<FMT, D, 2, KEEP, TREE>(tmK, tmV, P, groups, s);
+  return launch_attn<FMT, D, 1, KEEP, TREE>(tmK, tmV, P, groups, s);
 }
 
 // A 16-token box of a pool [cells][T][D]; inner rows of D bytes, swizzled over their width.
@@ -767,9 +768,10 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
   const long long sms = num_sms(current_device());
   // 64 rows (16 sequences x 2000 tokens, 8 heads a group): this kernel 51.5 us, with weights 99.6; the tcgen05
   // kernel 47.6, with its second pass for the weights 124.  At 32 rows this one takes 39.
-  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (weights ? kFewRows : kFewRows / 2) ? 2 : -1;
-  // Trees: up to 128 rows have a tcgen05 kernel of their own (16 sequences of 4096 tokens, 8 KV heads: 32 rows 53 us
-  // in the kernel for few rows and 55 in that one, 128 rows 52).
+  // Trees: up to 128 rows have a tcgen05 kernel of their own (16 sequences of 4096 tokens, 8 KV heads: 12 rows 37 us in
+  // the kernel for few rows and 45 in that one, 16 rows 38 and 45, 20 rows 51 and 45, 128 rows 48; one sequence of
+  // 600: 16 rows 9.6 and 11.6, 20 rows 11.8 and 11.6).
+  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (weights ? kFewRows : tree ? 16 : kFewRows / 2) ? 2 : -1;
   const bool narrow = tree && p.rt < 0 && rows <= 128;
   p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : narrow ? 128 : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
