@@ -133,6 +133,31 @@ def test_stream_graph_and_repeats():
     assert torch.equal(out, want)
 
 
+def test_more_rows_and_adapters_than_one_tile_holds():
+    """700 rows of 600 adapters: three tiles, every slot of the table of adapters taken by several."""
+    Problem("lora/spans", [1] * 700, 64, 72, 8, 600, [(b * 512 + b // 7) % 601 for b in range(700)]).check(one_each=True)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, of both kernels: each as it is alone."""
+    p = Problem("lora/two", [1] * 40, 1024, 512, 16, 6, [b % 6 for b in range(40)])
+    q = Problem("lora/two/q", [300, 21], 1024, 512, 16, 6, [1, 4])
+    runs = []
+    for x, one_each in ((p, True), (q, False)):
+        ad = binding.Adapters(x.A.cuda(), x.B.cuda(), device(x.scale))
+        args = (x.Y.cuda()[:, 8:8 + x.N], x.X.cuda()[:, 8:], ad, device(x.ids))
+        starts = None if one_each else device(x.q_start)
+        alone = binding.lora_add(*args, q_start=starts, out=torch.zeros(x.rows, x.N, dtype=torch.float16, device="cuda"))
+        runs.append((args, starts, alone, torch.cuda.Stream(), [torch.zeros_like(alone) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for args, starts, _, stream, outs in runs:
+            binding.lora_add(*args, q_start=starts, out=outs[i], stream=stream)
+    torch.cuda.synchronize()
+    for _, _, alone, _, outs in runs:
+        assert all(torch.equal(o, alone) for o in outs)
+
+
 def test_offsets_past_32_bits():
     """Adapters beyond 4 GiB of A and B."""
     n, R, K, N = 2100, 128, 8192, 8192

@@ -385,3 +385,27 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once():
+    """Attention calls that overlap, each with its workspace: sliced on tensor cores, few rows, many rows."""
+    runs = []
+    for new, lens in (([26, 9], [1300, 2900]), ([3, 2], [1500, 700]), ([70, 66], [900, 1700])):
+        c = Cache(f"tree/two{new[0]}", lens, 2, 128, 64, "int8")
+        rows = sum(new)
+        Q = rounded(normal(f"two{new[0]}/q", rows, 8, 128), "fp16")[0].cuda()
+        mask = binding.tree_masks(random_trees(f"two{new[0]}", new)).cuda()
+        blocks = c.to_device(binding)
+        batch = binding.KVBatch(device(c.table), device(c.kv_len), device(starts(new)), max_q=max(new))
+        size = binding.kvb_attention_workspace(blocks, batch, 8, rows)
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+        alone = binding.kvb_attention_tree(blocks, batch, Q, mask)
+        runs.append((blocks, batch, Q, mask, ws, alone, torch.cuda.Stream(), [torch.zeros_like(alone) for _ in range(12)]))
+    torch.cuda.synchronize()
+    for i in range(12):
+        for blocks, batch, Q, mask, ws, _, stream, outs in runs:
+            binding.kvb_attention_tree(blocks, batch, Q, mask, out=outs[i], workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    assert binding.device_error(clear=True) == 0
+    for *_, alone, _, outs in runs:
+        assert all(torch.equal(o, alone) for o in outs)
