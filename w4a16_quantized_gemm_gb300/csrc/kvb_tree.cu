@@ -11,11 +11,13 @@
 //   warp 17: pages and scales of the tiles to come, whose codes it requests into L2.
 // All waits are bounded.
 //
-// Measured: 16 trees of up to 26 nodes over up to 4096 tokens, int8, 32 query and 8 KV heads (104 rows): 55 us for
-// 108 MB of codes; a tile takes 2.9 k cycles (softmax of a row 2.0 k, one half's, converting K and V 1.9 k each, at
-// once; tensor pipe 19 %), starting a CTA and its last output 13 k.  128 CTAs of unequal length leave 35 % of the SMs'
-// time idle.  What mattered, in us for that case: pages and scales of four tiles at a time 71 -> 60, requested a page
-// at a time 56; masks as bits (instruction cache) 79 -> 67 in the kernel for prompts, which this one replaced at 66.
+// Measured: 16 trees of up to 26 nodes over up to 4096 tokens, int8, 32 query and 8 KV heads (104 rows): 47 us for
+// 108 MB of codes.  A tile takes 2.2 k cycles, which is what converting K takes four warps, and V four others (eight
+// each: 56 us in all, by the registers that the softmax then lacks); the softmax of a row takes 2.3 k, one half's, and
+// the hand-overs to the tensor cores and back 2 k more.  Tensor pipe 22 %, a third of it while the SMs are busy; 128
+// CTAs of unequal length leave 37 % of the SMs' time idle, and cutting them evenly costs more than it saves.  What
+// mattered, in us for that case: pages and scales of four tiles looked up at a time 71 -> 60, codes requested a page at
+// a time 56; rows of no node out of the mask's way 49; scores kept and fetched ahead 47.5.
 #include "kvb_attn.h"
 
 namespace w4 {
