@@ -220,6 +220,15 @@ def test_trees(fmt, dtype, D, T, Hq, Hkv, weights):
     run_tree(Cache(tag + "/c", [131, 41, 300], Hkv, D, T, fmt), [33, 41, 64], Hq, dtype, tag + "c", weights=weights)
 
 
+@pytest.mark.parametrize("fmt,dtype,D", [("int8", "bf16", 128), ("e4m3", "fp16", 128), ("e4m3", "bf16", 64)])
+def test_weights_of_one_row_tile(fmt, dtype, D):
+    """33 to 128 rows a head: several slices of the tokens, trees over a tile's and a slice's end, a sequence shorter than
+    a tile, one without rows, weights past the longest sequence."""
+    c = Cache(f"tree/second/{fmt}/{D}", [1300, 650, 21, 1036, 300], 2, D, 64, fmt)
+    run_tree(c, [21, 17, 21, 20, 0], 8, dtype, f"second/{fmt}/{D}", wide=1)
+    run_tree(c, [21, 17, 21, 20, 0], 12, dtype, f"second/{fmt}/{D}/six", max_len=1300, scale=-0.1)
+
+
 @pytest.mark.parametrize("nodes", [1, 2, 3, 8, 16, 17, 31, 32, 33, 64, 65, 129])
 def test_tree_sizes(nodes):
     """Every kernel and row tile, masks of one to five words, tokens before the tree in every phase of a tile."""

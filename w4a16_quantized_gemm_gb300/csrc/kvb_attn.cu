@@ -773,8 +773,10 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
   // kernel 47.6, with its second pass for the weights 124.  At 32 rows this one takes 39.
   // Trees: up to 128 rows have a tcgen05 kernel of their own (16 sequences of 4096 tokens, 8 KV heads: 12 rows 37 us in
   // the kernel for few rows and 45 in that one, 16 rows 38 and 45, 20 rows 51 and 45, 128 rows 48; one sequence of
-  // 600: 16 rows 9.6 and 11.6, 20 rows 11.8 and 11.6).
-  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (weights ? kFewRows : tree ? 16 : kFewRows / 2) ? 2 : -1;
+  // 600: 16 rows 9.6 and 11.6, 20 rows 11.8 and 11.6), and a second pass for the weights (16 x 4096: 32 rows 72 and 84
+  // us with weights, 36 rows 84 and 85, 52 rows 114 and 85; 9 x 1531, 12 heads of 64: 17 rows 27 and 28, 48 rows 50
+  // and 28).
+  p.rt = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= (tree ? kFewRows / 4 : kFewRows / 2) * (weights ? 2 : 1) ? 2 : -1;
   const bool narrow = tree && p.rt < 0 && rows <= 128;
   p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : narrow ? 128 : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
@@ -788,20 +790,11 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
     least = 2 * kTile;
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
   } else if (tree) {
-    // The slices for which waves of CTAs x (tiles of a slice + what starting a CTA costs, about six) is the least;
-    // the joining launch costs about four.
+    // Starting a CTA costs about six tiles, the joining launch four.
     unit = 128;
     least = 512;
-    const long long tiles = (V.max_len + 127) / 128;
-    long long best = 1, cost = -1;
-    for (long long c = 1; c == 1 || (c <= 64 && tiles / c >= 4); ++c) {
-      const long long t = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 6) + (c > 1 ? 4 : 0);
-      if (cost < 0 || t < cost) {
-        best = c;
-        cost = t;
-      }
-    }
-    chunk = (V.max_len + best - 1) / best;
+    const long long slices = slices_by_waves(ctas, (V.max_len + 127) / 128, 6, 4);
+    chunk = (V.max_len + slices - 1) / slices;
   } else {
     // Slices only where the rows alone leave SMs idle (300 tokens over 30000: 182 us; unsliced 574).
     unit = 128;

@@ -6,7 +6,8 @@
 namespace w4 {
 namespace kvb {
 
-constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows (without weights: half)
+constexpr int kFewRows = 64;  // most rows per (sequence, KV head) of the kernel for few rows (without weights, and of
+                              // trees: half)
 
 struct AttnParams {
   View V;
@@ -42,6 +43,21 @@ tm_status launch_tree_attn(const AttnParams& P, int format, int D, cudaStream_t 
 
 // The weights that tokens drew from many rows, by their lse (kvb_weights.cu).
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream);
+
+// Slices of `tiles` token tiles, each in a CTA of its own, for which waves of CTAs x (tiles of a slice + what starting
+// one costs) is the least; `join` for joining several.  None shorter than four tiles, at most 64.
+inline long long slices_by_waves(long long ctas, long long tiles, int start, int join) {
+  const long long sms = num_sms(current_device());
+  long long best = 1, cost = -1;
+  for (long long c = 1; c == 1 || (c <= 64 && tiles / c >= 4); ++c) {
+    const long long t = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + start) + (c > 1 ? join : 0);
+    if (cost < 0 || t < cost) {
+      best = c;
+      cost = t;
+    }
+  }
+  return best;
+}
 
 #if defined(__CUDACC__)
 // What a tree's row sees of 32 tokens: bit x stands for new token `first` + x (below 0: a token before the tree).

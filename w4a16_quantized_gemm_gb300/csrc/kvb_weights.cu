@@ -347,6 +347,247 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
+// Trees of up to 128 rows: one row tile for all tokens.  A CTA keeps its queries and takes a slice of the tokens in
+// tiles of 128, which its two groups of four warps take in turn, a token per thread: convert the codes of the group's
+// next tile into tensor memory, sum this one's scores.  16 sequences of 4096 tokens, 8 KV heads, 104 rows: 39 us (a new
+// CTA for every 256 tokens, as above: 90; masks from global memory in place of shared: 52).
+constexpr int kRtThreads = 288;
+
+template <int D>
+struct RtShape {
+  static constexpr uint32_t PANEL = kWtTile * 128;
+  static constexpr uint32_t ROWS = D / 64 * PANEL;       // [128] x -lse (base 2; -inf: no row)
+  static constexpr uint32_t MASK = ROWS + kWtTile * 4;   // [128][4] words: 128 rows are at most 128 nodes
+  static constexpr uint32_t BARS = MASK + kWtTile * 16;
+  static constexpr uint32_t SMEM = BARS + 64 + 1024;
+};
+
+template <int FMT, int D, bool BF16>
+__global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnParams P, int slice) {
+  using SH = RtShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+  const View& V = P.V;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
+  const Span s = span(V, b);
+  const int rows = s.n * P.G;
+  const long long j0 = (long long)blockIdx.y * slice, j1 = min(j0 + slice, P.w_stride);
+  const int N = rows > 0 && j0 < s.len ? (int)((min(j1, (long long)s.len) - j0 + kWtTile - 1) / kWtTile) : 0;
+  const size_t out = ((size_t)b * V.Hkv + h) * P.w_stride;
+  // What no tile holds: nothing is added there.
+  for (long long j = j0 + (long long)N * kWtTile + tid; j < j1; j += kRtThreads)
+    P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
+  if (N == 0) return;
+
+  const uint32_t bars = base + SH::BARS;
+  auto a_full = [&](int i) { return bars + 8 * i; };
+  auto s_full = [&](int i) { return bars + 16 + 8 * i; };
+  const uint32_t done = bars + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 40);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SH::BARS + 44);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(a_full(i), 4);
+      mbar_init(s_full(i), 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  } else {
+    // The queries, 16 bytes a thread, a row by neighbouring lanes; their lse.
+    constexpr int LANES = D / 8, STEP = 256 / LANES;
+    const int c = tid % LANES;
+#pragma unroll
+    for (int row = tid / LANES; row < kWtTile; row += STEP) {
+      const bool have = row < rows;
+      const int q = have ? row / P.G : 0, head = h * P.G + (have ? row - q * P.G : 0);
+      const uint4 x = ldg_or_zero(P.Q + (s.row0 + q) * P.q_stride + (long long)head * D + 8 * c, have);
+      sts128(base + (c >> 3) * SH::PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+    }
+    if (tid < kWtTile) {
+      const bool have = tid < rows;
+      const int q = have ? tid / P.G : 0, head = h * P.G + (have ? tid - q * P.G : 0);
+      const float x = have ? P.lse[(size_t)(s.row0 + q) * P.Hq + head] : -INFINITY;
+      reinterpret_cast<float*>(smem + SH::ROWS)[tid] = x != -INFINITY ? x * -1.44269504088896f : -INFINITY;
+      const uint32_t* mask = P.tree + (s.row0 + q) * P.tree_stride;
+      auto word = [&](int k) { return have && k < P.tree_words ? mask[k] : 0u; };
+      sts128(base + SH::MASK + 16 * tid, word(0), word(1), word(2), word(3));
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // A of group i's even and odd tiles at 128 i and 128 i + 64, scores at 256 + 128 i
+
+  if (warp < 8) {
+    const int i = warp >> 2, t = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, ts = tmem + lanes + 256 + 128 * i;
+    auto token = [&](int n) { return (int)j0 + n * kWtTile + t; };
+    auto page_for = [&](int n) {
+      return n < N && token(n) < s.len ? page_of(V, V.table, b, V.table_stride, token(n) >> V.t_shift) : -1;
+    };
+    // The page of a tile is looked up three of the group's tiles ahead, its codes are fetched two ahead.
+    uint4 x[D / 16];
+    auto fetch = [&](int n, int page) {  // returns what multiplies the scores; 0: no token
+      const size_t cell = (size_t)max(page, 0) * V.Hkv + h;
+      const uint8_t* src = V.k + ((cell << V.t_shift) + (token(n) & ((1 << V.t_shift) - 1))) * D;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) x[c] = ldg_or_zero(src + 16 * c, page >= 0);
+      return page >= 0 ? V.ks[cell] * P.scale_log2 : 0.f;
+    };
+    auto convert = [&](int odd) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          codes_half<FMT>(x[4 * c + k].x, o[8 * k], o[8 * k + 1]);
+          codes_half<FMT>(x[4 * c + k].y, o[8 * k + 2], o[8 * k + 3]);
+          codes_half<FMT>(x[4 * c + k].z, o[8 * k + 4], o[8 * k + 5]);
+          codes_half<FMT>(x[4 * c + k].w, o[8 * k + 6], o[8 * k + 7]);
+        }
+        if (BF16)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float2 f = unpack(o[k], false);
+            o[k] = pack_bf162(f.x, f.y);
+          }
+        tc_st_32x32b_x32(tmem + lanes + 128 * i + 64 * odd + 32 * c, o);
+      }
+      tc_wait_st();
+    };
+    int page = page_for(i), page_next = page_for(i + 2);
+    bool there = page >= 0, there_next = false;
+    float scale = fetch(i, page), scale_next = 0.f;
+    if (i < N) {
+      convert(0);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full(i));
+    }
+    if (i + 2 < N) {
+      there_next = page_next >= 0;
+      scale_next = fetch(i + 2, page_next);
+    }
+    page_next = page_for(i + 4);
+#pragma unroll 1
+    for (int n = i; n < N; n += 2) {
+      const int turn = n >> 1;
+      const float c = scale;
+      const bool counts = there;
+      scale = scale_next;
+      there = there_next;
+      if (n + 2 < N) {
+        convert((turn + 1) & 1);
+        if (n + 4 < N) {
+          there_next = page_next >= 0;
+          scale_next = fetch(n + 4, page_next);
+          page_next = page_for(n + 6);
+        }
+      }
+      const bool alive = wait_bar(s_full(i), (uint32_t)turn & 1u, abort_flag, &s_err_kvbw);
+      if (!__all_sync(0xffffffffu, alive)) break;
+      tc_fence_after();
+      const int j = token(n);
+      const bool whole = (int)j0 + n * kWtTile + kWtTile <= s.old;  // every row sees every token
+      const uint64_t c2 = f32x2(c, c);
+      uint64_t part[4] = {};
+#pragma unroll 1
+      for (int x0 = 0; x0 < 128; x0 += 64) {
+        uint32_t v[2][32];
+        tc_ld_32x32b_x32(ts + x0, v[0]);
+        tc_ld_32x32b_x32(ts + x0 + 32, v[1]);
+        tc_wait_ld_of(v[0]);
+        tc_wait_ld_of(v[1]);
+        if (x0 && n + 2 < N) {  // the next tile's codes stand ready, and the scores are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(a_full(i));
+        }
+        const uint8_t* row = smem + SH::ROWS + 4 * x0;
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
+            const uint32_t* y = &v[k >> 5][k & 31];
+            const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, l.x));
+            const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[2]), __uint_as_float(y[3])), c2, l.y));
+            part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
+            part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
+          }
+        } else {
+          const int node = j - s.old;
+          const uint32_t mask = base + SH::MASK + 16 * x0 + 4 * min(max(node, 0) >> 5, 3);
+          const uint32_t before = node < 0 ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const float y = fmaf(__uint_as_float(v[k >> 5][k & 31]), c, *reinterpret_cast<const float*>(row + 4 * k));
+            const bool see = ((lds32(mask + 16 * k) | before) >> (node & 31)) & 1u;
+            reinterpret_cast<float*>(part)[k & 7] += see ? ex2(y) : 0.f;
+          }
+        }
+      }
+      const float2 all = f32x2_get(add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3])));
+      if (j < j1) P.w_out[out + j] = (P.w_in ? P.w_in[out + j] : 0.f) + (counts ? all.x + all.y : 0.f);
+    }
+    tc_fence_before();
+  } else {
+    // ---------------- products ----------------
+    constexpr uint32_t id = idesc_f16_f32(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+    const uint32_t lead = elect_one(), tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq = smem_desc_sw128(base);
+#pragma unroll 1
+    for (int n = 0; n < N; ++n) {
+      const int i = n & 1, turn = n >> 1;
+      if (!__all_sync(0xffffffffu, wait_bar(a_full(i), (uint32_t)turn & 1u, abort_flag, &s_err_kvbw))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ts_if(lead, tm0 + 256 + 128 * i, tm0 + 128 * i + 64 * (turn & 1) + 8 * k,
+                  dq + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
+      commit_if(lead, s_full(i));
+    }
+    commit_if(lead, done);
+    if (lead) {  // nothing is left in flight when tensor memory is freed, on an abort either
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try_wait(done, 0)) {
+        if (globaltimer() - t0 > kWaitLimitNs) {
+          atomicOr(&s_err_kvbw, kErrTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int D, bool BF16>
+static tm_status launch_tree(const AttnParams& P, cudaStream_t stream) {
+  using SH = RtShape<D>;
+  static std::atomic<unsigned long long> done{0};
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(tree_weights_kernel<FMT, D, BF16>), SH::SMEM))
+    return TM_ERR_CUDA;
+  // A start costs about as much as ten tiles.
+  const long long ctas = (long long)P.V.B * P.V.Hkv, tiles = ((long long)P.V.max_len + kWtTile - 1) / kWtTile;
+  const long long slices = slices_by_waves(ctas, tiles, 10, 0);
+  const long long slice = ((tiles + slices - 1) / slices > 4 ? (tiles + slices - 1) / slices : 4) * kWtTile;
+  const dim3 grid((unsigned)ctas, (unsigned)((P.w_stride + slice - 1) / slice));
+  tree_weights_kernel<FMT, D, BF16><<<grid, kRtThreads, SH::SMEM, stream>>>(P, (int)slice);
+  return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
+}
+
 template <int FMT, int D, bool BF16, bool TREE>
 static tm_status launch(const AttnParams& P, cudaStream_t stream) {
   using SH = WtShape<D>;
@@ -371,6 +612,8 @@ static tm_status launch(const AttnParams& P, cudaStream_t stream) {
 
 template <int FMT, int D>
 static tm_status launch(const AttnParams& P, cudaStream_t stream) {
+  if (P.tree && (long long)P.V.max_q * P.G <= kWtTile)
+    return P.bf16 ? launch_tree<FMT, D, true>(P, stream) : launch_tree<FMT, D, false>(P, stream);
   if (P.tree) return P.bf16 ? launch<FMT, D, true, true>(P, stream) : launch<FMT, D, false, true>(P, stream);
   return P.bf16 ? launch<FMT, D, true, false>(P, stream) : launch<FMT, D, false, false>(P, stream);
 }
