@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
 // Trees of up to 128 rows: one row tile for all tokens.  A CTA keeps its queries and takes a slice of the tokens in
 // tiles of 128, which its two groups of four warps take in turn, a token per thread: convert the codes of the group's
 // next tile into tensor memory, sum this one's scores.  16 sequences of 4096 tokens, 8 KV heads, 104 rows: 39 us (a new
-// CTA for every 256 tokens, as above: 90; masks from global memory in place of shared: 52).
+// CTA for every 256 tokens 90, a pair of them, as above, 171; masks from global memory in place of shared 52).
 constexpr int kRtThreads = 288;
 
 template <int D>
