@@ -229,6 +229,14 @@ def test_weights_of_one_row_tile(fmt, dtype, D):
     run_tree(c, [21, 17, 21, 20, 0], 12, dtype, f"second/{fmt}/{D}/six", max_len=1300, scale=-0.1)
 
 
+@pytest.mark.parametrize("fmt,dtype,D", [("int8", "fp16", 128), ("e4m3", "bf16", 64)])
+@pytest.mark.parametrize("Hq,new", [(5, [30, 52, 3]), (8, [64, 17, 40]), (8, [65, 70, 1]), (2, [140, 256, 201])])
+def test_weights_of_more_row_tiles(fmt, dtype, D, Hq, new):
+    """Two to four row tiles, not all of them used by every sequence, and more; masks of up to eight words."""
+    c = Cache(f"tree/rows/{fmt}/{Hq}/{new[0]}", [new[0] + 700, new[1], new[2] + 130], 1, D, 32, fmt)
+    run_tree(c, new, Hq, dtype, f"rows/{fmt}/{Hq}/{new[0]}", wide=1)
+
+
 @pytest.mark.parametrize("nodes", [1, 2, 3, 8, 16, 17, 31, 32, 33, 64, 65, 129])
 def test_tree_sizes(nodes):
     """Every kernel and row tile, masks of one to five words, tokens before the tree in every phase of a tile."""

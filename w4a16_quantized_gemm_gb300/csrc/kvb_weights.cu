@@ -347,19 +347,22 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
   cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
-// Trees of up to 128 rows: one row tile for all tokens.  A CTA keeps its queries and takes a slice of the tokens in
-// tiles of 128, which its two groups of four warps take in turn, a token per thread: convert the codes of the group's
-// next tile into tensor memory, sum this one's scores.  16 sequences of 4096 tokens, 8 KV heads, 104 rows: 39 us (a new
-// CTA for every 256 tokens 90, a pair of them, as above, 171; masks from global memory in place of shared 52).
+// Trees of up to 512 rows: the same row tiles for all tokens.  A CTA keeps its queries and takes a slice of the tokens
+// in tiles of 128, which its two groups of four warps take in turn, a token per thread: convert the codes of the group's
+// next tile into tensor memory, sum this one's scores, a row tile at a time.  16 sequences of 4096 tokens, 8 KV heads,
+// 104 rows: 39 us (a new CTA for every 256 tokens 90, a pair of them, as above, 171; masks from global memory in place
+// of shared 52); 160 rows 125 with the attention (238), 2 x 30000 tokens, 504 rows 198 (308).
 constexpr int kRtThreads = 288;
+constexpr int kRtTiles = 4;  // row tiles at most: 128 KB of queries, 32 KB of masks
 
 template <int D>
 struct RtShape {
   static constexpr uint32_t PANEL = kWtTile * 128;
-  static constexpr uint32_t ROWS = D / 64 * PANEL;       // [128] x -lse (base 2; -inf: no row)
-  static constexpr uint32_t MASK = ROWS + kWtTile * 4;   // [128][4] words: 128 rows are at most 128 nodes
-  static constexpr uint32_t BARS = MASK + kWtTile * 16;
-  static constexpr uint32_t SMEM = BARS + 64 + 1024;
+  static constexpr uint32_t TILE = D / 64 * PANEL;
+  static constexpr uint32_t BARS = 0;
+  static constexpr uint32_t Q = 1024;  // [tiles]
+  // behind them [tiles * 128] x -lse (base 2; -inf: no row), then [tiles * 128][words] of the masks
+  static uint32_t smem(int tiles, int words) { return 1024 + Q + tiles * (TILE + kWtTile * (4 + 4 * words)); }
 };
 
 template <int FMT, int D, bool BF16>
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int b = blockIdx.x / V.Hkv, h = blockIdx.x - b * V.Hkv;
   const Span s = span(V, b);
-  const int rows = s.n * P.G;
+  const int rows = s.n * P.G, tiles = (rows + kWtTile - 1) / kWtTile;
   const long long j0 = (long long)blockIdx.y * slice, j1 = min(j0 + slice, P.w_stride);
   const int N = rows > 0 && j0 < s.len ? (int)((min(j1, (long long)s.len) - j0 + kWtTile - 1) / kWtTile) : 0;
   const size_t out = ((size_t)b * V.Hkv + h) * P.w_stride;
@@ -381,6 +384,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
     P.w_out[out + j] = P.w_in ? P.w_in[out + j] : 0.f;
   if (N == 0) return;
 
+  const uint32_t lse_at = SH::Q + tiles * SH::TILE, masks_at = lse_at + tiles * kWtTile * 4;
   const uint32_t bars = base + SH::BARS;
   auto a_full = [&](int i) { return bars + 8 * i; };
   auto s_full = [&](int i) { return bars + 16 + 8 * i; };
@@ -403,21 +407,22 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
     // The queries, 16 bytes a thread, a row by neighbouring lanes; their lse.
     constexpr int LANES = D / 8, STEP = 256 / LANES;
     const int c = tid % LANES;
-#pragma unroll
-    for (int row = tid / LANES; row < kWtTile; row += STEP) {
+#pragma unroll 4
+    for (int row = tid / LANES; row < tiles * kWtTile; row += STEP) {
       const bool have = row < rows;
       const int q = have ? row / P.G : 0, head = h * P.G + (have ? row - q * P.G : 0);
       const uint4 x = ldg_or_zero(P.Q + (s.row0 + q) * P.q_stride + (long long)head * D + 8 * c, have);
-      sts128(base + (c >> 3) * SH::PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+      sts128(base + SH::Q + (row >> 7) * SH::TILE + (c >> 3) * SH::PANEL + (row & 127) * 128 +
+                 (((c & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
     }
-    if (tid < kWtTile) {
-      const bool have = tid < rows;
-      const int q = have ? tid / P.G : 0, head = h * P.G + (have ? tid - q * P.G : 0);
+    for (int row = tid; row < tiles * kWtTile; row += 256) {
+      const bool have = row < rows;
+      const int q = have ? row / P.G : 0, head = h * P.G + (have ? row - q * P.G : 0);
       const float x = have ? P.lse[(size_t)(s.row0 + q) * P.Hq + head] : -INFINITY;
-      reinterpret_cast<float*>(smem + SH::ROWS)[tid] = x != -INFINITY ? x * -1.44269504088896f : -INFINITY;
+      reinterpret_cast<float*>(smem + lse_at)[row] = x != -INFINITY ? x * -1.44269504088896f : -INFINITY;
       const uint32_t* mask = P.tree + (s.row0 + q) * P.tree_stride;
-      auto word = [&](int k) { return have && k < P.tree_words ? mask[k] : 0u; };
-      sts128(base + SH::MASK + 16 * tid, word(0), word(1), word(2), word(3));
+      for (int k = 0; k < P.tree_words; ++k)
+        reinterpret_cast<uint32_t*>(smem + masks_at)[row * P.tree_words + k] = have ? mask[k] : 0u;
     }
     fence_proxy_async_smem();
   }
@@ -477,6 +482,8 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
       scale_next = fetch(i + 2, page_next);
     }
     page_next = page_for(i + 4);
+    bool alive = true;
+    int unit = 0;  // row tiles of this group's tokens so far
 #pragma unroll 1
     for (int n = i; n < N; n += 2) {
       const int turn = n >> 1;
@@ -492,48 +499,58 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
           page_next = page_for(n + 6);
         }
       }
-      const bool alive = wait_bar(s_full(i), (uint32_t)turn & 1u, abort_flag, &s_err_kvbw);
-      if (!__all_sync(0xffffffffu, alive)) break;
-      tc_fence_after();
       const int j = token(n);
       const bool whole = (int)j0 + n * kWtTile + kWtTile <= s.old;  // every row sees every token
       const uint64_t c2 = f32x2(c, c);
-      uint64_t part[4] = {};
+      uint64_t part[4] = {};  // each at most 64 rows' sums
 #pragma unroll 1
-      for (int x0 = 0; x0 < 128; x0 += 64) {
-        uint32_t v[2][32];
-        tc_ld_32x32b_x32(ts + x0, v[0]);
-        tc_ld_32x32b_x32(ts + x0 + 32, v[1]);
-        tc_wait_ld_of(v[0]);
-        tc_wait_ld_of(v[1]);
-        if (x0 && n + 2 < N) {  // the next tile's codes stand ready, and the scores are read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(a_full(i));
-        }
-        const uint8_t* row = smem + SH::ROWS + 4 * x0;
-        if (whole) {
-#pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
-            const uint32_t* y = &v[k >> 5][k & 31];
-            const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, l.x));
-            const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[2]), __uint_as_float(y[3])), c2, l.y));
-            part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
-            part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
+      for (int r = 0; r < tiles; ++r, ++unit) {
+        alive = wait_bar(s_full(i), (uint32_t)unit & 1u, abort_flag, &s_err_kvbw);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int x0 = 0; x0 < 128; x0 += 64) {
+          uint32_t v[2][32];
+          tc_ld_32x32b_x32(ts + x0, v[0]);
+          tc_ld_32x32b_x32(ts + x0 + 32, v[1]);
+          tc_wait_ld_of(v[0]);
+          tc_wait_ld_of(v[1]);
+          // The scores are read; after the last row tile's the next codes stand ready.
+          if (x0 && (r + 1 < tiles || n + 2 < N)) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(a_full(i));
           }
-        } else {
-          const int node = j - s.old;
-          const uint32_t mask = base + SH::MASK + 16 * x0 + 4 * min(max(node, 0) >> 5, 3);
-          const uint32_t before = node < 0 ? 0xffffffffu : 0u;
+          const int row0 = r * kWtTile + x0;
+          const uint8_t* row = smem + lse_at + 4 * row0;
+          if (whole) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float y = fmaf(__uint_as_float(v[k >> 5][k & 31]), c, *reinterpret_cast<const float*>(row + 4 * k));
-            const bool see = ((lds32(mask + 16 * k) | before) >> (node & 31)) & 1u;
-            reinterpret_cast<float*>(part)[k & 7] += see ? ex2(y) : 0.f;
+            for (int k = 0; k < 64; k += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(row + 4 * k);  // -lse of four rows
+              const uint32_t* y = &v[k >> 5][k & 31];
+              const float2 e0 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, l.x));
+              const float2 e1 = f32x2_get(fma_f32x2(f32x2(__uint_as_float(y[2]), __uint_as_float(y[3])), c2, l.y));
+              part[(k >> 1) & 2] = add_f32x2(part[(k >> 1) & 2], f32x2(ex2(e0.x), ex2(e0.y)));
+              part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
+            }
+          } else {
+            const int node = j - s.old, words = P.tree_words;
+            uint32_t mask = base + masks_at + 4 * (row0 * words + min(max(node, 0) >> 5, words - 1));
+            const uint32_t before = node < 0 ? 0xffffffffu : 0u;
+#pragma unroll
+            for (int k = 0; k < 64; k += 2, mask += 8 * words) {
+              const float2 l = *reinterpret_cast<const float2*>(row + 4 * k);
+              const float e0 = fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x);
+              const float e1 = fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y);
+              const bool see0 = ((lds32(mask) | before) >> (node & 31)) & 1u;
+              const bool see1 = ((lds32(mask + 4 * words) | before) >> (node & 31)) & 1u;
+              part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(see0 ? ex2(e0) : 0.f, see1 ? ex2(e1) : 0.f));
+            }
           }
         }
       }
+      if (!alive) break;
       const float2 all = f32x2_get(add_f32x2(add_f32x2(part[0], part[1]), add_f32x2(part[2], part[3])));
       if (j < j1) P.w_out[out + j] = (P.w_in ? P.w_in[out + j] : 0.f) + (counts ? all.x + all.y : 0.f);
     }
@@ -542,17 +559,24 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
     // ---------------- products ----------------
     constexpr uint32_t id = idesc_f16_f32(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
     const uint32_t lead = elect_one(), tm0 = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dq = smem_desc_sw128(base);
+    const uint64_t dq = smem_desc_sw128(base + SH::Q);
+    bool alive = true;
 #pragma unroll 1
-    for (int n = 0; n < N; ++n) {
-      const int i = n & 1, turn = n >> 1;
-      if (!__all_sync(0xffffffffu, wait_bar(a_full(i), (uint32_t)turn & 1u, abort_flag, &s_err_kvbw))) break;
-      tc_fence_after();
+    for (int n0 = 0; n0 < N && alive; n0 += 2) {
+#pragma unroll 1
+      for (int x = 0; x < 2 * tiles && alive; ++x) {  // the two tiles' rows in turn
+        const int i = x & 1, r = x >> 1, turn = n0 >> 1, unit = turn * tiles + r;
+        if (n0 + i >= N) continue;
+        alive = __all_sync(0xffffffffu, wait_bar(a_full(i), (uint32_t)unit & 1u, abort_flag, &s_err_kvbw));
+        if (!alive) break;
+        tc_fence_after();
+        const uint64_t db = dq + (uint64_t)r * (SH::TILE >> 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ts_if(lead, tm0 + 256 + 128 * i, tm0 + 128 * i + 64 * (turn & 1) + 8 * k,
-                  dq + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
-      commit_if(lead, s_full(i));
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts_if(lead, tm0 + 256 + 128 * i, tm0 + 128 * i + 64 * (turn & 1) + 8 * k,
+                    db + (k >> 2) * (uint64_t)(SH::PANEL >> 4) + (uint64_t)((k & 3) * 2), id, k > 0);
+        commit_if(lead, s_full(i));
+      }
     }
     commit_if(lead, done);
     if (lead) {  // nothing is left in flight when tensor memory is freed, on an abort either
@@ -577,14 +601,15 @@ template <int FMT, int D, bool BF16>
 static tm_status launch_tree(const AttnParams& P, cudaStream_t stream) {
   using SH = RtShape<D>;
   static std::atomic<unsigned long long> done{0};
-  if (!smem_attr_once(done, reinterpret_cast<const void*>(tree_weights_kernel<FMT, D, BF16>), SH::SMEM))
+  if (!smem_attr_once(done, reinterpret_cast<const void*>(tree_weights_kernel<FMT, D, BF16>), SH::smem(kRtTiles, 16)))
     return TM_ERR_CUDA;
   // A start costs about as much as ten tiles.
   const long long ctas = (long long)P.V.B * P.V.Hkv, tiles = ((long long)P.V.max_len + kWtTile - 1) / kWtTile;
   const long long slices = slices_by_waves(ctas, tiles, 10, 0);
   const long long slice = ((tiles + slices - 1) / slices > 4 ? (tiles + slices - 1) / slices : 4) * kWtTile;
   const dim3 grid((unsigned)ctas, (unsigned)((P.w_stride + slice - 1) / slice));
-  tree_weights_kernel<FMT, D, BF16><<<grid, kRtThreads, SH::SMEM, stream>>>(P, (int)slice);
+  const uint32_t smem = SH::smem((P.V.max_q * P.G + kWtTile - 1) / kWtTile, P.tree_words);
+  tree_weights_kernel<FMT, D, BF16><<<grid, kRtThreads, smem, stream>>>(P, (int)slice);
   return cudaGetLastError() == cudaSuccess ? TM_OK : TM_ERR_CUDA;
 }
 
@@ -612,7 +637,7 @@ static tm_status launch(const AttnParams& P, cudaStream_t stream) {
 
 template <int FMT, int D>
 static tm_status launch(const AttnParams& P, cudaStream_t stream) {
-  if (P.tree && (long long)P.V.max_q * P.G <= kWtTile)
+  if (P.tree && (long long)P.V.max_q * P.G <= kRtTiles * kWtTile)
     return P.bf16 ? launch_tree<FMT, D, true>(P, stream) : launch_tree<FMT, D, false>(P, stream);
   if (P.tree) return P.bf16 ? launch<FMT, D, true, true>(P, stream) : launch<FMT, D, false, true>(P, stream);
   return P.bf16 ? launch<FMT, D, true, false>(P, stream) : launch<FMT, D, false, false>(P, stream);
