@@ -1010,6 +1010,8 @@ class Rope:
         self.table, self.interleaved = table, bool(interleaved)
         self.positions, self.dims = table.shape
         self._p = _dev(table, torch.float32, "table")
+        self._c = KVBRopeStruct(self._p, self.positions, self.dims, self.interleaved, None)  # positions: the slots
+        self._ref = ctypes.byref(self._c)
 
 
 def kvb_append_rope(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.Tensor, rope: Rope,
@@ -1040,15 +1042,15 @@ def kvb_append_rope(cache: KVBlocks, batch: KVBatch, K: torch.Tensor, V: torch.T
             raise ValueError("q_out must have the shape and dtype of Q")
     elif q_out is not None:
         raise ValueError("q_out comes with Q")
-    pp = None
+    ref = rope._ref
     if pos is not None:
         if pos.shape != (rows,):
             raise ValueError("pos must be int32 [rows]")
-        pp = _dev(pos, torch.int32, "pos")
+        ref = ctypes.byref(KVBRopeStruct(rope._p, rope.positions, rope.dims, rope.interleaved,
+                                         _dev(pos, torch.int32, "pos")))
     wp, wn = _kvb_weights(w, batch.B, Hkv, "w")
-    r = KVBRopeStruct(rope._p, rope.positions, rope.dims, rope.interleaved, pp)
     st = (_lib or load()).tm_kvb_append_rope(cache._ref, batch._rows(rows), kp, ks, vp, vs, qp, qs, Hq, op, os_,
-                                             ctypes.byref(r), dtype, wp, wn, _kvb_stream(cache, stream))
+                                             ref, dtype, wp, wn, _kvb_stream(cache, stream))
     if st:
         raise TMError(st, "tm_kvb_append_rope")
     return q_out
