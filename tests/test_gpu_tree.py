@@ -99,6 +99,20 @@ def test_rope_append(fmt, dtype, D, T, Hq, Hkv, dims, inter):
     run_rope(c, [9, 3], Hq, dtype, "rope3", dims, inter, pos=pos, positions=901)
 
 
+@pytest.mark.parametrize("fmt,dtype,D,T,Hq,Hkv,dims,inter", ROPES)
+def test_rope_append_of_many_pages(fmt, dtype, D, T, Hq, Hkv, dims, inter):
+    """More CTAs than start at once, of single tokens, of whole pages, and of a few tokens."""
+    B = 520 // Hkv + 1
+    c = Cache(f"rope/wide/one/{fmt}/{D}/{T}", [1 + 7 * b % (T + 3) for b in range(B)], Hkv, D, T, fmt)
+    run_rope(c, [1] * B, Hq, dtype, "rope4", dims, inter, one_each=True)
+    new = [(2 * T, 5, 1, T + 3, 0)[b % 5] for b in range(B // 2)]
+    c = Cache(f"rope/wide/many/{fmt}/{D}/{T}", [n + 3 * b % T for b, n in enumerate(new)], Hkv, D, T, fmt, spread=0.2)
+    run_rope(c, new, Hq, dtype, "rope5", dims, inter)
+    new = [1 + b % 5 for b in range(B)]
+    c = Cache(f"rope/wide/few/{fmt}/{D}/{T}", [n + 5 * b % (T + 9) for b, n in enumerate(new)], Hkv, D, T, fmt, spread=0.2)
+    run_rope(c, new, Hq, dtype, "rope6", dims, inter, in_place=True)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_rope_append_of_infinities_and_nan(fmt, dtype):

@@ -43,9 +43,9 @@ __device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, const Divisor
   return e4m3x4(f32x2_get(divide(f32x2(x.x, x.y), by)), f32x2_get(divide(f32x2(y.x, y.y), by))) | signs;
 }
 
-// One CTA of kAppendThreads: the tokens of slots lo .. hi - 1 (all in the page of slots begin ..) of head h into
+// One CTA of THREADS: the tokens of slots lo .. hi - 1 (all in the page of slots begin ..) of head h into
 // `pool`.  VECS: vectors of 8 values per thread, enough for the new tokens of one page.
-template <int FMT, bool BF16, int VECS>
+template <int FMT, bool BF16, int VECS, int THREADS = kAppendThreads>
 __device__ __forceinline__ void append_page(const View& V, const Span& s, int h, int page, int begin, int lo, int hi,
                                             const uint16_t* x_in, long long stride, int d_shift, uint8_t* pool,
                                             float* scales, uint32_t* warp_max) {
@@ -57,7 +57,7 @@ __device__ __forceinline__ void append_page(const View& V, const Span& s, int h,
   uint4 x[VECS];
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
-    const int v = tid + i * kAppendThreads;
+    const int v = tid + i * THREADS;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (v < total)
       x[i] = *reinterpret_cast<const uint4*>(src + (v >> vec_shift) * stride +
@@ -79,7 +79,7 @@ __device__ __forceinline__ void append_page(const View& V, const Span& s, int h,
   const float was = continued ? *scale : 0.f;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
+  for (int i = 0; i < THREADS / 32; ++i) m = max(m, warp_max[i]);
   const bool clean = m < (BF16 ? 0x7f80u : 0x7c00u);
   float a = unpack(m, BF16).x;
   if (!clean) {  // uniform: the largest finite magnitude, an infinity counting as `top`
@@ -98,7 +98,7 @@ __device__ __forceinline__ void append_page(const View& V, const Span& s, int h,
     if ((tid & 31) == 0) warp_max[tid >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
+    for (int i = 0; i < THREADS / 32; ++i) m = max(m, warp_max[i]);
     a = __uint_as_float(m);
   }
   const float now = fmaxf(scale_for<FMT>(a), was);
@@ -110,7 +110,7 @@ __device__ __forceinline__ void append_page(const View& V, const Span& s, int h,
   auto store = [&](auto is_clean) {
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-      const int v = tid + i * kAppendThreads;
+      const int v = tid + i * THREADS;
       if (v >= total) break;
       uint2 c;
       c.x = codes4<FMT, BF16, decltype(is_clean)::value>(x[i].x, x[i].y, by, top);
@@ -125,7 +125,7 @@ __device__ __forceinline__ void append_page(const View& V, const Span& s, int h,
   if (continued && now > was) {
     const int earlier = (lo - begin) << vec_shift;
     const uint64_t was2 = f32x2(was, was);
-    for (int v = tid; v < earlier; v += kAppendThreads) {
+    for (int v = tid; v < earlier; v += THREADS) {
       uint2* at = reinterpret_cast<uint2*>(codes + ((size_t)v << 3));
       uint2 c = *at;
       c.x = recode4<FMT>(c.x, was2, by);

@@ -9,9 +9,9 @@
 // query heads of the group.  A thread works on units of 16 dimensions: two vectors of 8 that hold both halves of their
 // pairs.  The rotated keys stay in registers (at most 64 a thread) across the maximum and the rounding.
 //
-// Bound by memory.  Measured: 26.6 k tokens, bf16, 32 query heads, 8 KV heads of 128 to e4m3: 107 us for 600 MB, 0.83 of
-// the HBM copy rate (queries in the keys' CTAs, which then are two per SM: 141 us).  One token of 32 sequences: 4.1 us,
-// a launch and three dependent loads.
+// Bound by memory.  Measured: 26.6 k tokens, bf16, 32 query heads, 8 KV heads of 128 to e4m3: 99.6 us for 600 MB, 0.89 of
+// the HBM copy rate (queries in the keys' CTAs of 256 threads, which then are two per SM: 141 us).  One token of 32
+// sequences: 2.5 us, a launch and three dependent loads.
 #include "kvb_append.cuh"
 
 namespace w4 {
@@ -78,9 +78,9 @@ __device__ __forceinline__ uint32_t codes_of(const float* y, const Divisor& by) 
 }
 
 // UNITS: units of 16 dimensions per thread, enough for the new tokens of one page and head.
-template <int FMT, bool BF16, int UNITS, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rope_kernel(const RopeParams R) {
-  __shared__ uint32_t warp_max[kAppendThreads / 32];
+template <int FMT, bool BF16, int UNITS, bool INTER, int THREADS>
+__global__ void __launch_bounds__(THREADS, (UNITS == 4 ? 2 : 3) * 256 / THREADS) append_rope_kernel(const RopeParams R) {
+  __shared__ uint32_t warp_max[THREADS / 32];
   const AppendParams& P = R.A;
   const View& V = P.V;
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
 
   if (role == 2) {  // ---- queries: four heads of the group, so that angles serve them together
     const int fours = (R.G + 3) >> 2;
-    for (int i = tid; i < total * fours; i += kAppendThreads) {
+    for (int i = tid; i < total * fours; i += THREADS) {
       const int u = i / fours, g0 = 4 * (i - u * fours);
       const int t = lo + (u >> unit_shift), p = u & ((1 << unit_shift) - 1);
       const long long row = s.row0 + (long long)(t - s.old);
@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
   const int page = slots ? page_of(V, V.table, b, V.table_stride, blk) : -1;
   if (role == 1) {  // ---- values
     if (P.w && slots)
-      for (int t = lo + tid; t < hi && t < P.w_stride; t += kAppendThreads)
+      for (int t = lo + tid; t < hi && t < P.w_stride; t += THREADS)
         P.w[((size_t)b * V.Hkv + h) * P.w_stride + t] = 0.f;
     if (page >= 0)
-      append_page<FMT, BF16, 2 * UNITS>(V, s, h, page, begin, lo, hi, P.x[1], P.stride[1], P.d_shift, V.v, V.vs, warp_max);
+      append_page<FMT, BF16, 2 * UNITS, THREADS>(V, s, h, page, begin, lo, hi, P.x[1], P.stride[1], P.d_shift, V.v, V.vs, warp_max);
     return;
   }
 
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
   float y[UNITS][16];
   // The rotated keys; clean: NaN and infinities replaced before and after.
   auto fetch = [&](int i, auto clean) {
-    const int u = tid + i * kAppendThreads;
+    const int u = tid + i * THREADS;
 #pragma unroll
     for (int e = 0; e < 16; ++e) y[i][e] = 0.f;
     if (u >= total) return;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
     if ((tid & 31) == 0) warp_max[tid >> 5] = v;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAppendThreads / 32; ++i) v = max(v, warp_max[i]);
+    for (int i = 0; i < THREADS / 32; ++i) v = max(v, warp_max[i]);
     return v;
   };
   const size_t cell = (size_t)page * V.Hkv + h;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
   uint8_t* codes = V.k + ((cell << V.t_shift) << P.d_shift);
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
-    const int u = tid + i * kAppendThreads;
+    const int u = tid + i * THREADS;
     if (u >= total) break;
     const int t = lo + (u >> unit_shift), p = u & ((1 << unit_shift) - 1);
     int d0, d1;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
   if (continued && now > was) {  // earlier codes of the page, rounded anew
     const int earlier = (lo - begin) << (P.d_shift - 3);
     const uint64_t was2 = f32x2(was, was);
-    for (int v = tid; v < earlier; v += kAppendThreads) {
+    for (int v = tid; v < earlier; v += THREADS) {
       uint2* at = reinterpret_cast<uint2*>(codes + ((size_t)v << 3));
       uint2 c = *at;
       c.x = recode4<FMT>(c.x, was2, by);
@@ -248,12 +248,27 @@ __global__ void __launch_bounds__(kAppendThreads, UNITS == 4 ? 2 : 3) append_rop
 
 template <int FMT, bool BF16, bool INTER>
 static void launch_rope(const RopeParams& P, dim3 grid, int units, cudaStream_t s) {
-  if (units <= 1)
-    append_rope_kernel<FMT, BF16, 1, INTER><<<grid, kAppendThreads, 0, s>>>(P);
-  else if (units <= 2)
-    append_rope_kernel<FMT, BF16, 2, INTER><<<grid, kAppendThreads, 0, s>>>(P);
+  // Where the CTAs do not all start at once, smaller ones keep more pages in flight: 64 threads for up to 128 units, 128
+  // for up to 512.  Four prompts of 8191 tokens (512 units) 99.6 us (256 threads: 106.6); 16 k tokens, 32/8 heads, pages
+  // of 64 units 32 (83), of 128 units 30 and 52 (49 and 90; 128 threads: 33 and 57); 46 x 519, 256 units 13.6 (16.1; 64
+  // threads: 16.3); one token of each of 32 sequences 2.5 (4.1).  Else more threads are done earlier: 26 nodes of each of
+  // 16, 32/4 heads of 64: 2.9 (128 threads: 3.5).
+  constexpr int kHalf = kAppendThreads / 2, kQuarter = kAppendThreads / 4;
+  const bool waves = (long long)grid.x * grid.y * grid.z > 3ll * num_sms(current_device());
+  if (waves && units <= kQuarter)
+    append_rope_kernel<FMT, BF16, 1, INTER, kQuarter><<<grid, kQuarter, 0, s>>>(P);
+  else if (waves && units <= 2 * kQuarter)
+    append_rope_kernel<FMT, BF16, 2, INTER, kQuarter><<<grid, kQuarter, 0, s>>>(P);
+  else if (waves && units <= 2 * kHalf)
+    append_rope_kernel<FMT, BF16, 2, INTER, kHalf><<<grid, kHalf, 0, s>>>(P);
+  else if (waves && units <= 4 * kHalf)
+    append_rope_kernel<FMT, BF16, 4, INTER, kHalf><<<grid, kHalf, 0, s>>>(P);
+  else if (units <= kAppendThreads)
+    append_rope_kernel<FMT, BF16, 1, INTER, kAppendThreads><<<grid, kAppendThreads, 0, s>>>(P);
+  else if (units <= 2 * kAppendThreads)
+    append_rope_kernel<FMT, BF16, 2, INTER, kAppendThreads><<<grid, kAppendThreads, 0, s>>>(P);
   else
-    append_rope_kernel<FMT, BF16, 4, INTER><<<grid, kAppendThreads, 0, s>>>(P);
+    append_rope_kernel<FMT, BF16, 4, INTER, kAppendThreads><<<grid, kAppendThreads, 0, s>>>(P);
 }
 
 template <int FMT, bool BF16>
@@ -309,7 +324,7 @@ extern "C" tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_
   P.roles = Q ? 3 : 2;
   const dim3 grid((unsigned)(P.roles * append_pages(V)), (unsigned)V.Hkv, (unsigned)V.B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int units = ((cache->T < V.max_q ? cache->T : V.max_q) * D / 16 + kAppendThreads - 1) / kAppendThreads;
+  const int units = (cache->T < V.max_q ? cache->T : V.max_q) * D / 16;  // of a page
   const bool bf16 = dtype == TM_KVB_BF16, inter = rope->interleaved != 0;
   if (cache->format == TM_KVB_INT8)
     bf16 ? launch_rope<TM_KVB_INT8, true>(P, grid, units, inter, s)
