@@ -104,10 +104,12 @@ def tokens(codes, scales, row, length, h, fmt):
     return x, there
 
 
-def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None, tree=None):
+def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None, tree=None, max_q=None, max_len=None):
     """Q [rows][Hq][D] (binary64 values) -> out, lse [rows][Hq], w [B][Hkv][max len], and for
     error bounds sum p |v| [rows][Hq][D] and max_j scale sum |q k| [rows][Hq].
-    tree: mask words [rows][words] over the sequence's new tokens, in place of the causal rule."""
+    tree: mask words [rows][words] over the sequence's new tokens, in place of the causal rule.
+    max_q, max_len: the host's bounds.  Rows past max_q are left out, and tokens past max_len; of a mask the first
+    ceil(max_q / 32) words count, new tokens past them are not seen."""
     rows, Hq, D = Q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -117,17 +119,17 @@ def attention(Q, k, v, ks, vs, table, kv_len, q_start, fmt, scale=None, tree=Non
     w = np.zeros((table.shape[0], Hkv, max(1, int(max(kv_len, default=0)))))
     for b in range(table.shape[0]):
         n, length = int(q_start[b + 1] - q_start[b]), max(int(kv_len[b]), 0)
+        old, computed, length = length - n, n if max_q is None else min(n, max_q), length if max_len is None else min(length, max_len)
         for h in range(Hkv):
             kh, there = tokens(k, ks, table[b], length, h, fmt)
             vh, _ = tokens(v, vs, table[b], length, h, fmt)
-            for i in range(n):
+            for i in range(computed):
                 if tree is None:
-                    seen = there & (np.arange(length) <= length - n + i)
+                    seen = there & (np.arange(length) <= old + i)
                 else:
-                    words = [int(x) & 0xffffffff for x in tree[q_start[b] + i]]
+                    words = [int(x) & 0xffffffff for x in tree[q_start[b] + i][:None if max_q is None else -(-max_q // 32)]]
                     mask = sum(x << (32 * k) for k, x in enumerate(words))
-                    seen = there & np.array([j < length - n or mask >> (j - length + n) & 1 == 1 for j in range(length)],
-                                            dtype=bool)
+                    seen = there & np.array([j < old or mask >> (j - old) & 1 == 1 for j in range(length)], dtype=bool)
                 if not seen.any():
                     continue
                 for g in range(G):

@@ -535,16 +535,17 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
               part[((k >> 1) & 2) + 1] = add_f32x2(part[((k >> 1) & 2) + 1], f32x2(ex2(e1.x), ex2(e1.y)));
             }
           } else {
-            const int node = j - s.old, words = P.tree_words;
-            uint32_t mask = base + masks_at + 4 * (row0 * words + min(max(node, 0) >> 5, words - 1));
-            const uint32_t before = node < 0 ? 0xffffffffu : 0u;
+            const int node = j - s.old, words = P.tree_words, word = max(node, 0) >> 5;
+            uint32_t mask = base + masks_at + 4 * (row0 * words + min(word, words - 1));
+            // All rows see the tokens before the new ones, none the new ones that no word stands for.
+            const uint32_t before = node < 0 ? 0xffffffffu : 0u, named = word < words ? 0xffffffffu : 0u;
 #pragma unroll
             for (int k = 0; k < 64; k += 2, mask += 8 * words) {
               const float2 l = *reinterpret_cast<const float2*>(row + 4 * k);
               const float e0 = fmaf(__uint_as_float(v[k >> 5][k & 31]), c, l.x);
               const float e1 = fmaf(__uint_as_float(v[k >> 5][(k & 31) + 1]), c, l.y);
-              const bool see0 = ((lds32(mask) | before) >> (node & 31)) & 1u;
-              const bool see1 = ((lds32(mask + 4 * words) | before) >> (node & 31)) & 1u;
+              const bool see0 = (((lds32(mask) & named) | before) >> (node & 31)) & 1u;
+              const bool see1 = (((lds32(mask + 4 * words) & named) | before) >> (node & 31)) & 1u;
               part[(k >> 1) & 3] = add_f32x2(part[(k >> 1) & 3], f32x2(see0 ? ex2(e0) : 0.f, see1 ? ex2(e1) : 0.f));
             }
           }
