@@ -116,10 +116,13 @@ tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_batch* batc
                              void* q_out, long long qo_stride, const tm_kvb_rope* rope, int dtype, float* w,
                              long long w_stride, void* stream);
 
-/* Bytes of device workspace that tm_kvb_attention and tm_kvb_attention_tree need for these shapes
- * (only the host fields of cache and batch are read); weights != 0: with w_out. */
+/* Bytes of device workspace that tm_kvb_attention needs for these shapes (only the
+ * host fields of cache and batch are read); weights != 0: with w_out. */
 tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq, int weights,
                                      size_t* bytes);
+/* The same for tm_kvb_attention_tree. */
+tm_status tm_kvb_attention_tree_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq, int weights,
+                                          size_t* bytes);
 
 /*
  * Causal attention of the new tokens over the cache (their own keys and
@@ -162,7 +165,10 @@ tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
  *   tree  : device, 32-bit words [rows][tree_stride], 4-byte aligned,
  *           tree_stride >= ceil(max_q / 32), which is how many words of a row are read: new
  *           tokens past them are not seen, and bits past the new tokens say nothing
- * The rest as in tm_kvb_attention, its workspace too.
+ *   workspace: device, tm_kvb_attention_tree_workspace bytes, 16-byte aligned (may be NULL where that is 0).  With
+ *           fewer the sequences are cut into fewer slices, which is slower; what tm_kvb_attention_workspace
+ *           says for the same step is always enough
+ * The rest as in tm_kvb_attention.
  */
 tm_status tm_kvb_attention_tree(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,
                                 long long q_stride, int Hq, int dtype, float scale, const uint32_t* tree,

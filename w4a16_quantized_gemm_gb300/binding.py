@@ -29,7 +29,7 @@ EXPORTS = ("tm_status_str", "tm_packed_bytes", "tm_pack_weights", "tm_unpack_wei
            "tm_w8a8_quantize_act_f16", "tm_w8a8_gemm_f16", "tm_w4a16_gemm_host_static",
            "tm_w4a16_gemm_grouped", "tm_gemm_plan_grouped", "tm_kvb_append", "tm_kvb_attention",
            "tm_kvb_attention_workspace", "tm_kvb_evict", "tm_kvb_append_rope", "tm_kvb_attention_tree",
-           "tm_kvb_accept", "tm_lora_add")
+           "tm_kvb_attention_tree_workspace", "tm_kvb_accept", "tm_lora_add")
 
 GROUP_MAX = 4  # TM_GROUP_MAX
 
@@ -165,8 +165,9 @@ def load(path: Optional[str] = None):
     pc, pb, ll = ctypes.POINTER(KVBCacheStruct), ctypes.POINTER(KVBBatchStruct), ctypes.c_longlong
     lib.tm_kvb_append.restype = ci
     lib.tm_kvb_append.argtypes = [pc, pb, vp, ll, vp, ll, ci, vp, ll, vp]
-    lib.tm_kvb_attention_workspace.restype = ci
-    lib.tm_kvb_attention_workspace.argtypes = [pc, pb, ci, ci, ctypes.POINTER(csz)]
+    for query in (lib.tm_kvb_attention_workspace, lib.tm_kvb_attention_tree_workspace):
+        query.restype = ci
+        query.argtypes = [pc, pb, ci, ci, ctypes.POINTER(csz)]
     lib.tm_kvb_attention.restype = ci
     lib.tm_kvb_attention.argtypes = [pc, pb, vp, ll, ci, ci, ctypes.c_float, vp, vp, vp, vp, ll, vp, csz, vp]
     lib.tm_kvb_evict.restype = ci
@@ -911,9 +912,17 @@ def kvb_attention_workspace(cache: KVBlocks, batch: KVBatch, Hq: int, rows: int,
     return n.value
 
 
-def _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream):
+def kvb_attention_tree_workspace(cache: KVBlocks, batch: KVBatch, Hq: int, rows: int, weights: bool = False) -> int:
+    """Bytes of workspace for kvb_attention_tree (tm_kvb_attention_tree_workspace)."""
+    n = ctypes.c_size_t()
+    _check(load().tm_kvb_attention_tree_workspace(cache._ref, batch._rows(rows), Hq, 1 if weights else 0, ctypes.byref(n)),
+           "tm_kvb_attention_tree_workspace")
+    return n.value
+
+
+def _kvb_attention_args(size_of, cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream):
     """Arguments that kvb_attention and kvb_attention_tree share, before and after the tree's, out, and the workspace
-    (the caller holds it until its launches are made)."""
+    (of size_of bytes where none is given; the caller holds it until its launches are made)."""
     if scale and ctypes.c_float(scale).value == 0.0:
         raise ValueError("scale rounds to 0 in fp32, which stands for 1 / sqrt(D)")
     qp, qs, dtype, shape = _kvb_rows(Q, None, cache.D, "Q")
@@ -932,7 +941,7 @@ def _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace
     if wi is not None and (wo is None or ni != no):
         raise ValueError("w_in comes with a w_out of its shape")
     if workspace is None:
-        size = kvb_attention_workspace(cache, batch, Hq, rows, wo is not None)
+        size = size_of(cache, batch, Hq, rows, wo is not None)
         if size:
             workspace = _empty(size, torch.uint8, Q.device, stream)
     sp, size = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
@@ -954,7 +963,8 @@ def kvb_attention(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, out: Optiona
     w_out: fp32 [B][Hkv][tokens], receives w_in (None: 0) plus the weight that each
            token drew in this call; may be w_in
     workspace: a uint8 tensor of kvb_attention_workspace bytes; None: allocated"""
-    head, tail, out, held = _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream)
+    head, tail, out, held = _kvb_attention_args(kvb_attention_workspace, cache, batch, Q, out, lse, w_in, w_out, scale,
+                                                workspace, stream)
     st = (_lib or load()).tm_kvb_attention(*head, *tail)
     if st:
         raise TMError(st, "tm_kvb_attention")
@@ -972,11 +982,15 @@ def kvb_attention_tree(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, tree: t
     tree: int32 [rows][>= ceil(max_q / 32)], rows may be strided: bit k % 32 of word k / 32 stands for the
           sequence's new token k (``tree_masks`` builds them from parents)
 
-    The rest as in kvb_attention, the workspace too."""
+    workspace: a uint8 tensor of kvb_attention_tree_workspace bytes (fewer make it slower; kvb_attention_workspace's
+          are always enough); None: allocated
+
+    The rest as in kvb_attention."""
     if (tree.dim() != 2 or tree.shape[0] != Q.shape[0] or tree.dtype is not torch.int32 or not tree.is_cuda
             or 32 * tree.shape[1] < batch.max_q or (tree.stride(1) != 1 and tree.shape[1] > 1)):
         raise ValueError("tree must be CUDA int32 [rows][ceil(max_q / 32)], its words contiguous")
-    head, tail, out, held = _kvb_attention_args(cache, batch, Q, out, lse, w_in, w_out, scale, workspace, stream)
+    head, tail, out, held = _kvb_attention_args(kvb_attention_tree_workspace, cache, batch, Q, out, lse, w_in, w_out, scale,
+                                                workspace, stream)
     stride = tree.stride(0) if tree.shape[0] > 1 else tree.shape[1]
     st = (_lib or load()).tm_kvb_attention_tree(*head, tree.data_ptr(), stride, *tail)
     if st:

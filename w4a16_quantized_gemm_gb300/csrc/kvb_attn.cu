@@ -764,7 +764,42 @@ struct Plan {
   size_t part, part_ml, lse, score, bytes;  // offsets, total
 };
 
-static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
+// Slices of about `chunk` tokens, and where each part of the workspace lies.
+static void lay_out(const View& V, int D, int Hq, bool weights, long long chunk, Plan* p) {
+  const long long unit = p->rt >= 0 ? kTile : 128, least = p->rt >= 0 ? 2 * kTile : 512;
+  chunk = (chunk + unit - 1) / unit * unit;
+  if (chunk < least) chunk = least;
+  long long chunks = (V.max_len + chunk - 1) / chunk;
+  if (chunks < 1) chunks = 1;
+  p->chunk = (int)(chunk > 0x7fffff80ll ? 0x7fffff80ll : chunk);
+  p->chunks = (int)chunks;
+  auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
+  const size_t hr = (size_t)V.rows * Hq;
+  size_t at = 0;
+  p->scores = weights && p->rt >= 0;
+  if (chunks > 1) {
+    p->part = at;
+    at = al(at + hr * chunks * D * 4);
+  }
+  if (chunks > 1 || p->scores) {
+    p->part_ml = at;
+    at = al(at + hr * chunks * 8);
+  }
+  if (weights) {
+    if (p->scores) {
+      p->score = at;
+      at = al(at + hr * (((size_t)V.max_len + kTile - 1) / kTile * kTile) * 4);
+    } else {
+      p->lse = at;
+      at = al(at + hr * 4);
+    }
+  }
+  p->bytes = at;
+}
+
+// A tree's plan keeps to a workspace of `room` bytes: fewer slices where their best number does not fit (a causal call's
+// workspace holds one at least).
+static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree, size_t room = SIZE_MAX) {
   Plan p = {};
   const int G = Hq / V.Hkv;
   const long long rows = (long long)V.max_q * G;
@@ -781,54 +816,23 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree) {
   p.rows_per_cta = p.rt == 0 ? 8 : p.rt > 0 ? 16 * p.rt : narrow ? 128 : 256;
   p.groups = (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta);
   const long long ctas = (long long)V.B * V.Hkv * p.groups;
-  long long chunk, least, unit;
+  long long chunk;
   if (p.rt >= 0) {
     // Slices for two waves of CTAs, none shorter than two steps per warp (2 x 131072 tokens: two waves
     // 94 us, four 98, eight 101 at the time: starting a CTA costs about 3 us).
     const long long slots = sms * (p.rt < 2 ? 3 : 2);
-    unit = kTile;
-    least = 2 * kTile;
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
   } else if (tree) {
     // Starting a CTA costs about six tiles, the joining launch four.
-    unit = 128;
-    least = 512;
     const long long slices = slices_by_waves(ctas, (V.max_len + 127) / 128, 6, 4);
     chunk = (V.max_len + slices - 1) / slices;
   } else {
     // Slices only where the rows alone leave SMs idle (300 tokens over 30000: 182 us; unsliced 574).
-    unit = 128;
-    least = 512;
     chunk = ctas >= sms ? V.max_len : ((long long)V.max_len * ctas + 2 * sms - 1) / (2 * sms);
   }
-  chunk = (chunk + unit - 1) / unit * unit;
-  if (chunk < least) chunk = least;
-  long long chunks = (V.max_len + chunk - 1) / chunk;
-  if (chunks < 1) chunks = 1;
-  p.chunk = (int)(chunk > 0x7fffff80ll ? 0x7fffff80ll : chunk);
-  p.chunks = (int)chunks;
-  auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
-  const size_t hr = (size_t)V.rows * Hq;
-  size_t at = 0;
-  p.scores = weights && p.rt >= 0;
-  if (chunks > 1) {
-    p.part = at;
-    at = al(at + hr * chunks * D * 4);
-  }
-  if (chunks > 1 || p.scores) {
-    p.part_ml = at;
-    at = al(at + hr * chunks * 8);
-  }
-  if (weights) {
-    if (p.scores) {
-      p.score = at;
-      at = al(at + hr * (((size_t)V.max_len + kTile - 1) / kTile * kTile) * 4);
-    } else {
-      p.lse = at;
-      at = al(at + hr * 4);
-    }
-  }
-  p.bytes = at;
+  lay_out(V, D, Hq, weights, chunk, &p);
+  while (tree && p.bytes > room && p.chunks > 1)
+    lay_out(V, D, Hq, weights, ((long long)V.max_len + p.chunks - 2) / (p.chunks - 1), &p);
   return p;
 }
 
@@ -864,8 +868,8 @@ static tm_status check_heads(const View& V, const tm_kvb_batch* batch, int Hq) {
   return TM_OK;
 }
 
-extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq,
-                                                int weights, size_t* bytes) {
+static tm_status workspace_bytes(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq, int weights, bool tree,
+                                 size_t* bytes) {
   View V;
   if (!bytes) return TM_ERR_INVALID_ARG;
   tm_status st = check(cache, batch, false, &V);
@@ -873,10 +877,20 @@ extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const
   if (st != TM_OK) return st;
   *bytes = 0;
   if (V.B == 0 || V.rows == 0 || V.max_q == 0) return TM_OK;
-  const Plan p = make_plan(V, cache->D, Hq, weights != 0, false), t = make_plan(V, cache->D, Hq, weights != 0, true);
+  const Plan p = make_plan(V, cache->D, Hq, weights != 0, tree);
   if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
-  *bytes = p.bytes > t.bytes ? p.bytes : t.bytes;
+  *bytes = p.bytes;
   return TM_OK;
+}
+
+extern "C" tm_status tm_kvb_attention_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq,
+                                                int weights, size_t* bytes) {
+  return workspace_bytes(cache, batch, Hq, weights, false, bytes);
+}
+
+extern "C" tm_status tm_kvb_attention_tree_workspace(const tm_kvb_cache* cache, const tm_kvb_batch* batch, int Hq,
+                                                     int weights, size_t* bytes) {
+  return workspace_bytes(cache, batch, Hq, weights, true, bytes);
 }
 
 template <int FMT, int D, bool TREE>
@@ -956,7 +970,7 @@ static tm_status attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
     if (!tree || tree_stride < P.tree_words) return TM_ERR_INVALID_ARG;
     if (!aligned(tree, 4)) return TM_ERR_ALIGNMENT;
   }
-  const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr, TREE);
+  const Plan p = make_plan(V, cache->D, Hq, w_out != nullptr, TREE, workspace ? workspace_bytes : 0);
   if (!plan_fits(V, p)) return TM_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return TM_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
