@@ -303,7 +303,9 @@ def _own_tree(state):
     binding, cache, batch = _own_handles(state)
     Hq, weights = state["case"]["Hq"], state["case"]["weights"]
     if "workspace" not in state:
-        size = binding.kvb_attention_workspace(cache, batch, Hq, state["qkv"].shape[0], weights)
+        # the call's own query (a library without one has a query for both calls)
+        query = getattr(binding, "kvb_attention_tree_workspace", binding.kvb_attention_workspace)
+        size = query(cache, batch, Hq, state["qkv"].shape[0], weights)
         state["workspace"] = torch.empty(size, dtype=torch.uint8, device="cuda")
     more = {"w_in": state["w"], "w_out": state["w_out"]} if weights else {}
     binding.kvb_attention_tree(cache, batch, state["qkv"][:, :Hq], state["mask"], out=state["out"], lse=state["lse"],
