@@ -374,25 +374,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const AttnParam
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-          if (!ok) continue;
-          if (P.chunks == 1) {
-            uint16_t* out = P.out + hr * D + c;
+          if (ok) {
+            if (P.chunks == 1) {
+              uint16_t* out = P.out + hr * D + c;
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t wd[4];
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t wd[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float f0 = __uint_as_float(o[k + 2 * e]) * inv, f1 = __uint_as_float(o[k + 2 * e + 1]) * inv;
-                wd[e] = P.bf16 ? pack_bf162(f0, f1) : pack_half2(f0, f1);
+                for (int e = 0; e < 4; ++e) {
+                  const float f0 = __uint_as_float(o[k + 2 * e]) * inv, f1 = __uint_as_float(o[k + 2 * e + 1]) * inv;
+                  wd[e] = P.bf16 ? pack_bf162(f0, f1) : pack_half2(f0, f1);
+                }
+                *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
               }
-              *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-            }
-          } else {
-            float* dst = P.part + (hr * P.chunks + chunk) * D + c;
+            } else {
+              float* dst = P.part + (hr * P.chunks + chunk) * D + c;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
           }
+          __syncwarp();  // whole again for the next load
         }
         if (ok) {
           if (P.chunks > 1)

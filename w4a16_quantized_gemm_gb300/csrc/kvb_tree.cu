@@ -323,28 +323,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnParams 
       for (int c = 0; c < COLS; c += 32) {
         uint32_t o[32];
         output(i * COLS + c, o);
-        if (!ok) continue;
+        if (ok) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          o[k] = __float_as_uint(__uint_as_float(o[k]) * mine + given(i)[(c + k) * kTreeTile] * others);
-        if (P.chunks == 1) {
-          uint16_t* out = P.out + hr * D + i * COLS + c;
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) * mine + given(i)[(c + k) * kTreeTile] * others);
+          if (P.chunks == 1) {
+            uint16_t* out = P.out + hr * D + i * COLS + c;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t wd[4];
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t wd[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = __uint_as_float(o[k + 2 * e]) * inv, a2 = __uint_as_float(o[k + 2 * e + 1]) * inv;
-              wd[e] = P.bf16 ? pack_bf162(a, a2) : pack_half2(a, a2);
+              for (int e = 0; e < 4; ++e) {
+                const float a = __uint_as_float(o[k + 2 * e]) * inv, a2 = __uint_as_float(o[k + 2 * e + 1]) * inv;
+                wd[e] = P.bf16 ? pack_bf162(a, a2) : pack_half2(a, a2);
+              }
+              *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
             }
-            *reinterpret_cast<uint4*>(out + k) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-          }
-        } else {
-          float* dst = P.part + (hr * P.chunks + chunk) * D + i * COLS + c;
+          } else {
+            float* dst = P.part + (hr * P.chunks + chunk) * D + i * COLS + c;
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(dst + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
         }
+        __syncwarp();  // whole again for the next load
       }
       if (ok && i == 0) {
         if (P.chunks > 1)

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) weights_kernel(const AttnParams
             const float2 f = unpack(o[k], false);
             o[k] = pack_bf162(f.x, f.y);
           }
+        __syncwarp();  // lanes without a token took another way
         tc_st_32x32b_x32(tmem + lanes + 64 * half + c / 2, o);
       }
       tc_wait_st();
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) tree_weights_kernel(const AttnP
             const float2 f = unpack(o[k], false);
             o[k] = pack_bf162(f.x, f.y);
           }
+        __syncwarp();  // lanes without a token took another way
         tc_st_32x32b_x32(tmem + lanes + 128 * i + 64 * odd + 32 * c, o);
       }
       tc_wait_st();

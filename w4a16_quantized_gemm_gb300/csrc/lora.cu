@@ -167,6 +167,7 @@ __device__ __forceinline__ void exchange(const Params& P, int a, int rank, uint3
       for (int q = 0; q < kCluster; ++q) st_dsmem_u16(map_shared_rank(at, q), bits);
     }
     if (lane < kCluster) st_dsmem_f32(map_shared_rank(mul + r * 4, lane), down);
+    __syncwarp();
   }
   cluster_sync_all();
 }
