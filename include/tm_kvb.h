@@ -185,7 +185,7 @@ tm_status tm_kvb_attention_tree(const tm_kvb_cache* cache, const tm_kvb_batch* b
  * to what these need, and becomes that where the page keeps no token (of before, or of the path).
  * Slots from old + count on keep what they hold.  A hole's tokens move as zeros,
  * and what falls into a hole is dropped.
- *   path   : device int32 [B][path_stride]
+ *   path   : device int32 [B][path_stride] (not read, and may be NULL, where path_stride is 0)
  *   count  : device int32 [B] (clamped to 0 .. path_stride)
  *   w      : NULL, or the token weights fp32 [B][Hkv][w_stride]: they move along, those of the
  *            new tokens that are not kept become 0

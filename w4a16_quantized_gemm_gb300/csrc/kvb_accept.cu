@@ -190,7 +190,7 @@ extern "C" tm_status tm_kvb_accept(const tm_kvb_cache* cache, const tm_kvb_batch
   if (!batch->q_start && batch->rows != batch->B) return TM_ERR_INVALID_ARG;
   if (path_stride < 0 || w_stride < 0) return TM_ERR_INVALID_ARG;
   if (V.B == 0) return TM_OK;
-  if (!path || !count || !new_len || new_len == batch->kv_len) return TM_ERR_INVALID_ARG;
+  if ((!path && path_stride > 0) || !count || !new_len || new_len == batch->kv_len) return TM_ERR_INVALID_ARG;
   if (!aligned(path, 4) || !aligned(count, 4) || !aligned(new_len, 4) || !aligned(w, 4)) return TM_ERR_ALIGNMENT;
   P.path = path;
   P.count = count;
