@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
   const int most = min(min(max(P.count[b], 0), P.path_stride), n);
   if (tid == 0) cut_s = most;
   __syncthreads();
-  for (int i = tid; i < most; i += kAcceptThreads) {
+  for (unsigned i = tid; i < (unsigned)most; i += kAcceptThreads) {  // counts reach 2^31 - 1
     const int at = path[i];
-    if (at < 0 || at >= n || (i > 0 && path[i - 1] >= at)) atomicMin(&cut_s, i);
+    if (at < 0 || at >= n || (i > 0 && path[i - 1] >= at)) atomicMin(&cut_s, (int)i);
   }
   __syncthreads();
   const int count = cut_s;
@@ -72,12 +72,13 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
     if (blockIdx.x == 0 && tid == 0) P.new_len[b] = old + count;
     if (P.w) {  // the weights move along, the rest of the new ones are cleared
       float* w = P.w + ((size_t)b * V.Hkv + h) * P.w_stride;
-      for (int i0 = 0; i0 < n; i0 += kAcceptThreads) {
-        const int i = i0 + tid;
+      const long long room = min((long long)n, P.w_stride - old);  // new tokens that have a weight
+      for (long long i0 = 0; i0 < room; i0 += kAcceptThreads) {
+        const long long i = i0 + tid;
         const long long src = i < count ? (long long)old + path[i] : P.w_stride;
         const float x = src < P.w_stride ? w[src] : 0.f;
         __syncthreads();
-        if (i < n && (long long)old + i < P.w_stride) w[old + i] = x;
+        if (i < room) w[old + i] = x;
       }
     }
   }
