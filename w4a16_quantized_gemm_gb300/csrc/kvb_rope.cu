@@ -88,10 +88,11 @@ __global__ void __launch_bounds__(THREADS, (UNITS == 4 ? 2 : 3) * 256 / THREADS)
   const Span s = span(V, b);
   const int T = 1 << V.t_shift;
   // Pages by slot; queries of rows without one (more rows than tokens: negative slots) are rotated all the same.
+  const int end = s.old + s.n, pages = ((end - 1) >> V.t_shift) - (s.old >> V.t_shift);
+  if (s.n == 0 || nth > pages) return;
   const int blk = (s.old >> V.t_shift) + nth;
   const int begin = blk * T;
-  const int lo = max(s.old, begin), hi = min(s.old + s.n, begin + T);
-  if (lo >= hi) return;
+  const int lo = max(s.old, begin), hi = nth == pages ? end : begin + T;  // lengths reach 2^31 - 1
   const int D = 1 << P.d_shift, unit_shift = P.d_shift - 4;
   const int total = (hi - lo) << unit_shift;
   const int turning = R.dims >> 4;  // units of a token that rotate
