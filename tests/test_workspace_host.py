@@ -52,3 +52,15 @@ def test_a_causal_workspace_holds_one_slice_of_a_tree(lib, Hkv, G, D, weights):
                     assert one <= query(lib, False, Hkv * G, Hkv, D, B, max_q, room, weights)
                 else:
                     assert one == query(lib, False, Hkv * G, Hkv, D, B, max_q, room, weights)
+
+
+def test_slices_of_large_trees_fit_their_grid(lib):
+    """A tree's CTAs stand side by side along one axis of the grid, groups of 256 rows times slices: at most 65535."""
+    G, D, room = 8, 64, 1 << 24
+    most = 0
+    for groups in list(range(200, 15600, 97)) + [1023, 1024, 4095, 4096, 7000, 13107, 15625]:
+        max_q = groups * 256 // G
+        n = query(lib, True, G, 1, D, 1, max_q, room, rows=1)  # one row: the partial results of a slice are G (D + 2) numbers
+        slices = max(n // (G * (D + 2) * 4), 1)
+        most = max(most, groups * slices)
+    assert most <= 65535

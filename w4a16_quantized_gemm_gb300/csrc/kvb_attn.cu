@@ -823,8 +823,9 @@ static Plan make_plan(const View& V, int D, int Hq, bool weights, bool tree, siz
     const long long slots = sms * (p.rt < 2 ? 3 : 2);
     chunk = ((long long)V.max_len * ctas + 2 * slots - 1) / (2 * slots);
   } else if (tree) {
-    // Starting a CTA costs about six tiles, the joining launch four.
-    const long long slices = slices_by_waves(ctas, (V.max_len + 127) / 128, 6, 4);
+    // Starting a CTA costs about six tiles, the joining launch four.  Groups and slices share an axis of the grid.
+    const long long most = 65535 / p.groups < 64 ? 65535 / p.groups : 64;
+    const long long slices = slices_by_waves(ctas, (V.max_len + 127) / 128, 6, 4, most);
     chunk = (V.max_len + slices - 1) / slices;
   } else {
     // Slices only where the rows alone leave SMs idle (300 tokens over 30000: 182 us; unsliced 574).

@@ -45,11 +45,11 @@ tm_status launch_tree_attn(const AttnParams& P, int format, int D, cudaStream_t 
 tm_status launch_row_weights(const AttnParams& P, int format, int D, cudaStream_t stream);
 
 // Slices of `tiles` token tiles, each in a CTA of its own, for which waves of CTAs x (tiles of a slice + what starting
-// one costs) is the least; `join` for joining several.  None shorter than four tiles, at most 64.
-inline long long slices_by_waves(long long ctas, long long tiles, int start, int join) {
+// one costs) is the least; `join` for joining several.  None shorter than four tiles, at most `most`.
+inline long long slices_by_waves(long long ctas, long long tiles, int start, int join, long long most) {
   const long long sms = num_sms(current_device());
   long long best = 1, cost = -1;
-  for (long long c = 1; c == 1 || (c <= 64 && tiles / c >= 4); ++c) {
+  for (long long c = 1; c == 1 || (c <= most && tiles / c >= 4); ++c) {
     const long long t = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + start) + (c > 1 ? join : 0);
     if (cost < 0 || t < cost) {
       best = c;

@@ -608,7 +608,7 @@ static tm_status launch_tree(const AttnParams& P, cudaStream_t stream) {
     return TM_ERR_CUDA;
   // A start costs about as much as ten tiles.
   const long long ctas = (long long)P.V.B * P.V.Hkv, tiles = ((long long)P.V.max_len + kWtTile - 1) / kWtTile;
-  const long long slices = slices_by_waves(ctas, tiles, 10, 0);
+  const long long slices = slices_by_waves(ctas, tiles, 10, 0, 64);
   const long long slice = ((tiles + slices - 1) / slices > 4 ? (tiles + slices - 1) / slices : 4) * kWtTile;
   const dim3 grid((unsigned)ctas, (unsigned)((P.w_stride + slice - 1) / slice));
   const uint32_t smem = SH::smem((P.V.max_q * P.G + kWtTile - 1) / kWtTile, P.tree_words);
