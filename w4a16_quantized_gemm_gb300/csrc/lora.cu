@@ -139,15 +139,15 @@ __device__ __forceinline__ void exchange(const Params& P, int a, int rank, uint3
     for (int k = 0; k < PER; ++k) {
       const int c = lane + 32 * k;
       v[k] = 0.f;
-      if (c < RP) {
+      if (c < P.R) {  // ranks that fill RP up stay 0: their sums of products with 0 are NaN where X is infinite
         const uint32_t at = sum + (r * RP + c) * 4;
         float x[kCluster];
 #pragma unroll
         for (int q = 0; q < kCluster; ++q) x[q] = ld_dsmem_f32(map_shared_rank(at, q));
 #pragma unroll
         for (int q = 0; q < kCluster; ++q) v[k] += x[q];
+        v[k] *= factor;
       }
-      v[k] *= factor;
       big = fmaxf(big, fabsf(v[k]));
     }
 #pragma unroll
@@ -159,7 +159,7 @@ __device__ __forceinline__ void exchange(const Params& P, int a, int rank, uint3
     for (int k = 0; k < PER; ++k) {
       const int c = lane + 32 * k;
       if (c >= 16 * KS) continue;
-      const uint16_t bits = c < RP ? __half_as_ushort(__float2half_rn(v[k] * up)) : (uint16_t)0;
+      const uint16_t bits = __half_as_ushort(__float2half_rn(v[k] * up));
       int x, word;
       word_of(c & 15, x, word);
       const uint32_t at = frag + (((r >> 4) * KS + (c >> 4)) * 32 + (r & 7) * 4 + x) * 16 + (word + ((r >> 3) & 1)) * 4 + (c & 1) * 2;
