@@ -26,7 +26,7 @@ typedef struct {
   const void* B;      /* device fp16 [n][N][R], contiguous, 16-byte aligned */
   const float* scale; /* device fp32 [n]; NULL: 1 */
   int n;              /* adapters, >= 0 */
-  int K, N;           /* of the projection, multiples of 8 */
+  int K, N;           /* of the projection, multiples of 8, at most 2^30 */
   int R;              /* a multiple of 8, 8 .. 128 */
 } tm_lora_adapters;
 

@@ -57,9 +57,9 @@ struct Shape {
   static constexpr uint32_t SMEM = MUL + 16 * 4;
 };
 
-// Into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+// Into L2, which holds less than 2^30 bytes.
+__device__ __forceinline__ void prefetch_l2(const void* p, long long bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)min(bytes, 1ll << 30)) : "memory");
 }
 __device__ __forceinline__ uint4 ldg16(const __half* p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
@@ -288,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) add_kernel(const Pa
     // Its columns of B, one run of memory, on their way to L2 while T is computed; and the next item's A, a share
     // of it by each CTA.
     if (tid == 0 && n1 > n0)
-      prefetch_l2(P.B + ((size_t)a * P.N + 32 * n0) * P.R, (uint32_t)(min(32 * n1, P.N) - 32 * n0) * P.R * 2);
+      prefetch_l2(P.B + ((size_t)a * P.N + 32 * n0) * P.R, (min(32 * n1, P.N) - 32 * n0) * (2ll * P.R));
     if (tid == 32 && z + (int)gridDim.y < count) {
       const long long units = (long long)P.R * P.K / 8, u0 = units * rank / kCluster, u1 = units * (rank + 1) / kCluster;
       if (u1 > u0)
-        prefetch_l2(P.A + (size_t)items.adapter[z + gridDim.y] * P.R * P.K + 8 * u0, (uint32_t)(u1 - u0) * 16);
+        prefetch_l2(P.A + (size_t)items.adapter[z + gridDim.y] * P.R * P.K + 8 * u0, (u1 - u0) * 16);
     }
     // ---- T: this warp's chunks of 32 k
     {
@@ -727,7 +727,8 @@ extern "C" tm_status tm_lora_add(const tm_lora_adapters* ad, const void* X, long
   if (!ad || ad->n < 0 || ad->K < 8 || ad->K % 8 || ad->N < 8 || ad->N % 8 || ad->R < 8 || ad->R > 128 || ad->R % 8)
     return TM_ERR_INVALID_ARG;
   if (rows < 0 || B < 0 || (!q_start && rows != B)) return TM_ERR_INVALID_ARG;
-  if (rows > 0x7fffff00ll) return TM_ERR_UNSUPPORTED;  // row indices are 32-bit in the kernel
+  // Row and column indices are 32-bit in the kernels, and run ahead of the last one.
+  if (rows > 0x7fffff00ll || ad->K > 1 << 30 || ad->N > 1 << 30) return TM_ERR_UNSUPPORTED;
   if (rows == 0 || B == 0) return TM_OK;
   if (!X || !Y || !out || !ids || (ad->n > 0 && (!ad->A || !ad->B))) return TM_ERR_INVALID_ARG;
   if (x_stride < ad->K || y_stride < ad->N || out_stride < ad->N) return TM_ERR_INVALID_ARG;
