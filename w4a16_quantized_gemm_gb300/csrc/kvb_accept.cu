@@ -72,10 +72,10 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
     if (blockIdx.x == 0 && tid == 0) P.new_len[b] = old + count;
     if (P.w) {  // the weights move along, the rest of the new ones are cleared
       float* w = P.w + ((size_t)b * V.Hkv + h) * P.w_stride;
-      const long long room = min((long long)n, P.w_stride - old);  // new tokens that have a weight
-      for (long long i0 = 0; i0 < room; i0 += kAcceptThreads) {
-        const long long i = i0 + tid;
-        const long long src = i < count ? (long long)old + path[i] : P.w_stride;
+      const unsigned room = (unsigned)max(min((long long)n, P.w_stride - old), 0ll);  // new tokens that have a weight
+      for (unsigned i0 = 0; i0 < room; i0 += kAcceptThreads) {
+        const unsigned i = i0 + tid;
+        const long long src = i < (unsigned)count ? (long long)old + path[i] : P.w_stride;
         const float x = src < P.w_stride ? w[src] : 0.f;
         __syncthreads();
         if (i < room) w[old + i] = x;
