@@ -107,8 +107,8 @@ typedef struct {
  * are rounded once to their type (no value is replaced).
  *   Q, q_out : device, dtype [rows][Hq][D], token strides q_stride, qo_stride in elements
  *           (multiples of 8, >= Hq * D), 16-byte aligned; Hkv divides Hq.  q_out may be Q
- *           (with its stride), else it overlaps no input.  Rows of no sequence, and past max_q of one, are left
- *           as they are.  NULL, NULL: keys and values alone (Hq and the strides are then not read)
+ *           (with its stride, and each row in one sequence at most), else it overlaps no input.  Rows of no
+ *           sequence, and past max_q of one, are left as they are.  NULL, NULL: keys and values alone (Hq and the strides are then not read)
  * The rest as in tm_kvb_append.  One launch.
  */
 tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Kn, long long k_stride,
@@ -166,8 +166,8 @@ tm_status tm_kvb_attention(const tm_kvb_cache* cache, const tm_kvb_batch* batch,
  *           tree_stride >= ceil(max_q / 32), which is how many words of a row are read: new
  *           tokens past them are not seen, and bits past the new tokens say nothing
  *   workspace: device, tm_kvb_attention_tree_workspace bytes, 16-byte aligned (may be NULL where that is 0).  With
- *           fewer the sequences are cut into fewer slices, which is slower; what tm_kvb_attention_workspace
- *           says for the same step is always enough
+ *           fewer the sequences are cut into fewer slices, which can be slower and sums in another order; what
+ *           tm_kvb_attention_workspace says for the same step is always enough
  * The rest as in tm_kvb_attention.
  */
 tm_status tm_kvb_attention_tree(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Q,

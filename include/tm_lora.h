@@ -44,6 +44,7 @@ typedef struct {
  * The products accumulate in fp32.  X . A^T is rounded once to fp16 relative to
  * its row's largest element (11 bits; elements below 2^-29 of it lose bits), the
  * result once to fp16 from the fp32 sum.  The same inputs give the same bits.
+ * K or N past 2^30, 2^31 - 256 rows and more: TM_ERR_UNSUPPORTED.
  * One launch, no workspace.  B, rows == 0 is a no-op.
  */
 tm_status tm_lora_add(const tm_lora_adapters* adapters, const void* X, long long x_stride, const void* Y,

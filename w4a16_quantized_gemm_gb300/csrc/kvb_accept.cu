@@ -6,8 +6,9 @@
 // append's rule, x = c s_src being the new value:
 //   s = max(s_old, max |x| r) where the page keeps a token, else max |x| r;  codes Q(x / s), kept ones Q((c s_old) / s)
 // Latency-bound: a few dependent loads (lengths, path, pages, scales and codes), a few KB a CTA.  Measured: 32
-// sequences, paths of up to 6, 8 KV heads: 3.9 us; 64 sequences, paths of up to 40 through pages of 16: 8.4 us (1024
-// CTAs).
+// sequences, paths of up to 6, 8 KV heads: 3.7 us; 64 sequences, paths of up to 40 through pages of 16: 8.3 us (1024
+// CTAs, four on an SM: 1.7 waves, in which each of a thread's four vectors runs through its loads and the page's
+// shared maximum before the next one starts).
 #include "kvb_common.cuh"
 
 namespace w4 {

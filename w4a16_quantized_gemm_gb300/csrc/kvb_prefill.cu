@@ -27,7 +27,7 @@
 // the bottleneck), packed pairs and weights in halves 239, six converting warps 227, registers 192 / 64 / 64
 // 214 (184 / 80 / 64: 227; 200 / 64 / 48: 225).  Fresh prompts of 1499 tokens: 113 us, where starting a CTA for
 // each 256 rows costs as much as its six token tiles.  Trees of 63 nodes over up to 65536 tokens, e4m3, 8 heads a KV
-// head: 233 us, 0.83 PFLOP/s (two waves of CTAs; 258 us before the masks went by bits and four tiles' scales were
+// head: 234 us, 0.83 PFLOP/s (two waves of CTAs; 258 us before the masks went by bits and four tiles' scales were
 // looked up at a time, 243 before rows of no node left the masks alone).
 #include <type_traits>
 
