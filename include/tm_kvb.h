@@ -108,7 +108,8 @@ typedef struct {
  *   Q, q_out : device, dtype [rows][Hq][D], token strides q_stride, qo_stride in elements
  *           (multiples of 8, >= Hq * D), 16-byte aligned; Hkv divides Hq.  q_out may be Q
  *           (with its stride, and each row in one sequence at most), else it overlaps no input.  Rows of no
- *           sequence, and past max_q of one, are left as they are.  NULL, NULL: keys and values alone (Hq and the strides are then not read)
+ *           sequence, and past max_q of one, are left as they are.  NULL, NULL: keys and values alone (Hq and the
+ *           strides are then not read)
  * The rest as in tm_kvb_append.  One launch.
  */
 tm_status tm_kvb_append_rope(const tm_kvb_cache* cache, const tm_kvb_batch* batch, const void* Kn, long long k_stride,

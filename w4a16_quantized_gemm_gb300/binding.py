@@ -982,8 +982,8 @@ def kvb_attention_tree(cache: KVBlocks, batch: KVBatch, Q: torch.Tensor, tree: t
     tree: int32 [rows][>= ceil(max_q / 32)], rows may be strided: bit k % 32 of word k / 32 stands for the
           sequence's new token k (``tree_masks`` builds them from parents)
 
-    workspace: a uint8 tensor of kvb_attention_tree_workspace bytes (fewer make it slower; kvb_attention_workspace's
-          are always enough); None: allocated
+    workspace: a uint8 tensor of kvb_attention_tree_workspace bytes (with fewer it takes fewer slices;
+          kvb_attention_workspace's are always enough); None: allocated
 
     The rest as in kvb_attention."""
     if (tree.dim() != 2 or tree.shape[0] != Q.shape[0] or tree.dtype is not torch.int32 or not tree.is_cuda
